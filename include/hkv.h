@@ -288,6 +288,116 @@ HKV_API hkv_status hkv_ste_select_batch(const float* score, const int32_t* pos, 
                                 int32_t k_near, int32_t k_far, int32_t stratified,
                                 uint8_t* evict, void* stream);
 
+/* ---- Shared-prefix cache ---------------------------------------------------- */
+
+/* A batch whose sequences share prompts: the keys and values of each prompt
+ * are held once, every sequence adds the tokens of its own, and each own
+ * token carries the attention weight it has received so far, by which tokens
+ * are evicted.  (Many images of one prompt, and all unconditional streams
+ * under classifier-free guidance [Problem statement: the KV cache of
+ * autoregressive decoding]; scores from past queries [step 3].)  The calls
+ * keep no state of their own: this struct describes caller-owned device
+ * buffers, and host code may change or drop it after a call returns.
+ *
+ * H query heads attend over Hkv = num_kv_heads key heads: query head h reads
+ * key head h / (H / Hkv).  Strides are in elements, of (sequence, KV head,
+ * slot) and, for prefixes, (prefix, KV head, slot); the d elements of a row
+ * are contiguous.  k, v and prefix rows start on 16-byte boundaries (bases
+ * and strides).  Rows of two slots may not overlap.
+ * Integers read on the device are taken in range: a len outside
+ * [0, capacity] or a prefix_len outside [0, prefix_capacity] as the nearer
+ * bound, a prefix_of outside [0, num_prefixes) as no prefix. */
+typedef struct {
+    int32_t dtype;           /* hkv_dtype of q, k, v, outputs and the cache */
+    int32_t head_dim;        /* 64 or 128 */
+    int32_t num_seqs;        /* S */
+    int32_t num_heads;       /* H, a multiple of num_kv_heads */
+    int32_t num_kv_heads;    /* Hkv */
+    int32_t capacity;        /* own slots of each (sequence, KV head) */
+    int32_t num_prefixes;    /* G shared prefixes, 0..1024 */
+    int32_t prefix_capacity; /* slots of each (prefix, KV head) */
+    void* k;                 /* own rows, [S][Hkv][capacity][d] by strides */
+    void* v;
+    int64_t k_stride[3];
+    int64_t v_stride[3];
+    int32_t* pos;            /* [S][Hkv][capacity] positions of the own tokens */
+    float* weight;           /* [S][Hkv][capacity] accumulated weights */
+    int32_t* len;            /* [S][Hkv] own tokens held */
+    int32_t* next_pos;       /* [S][Hkv] position of the next appended token */
+    const void* prefix_k;    /* [G][Hkv][prefix_capacity][d] by strides */
+    const void* prefix_v;
+    int64_t prefix_k_stride[3];
+    int64_t prefix_v_stride[3];
+    const int32_t* prefix_len; /* [G] */
+    const int32_t* prefix_of;  /* [S] prefix each sequence continues */
+    int32_t* status;         /* [2] first error latched on the device, detail */
+} hkv_shared_cache;
+
+/* Appends num_tokens tokens to every (sequence, KV head): rows len .. len +
+ * num_tokens - 1 of k and v, their positions next_pos + 0, 1, ..., their
+ * accumulated weights from weight_t ([S][Hkv][num_tokens] contiguous; NULL:
+ * zeros); then len and next_pos grow by num_tokens.
+ *  k_t, v_t: [S][Hkv][num_tokens][d] by strides (sequence, KV head, token),
+ *            16-byte aligned rows, not overlapping the cache.
+ * A head with fewer than num_tokens free slots is left as it was and latches
+ * HKV_ERR_CAPACITY (detail: sequence * Hkv + head).
+ * Errors: INVALID_ARG, CUDA. */
+HKV_API hkv_status hkv_shared_append(const hkv_shared_cache* cache, const void* k_t,
+                                     const int64_t* k_stride, const void* v_t,
+                                     const int64_t* v_stride, const float* weight_t,
+                                     int32_t num_tokens, void* stream);
+
+/* Bytes of scratch one hkv_shared_attend of these sizes needs (0 may be
+ * returned).  Depends on the sizes and pointers' presence in *cache, on
+ * num_queries and accumulate only.  Errors: INVALID_ARG. */
+HKV_API hkv_status hkv_shared_attend_bytes(const hkv_shared_cache* cache, int32_t num_queries,
+                                           int32_t accumulate, size_t* bytes);
+
+/* Attention of each sequence's newest num_queries = T tokens (already
+ * appended) over its prefix and its own tokens, in one softmax.  Query t
+ * sees the whole prefix and the own slots before len - T + t + 1 (all the
+ * earlier ones whatever an eviction did to their order, and the new ones up
+ * to itself).  A query that sees nothing gets zeros and lse = -inf.
+ *  q, out: [S][H][T][d] by strides (sequence, head, query), 16-byte aligned
+ *          rows; out must not overlap any input.
+ *  lse:    fp32 [S][H][T] contiguous, log of each row's sum of exp(scale *
+ *          q.k); or NULL.
+ *  scale:  of the logits; 0 means 1 / sqrt(d).
+ *  accumulate: 1 adds to weight[slot] the softmax weights the slot received,
+ *          summed over the T queries and the H / Hkv query heads of its KV
+ *          head, in a fixed order (the same inputs give the same bits).
+ *  scratch: >= hkv_shared_attend_bytes bytes, 256-byte aligned, not shared
+ *          by calls that may overlap on the GPU.
+ * Rows of free slots are never used, whatever they hold; NaN or infinities
+ * in k or v rows of tokens that are held reach any query of their sequence.
+ * Errors: INVALID_ARG, CAPACITY (scratch too small), CUDA. */
+HKV_API hkv_status hkv_shared_attend(const hkv_shared_cache* cache, const void* q,
+                                     const int64_t* q_stride, void* out,
+                                     const int64_t* out_stride, float* lse, int32_t num_queries,
+                                     double scale, int32_t accumulate, void* scratch,
+                                     size_t scratch_bytes, void* stream);
+
+/* Bytes of scratch hkv_shared_evict needs.  Errors: INVALID_ARG. */
+HKV_API hkv_status hkv_shared_evict_bytes(const hkv_shared_cache* cache, size_t* bytes);
+
+/* Eviction by accumulated weight: every head whose len reached budget +
+ * slack (budget int32 [S][Hkv] on the device, below 0 taken as 0; slack >=
+ * 1) is brought back to its budget; the others are left untouched, so one
+ * call per step serves every step.  Evicted are the len - budget tokens
+ * lowest in the order
+ *   (recent, weight, position, slot)
+ * where a token is recent when its position is less than `recent` behind the
+ * head's newest one (recent tokens so go last, and among themselves by
+ * position, whatever their weight); a NaN weight counts as above every
+ * number.  The i-th surviving slot at or above the budget then moves (its k
+ * and v rows, position and weight) into the i-th evicted slot below it;
+ * slots at or above the budget keep what they held.
+ *  scratch: as for hkv_shared_attend.
+ * Errors: INVALID_ARG (also without pos or weight), CAPACITY, CUDA. */
+HKV_API hkv_status hkv_shared_evict(const hkv_shared_cache* cache, const int32_t* budget,
+                                    int32_t recent, int32_t slack, void* scratch,
+                                    size_t scratch_bytes, void* stream);
+
 /* ---- Allocation-free entry point ------------------------------------------ */
 
 /* Prefill attention and head grouping with no device allocation at all.

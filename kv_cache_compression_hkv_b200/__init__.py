@@ -11,6 +11,7 @@ from ._lib import (  # noqa: F401
     MODE_UNIFORM, Config, HeadKVCache, HkvError,
     LIB_PATH, classify_groups, classify_rows, declared_symbols, lib, pool_bytes,
     ste_select_batch)
+from .shared import SharedConfig, SharedPrefixCache  # noqa: F401
 
 
 def config_for(w, mode: int = MODE_HEADKV, stratified: bool = True, num_seqs: int | None = None,

@@ -72,6 +72,11 @@ def lib():
             "hkv_classify_rows": [P, I, I, I, D, P, P, P],
             "hkv_classify_groups": [P, I, I, I, I, P, I, D, P, P, P],
             "hkv_ste_select_batch": [P, P, P, P, I, I, I, I, I, I, P, P],
+            "hkv_shared_append": [P, P, P, P, P, P, I, P],
+            "hkv_shared_attend_bytes": [P, I, I, P],
+            "hkv_shared_attend": [P, P, P, P, P, P, I, D, I, P, Z, P],
+            "hkv_shared_evict_bytes": [P, P],
+            "hkv_shared_evict": [P, P, I, I, P, Z, P],
             "hkv_prefill_classify_noalloc": [I, I, I, P, P, P, I, I64, I, D, P, P, P, P, P],
         }
         for name, args in sig.items():

@@ -1,0 +1,516 @@
+// shared.cu -- shared-prefix cache: append, attention over prefix and own
+// tokens on the CUDA cores, the joining of partial results, and the
+// accumulated weights.
+//
+// A row (sequence s, query head h, query t) attends over the n_p keys of its
+// prefix and its own keys j < lim:
+//     x_j = log2(e) scale q.k_j,   m = max x_j,   l = sum 2^(x_j - m),
+//     o = sum 2^(x_j - m) v_j / l,   weight_j += 2^(x_j - m) / l.
+// Keys are cut into ranges that different blocks take; each leaves (m, l,
+// sum 2^(x - m) v) of its range, all in fp32, and combine_kernel joins them:
+// with M = max m_i, o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
+#include <math.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+#include "ptx.cuh"
+#include "shared.cuh"
+
+namespace hkv {
+namespace shared {
+
+namespace {
+
+template <typename T> __device__ __forceinline__ float4 load4(const T* p);
+template <> __device__ __forceinline__ float4 load4<float>(const float* p) {
+    return *reinterpret_cast<const float4*>(p);
+}
+template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// append
+// ---------------------------------------------------------------------------
+
+// One block per (sequence, KV head, slice of the new tokens): rows are copied
+// as 16-byte pieces.  With more than one slice per head the lengths are
+// advanced by bump_kernel behind this launch (another block may not have read
+// them yet); with one, here.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) append_rows_kernel(View a, const T* __restrict__ kt, int64_t k0, int64_t k1,
+                                                          int64_t k2, const T* __restrict__ vt, int64_t v0,
+                                                          int64_t v1, int64_t v2, const float* __restrict__ wt,
+                                                          int n_new, int slices) {
+    const int head = blockIdx.x / slices, part = blockIdx.x % slices;
+    const int s = head / a.Hk, hk = head % a.Hk;
+    const int len = own_len(a, s, hk), np0 = a.next_pos ? a.next_pos[head] : 0;
+    if (n_new > a.cap - len) {
+        if (a.status && part == 0 && threadIdx.x == 0 && atomicCAS(a.status, 0, HKV_ERR_CAPACITY) == 0)
+            atomicExch(a.status + 1, head);
+        return;
+    }
+    if (slices == 1) __syncthreads();  // everyone has read the length
+    const int per = (n_new + slices - 1) / slices;
+    const int lo = part * per, hi = min(n_new, lo + per);
+    constexpr int PIECES = D * (int)sizeof(T) / 16;
+    const T* ksrc = kt + s * k0 + hk * k1;
+    const T* vsrc = vt + s * v0 + hk * v1;
+    T* kd = static_cast<T*>(a.k) + s * a.ks[0] + hk * a.ks[1];
+    T* vd = static_cast<T*>(a.v) + s * a.vs[0] + hk * a.vs[1];
+    constexpr int EP = 16 / (int)sizeof(T);
+    for (int e = lo * PIECES + threadIdx.x; e < hi * PIECES; e += 256) {
+        const int i = e / PIECES, c = (e % PIECES) * EP;
+        const uint4 x = *reinterpret_cast<const uint4*>(ksrc + i * k2 + c);
+        const uint4 y = *reinterpret_cast<const uint4*>(vsrc + i * v2 + c);
+        *reinterpret_cast<uint4*>(kd + (int64_t)(len + i) * a.ks[2] + c) = x;
+        *reinterpret_cast<uint4*>(vd + (int64_t)(len + i) * a.vs[2] + c) = y;
+    }
+    const int64_t row0 = (int64_t)head * a.cap + len;
+    for (int i = lo + threadIdx.x; i < hi; i += 256) {
+        if (a.pos) a.pos[row0 + i] = np0 + i;
+        if (a.weight) a.weight[row0 + i] = wt ? wt[(int64_t)head * n_new + i] : 0.f;
+    }
+    if (slices == 1 && threadIdx.x == 0) {
+        a.len[head] = len + n_new;
+        if (a.next_pos) a.next_pos[head] = np0 + n_new;
+    }
+}
+
+__global__ void bump_kernel(View a, int n_new) {
+    const int head = blockIdx.x * blockDim.x + threadIdx.x;
+    if (head >= a.S * a.Hk) return;
+    const int len = clamp_len(a.len[head], a.cap);
+    if (n_new > a.cap - len) return;
+    a.len[head] = len + n_new;
+    if (a.next_pos) a.next_pos[head] += n_new;
+}
+
+cudaError_t launch_append(const View& a, int dtype, int d, const void* k_t, const int64_t* ks, const void* v_t,
+                          const int64_t* vs, const float* w_t, cudaStream_t st) {
+    const int heads = a.S * a.Hk, n_new = a.T;
+    int slices = 1;
+    while (heads * slices < 592 && n_new / slices > 64) slices *= 2;
+    auto go = [&](auto tag, auto dim) {
+        using E = decltype(tag);
+        constexpr int D = decltype(dim)::value;
+        append_rows_kernel<E, D><<<heads * slices, 256, 0, st>>>(a, (const E*)k_t, ks[0], ks[1], ks[2], (const E*)v_t,
+                                                                 vs[0], vs[1], vs[2], w_t, n_new, slices);
+    };
+    using I64 = std::integral_constant<int, 64>;
+    using I128 = std::integral_constant<int, 128>;
+    if (dtype == HKV_DTYPE_F32) d == 64 ? go(float(), I64()) : go(float(), I128());
+    else d == 64 ? go(__nv_bfloat16(), I64()) : go(__nv_bfloat16(), I128());
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && slices > 1) {
+        bump_kernel<<<(heads + 255) / 256, 256, 0, st>>>(a, n_new);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+// ---------------------------------------------------------------------------
+// attention on the CUDA cores
+// ---------------------------------------------------------------------------
+
+constexpr int RT = 16;   // rows of a block
+constexpr int KT = 32;   // keys a step
+
+template <int D> struct SimtSmem {
+    static constexpr int KP = D + 4;  // padded rows: float4 reads of 32 rows spread over the banks
+    float q[RT][KP];
+    float k[KT][KP];
+    float v[KT][D];
+    float p[KT][RT];
+    int list[RT + 1];
+    int res[4];
+};
+
+// One block per (tile of 16 rows, key range): prefix tiles first, then the
+// own keys.  Warp w owns rows 4w .. 4w + 3: lane = key for the logits, lanes
+// across d for the weighted sum.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) attend_simt_kernel(View a, int ptiles, int otiles) {
+    extern __shared__ __align__(16) unsigned char raw[];
+    SimtSmem<D>& sm = *reinterpret_cast<SimtSmem<D>*>(raw);
+    int* cnt = reinterpret_cast<int*>(raw + sizeof(SimtSmem<D>));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rps = a.rep * a.T;
+    const int64_t R = (int64_t)a.S * a.H * a.T;
+    const int n_prefix = ptiles * a.Hk * a.np;
+    const bool is_prefix = (int)blockIdx.x < n_prefix;
+    const T *kb, *vb;
+    int64_t kst, vst;
+    int lo, hi, slot, rows, hk, s = 0, first = 0, n_own = 0;
+    if (is_prefix) {
+        const int b = blockIdx.x;
+        const int j = b % a.np, tile = b / a.np / a.Hk;
+        hk = b / a.np % a.Hk;
+        int g;
+        if (!find_prefix_tile(a, tile, RT, g, first, rows, cnt, sm.res, sm.list)) return;
+        split_range(prefix_len(a, g), a.np, j, lo, hi);
+        slot = j;
+        kb = static_cast<const T*>(a.pk) + g * a.pks[0] + hk * a.pks[1];
+        vb = static_cast<const T*>(a.pv) + g * a.pvs[0] + hk * a.pvs[1];
+        kst = a.pks[2];
+        vst = a.pvs[2];
+    } else {
+        const int b = blockIdx.x - n_prefix;
+        const int j = b % a.no, tile = b / a.no % otiles;
+        const int sh = b / a.no / otiles;
+        s = sh / a.Hk;
+        hk = sh % a.Hk;
+        first = tile * RT;
+        rows = min(RT, rps - first);
+        n_own = own_len(a, s, hk);
+        split_range(n_own, a.no, j, lo, hi);
+        slot = a.np + j;
+        kb = static_cast<const T*>(a.k) + s * a.ks[0] + hk * a.ks[1];
+        vb = static_cast<const T*>(a.v) + s * a.vs[0] + hk * a.vs[1];
+        kst = a.ks[2];
+        vst = a.vs[2];
+    }
+    if (lo >= hi) return;  // combine_kernel knows
+    const int o0 = first / rps;
+    auto seq_row = [&](int r, int& sq, int& i) {  // row r of the tile -> sequence, row within (sequence, KV head)
+        const int f = first + r;
+        sq = is_prefix ? sm.list[f / rps - o0] : s;
+        i = is_prefix ? f % rps : f;
+    };
+    for (int e = tid; e < RT * (D / 4); e += 128) {
+        const int r = e / (D / 4), c = e % (D / 4) * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows) {
+            int sq, i;
+            seq_row(r, sq, i);
+            x = load4(static_cast<const T*>(a.q) + sq * a.qs[0] + (hk * a.rep + i % a.rep) * a.qs[1] +
+                      i / a.rep * a.qs[2] + c);
+        }
+        sm.q[r][c] = x.x * a.qscale;
+        sm.q[r][c + 1] = x.y * a.qscale;
+        sm.q[r][c + 2] = x.z * a.qscale;
+        sm.q[r][c + 3] = x.w * a.qscale;
+    }
+    constexpr int V = D / 32;
+    float m[4], l[4], o[4][V];
+    int lim[4];
+    float* lrow[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int r = warp * 4 + u;
+        m[u] = -INFINITY;
+        l[u] = 0.f;
+#pragma unroll
+        for (int c = 0; c < V; ++c) o[u][c] = 0.f;
+        lim[u] = r >= rows ? 0 : (is_prefix ? hi : own_limit(a, n_own, first + r));
+        lrow[u] = !is_prefix && a.logit && r < rows
+                      ? a.logit + ((int64_t)(s * a.Hk + hk) * rps + first + r) * a.cap : nullptr;
+    }
+    int stop = hi;
+    if (!is_prefix) stop = min(hi, own_limit(a, n_own, first + rows - 1));
+    if (!is_prefix && a.logit) stop = hi;  // every kept logit is written, -inf past a row's limit
+    for (int k0 = lo; k0 < stop; k0 += KT) {
+        __syncthreads();
+        for (int e = tid; e < KT * (D / 4); e += 128) {
+            const int r = e / (D / 4), c = e % (D / 4) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+            if (k0 + r < hi) {
+                x = load4(kb + (int64_t)(k0 + r) * kst + c);
+                y = load4(vb + (int64_t)(k0 + r) * vst + c);
+            }
+            *reinterpret_cast<float4*>(&sm.k[r][c]) = x;
+            *reinterpret_cast<float4*>(&sm.v[r][c]) = y;
+        }
+        __syncthreads();
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int c = 0; c < D; c += 4) {
+            const float4 kk = *reinterpret_cast<const float4*>(&sm.k[lane][c]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float4 qq = *reinterpret_cast<const float4*>(&sm.q[warp * 4 + u][c]);
+                x[u] = fmaf(kk.x, qq.x, fmaf(kk.y, qq.y, fmaf(kk.z, qq.z, fmaf(kk.w, qq.w, x[u]))));
+            }
+        }
+        const int key = k0 + lane;
+        float pw[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const bool in = key < lim[u] && key < hi;
+            x[u] = in ? x[u] : -INFINITY;
+            if (lrow[u] && key < hi) lrow[u][key] = x[u];
+            float mt = x[u];
+#pragma unroll
+            for (int off = 16; off; off >>= 1) mt = fmaxf(mt, __shfl_xor_sync(FULL_MASK, mt, off));
+            const float mn = fmaxf(m[u], mt);
+            const float mb = mn == -INFINITY ? 0.f : mn;
+            const float alpha = exp2f(m[u] - mb);
+            pw[u] = in ? exp2f(x[u] - mb) : 0.f;
+            l[u] = l[u] * alpha + pw[u];  // each lane its own keys; summed at the end
+            m[u] = mn;
+#pragma unroll
+            for (int c = 0; c < V; ++c) o[u][c] *= alpha;
+        }
+        *reinterpret_cast<float4*>(&sm.p[lane][warp * 4]) = make_float4(pw[0], pw[1], pw[2], pw[3]);
+        __syncwarp();
+#pragma unroll 4
+        for (int kk = 0; kk < KT; ++kk) {
+            const float4 p4 = *reinterpret_cast<const float4*>(&sm.p[kk][warp * 4]);
+            const float pr[4] = {p4.x, p4.y, p4.z, p4.w};
+            float vv[V];
+            if constexpr (V == 4) {
+                const float4 y = *reinterpret_cast<const float4*>(&sm.v[kk][lane * 4]);
+                vv[0] = y.x; vv[1] = y.y; vv[2] = y.z; vv[3] = y.w;
+            } else {
+                const float2 y = *reinterpret_cast<const float2*>(&sm.v[kk][lane * 2]);
+                vv[0] = y.x; vv[1] = y.y;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int c = 0; c < V; ++c) o[u][c] = fmaf(pr[u], vv[c], o[u][c]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int r = warp * 4 + u;
+        float ls = l[u];
+#pragma unroll
+        for (int off = 16; off; off >>= 1) ls += __shfl_xor_sync(FULL_MASK, ls, off);
+        if (r >= rows) continue;
+        int sq, i;
+        seq_row(r, sq, i);
+        const int64_t row = row_of(a, sq, hk, i);
+        // (a sum that is NaN, of NaN logits alone, must not pass for an empty row)
+        if (lane == 0) a.part_ml[slot * R + row] = make_float2(ls != ls && m[u] == -INFINITY ? 0.f : m[u], ls);
+        float* po = a.part_o + (slot * R + row) * D + lane * V;
+#pragma unroll
+        for (int c = 0; c < V; ++c) po[c] = o[u][c];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// joining the partial results; accumulated weights from kept logits
+// ---------------------------------------------------------------------------
+
+// (max, 1 / sum) of a row over its valid partial slots, by the calling warp;
+// the weight of slot j (lane j % 32, register j / 32) in f.
+__device__ __forceinline__ bool slot_valid(const View& a, int j, int np_keys, int own_keys) {
+    int lo, hi;
+    if (j < a.np) split_range(np_keys, a.np, j, lo, hi);
+    else split_range(own_keys, a.no, j - a.np, lo, hi);
+    return lo < hi;
+}
+
+// Blocks [0, row_blocks): one warp per row joins its slots and writes the
+// output.  Blocks beyond: one (sequence, KV head, 256 slots) each, weight +=
+// the kept logits' weights over the rows, in row order.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) combine_kernel(View a, int row_blocks) {
+    __shared__ float2 ml_s[STREAM_ROWS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t R = (int64_t)a.S * a.H * a.T;
+    const int ns = a.np + a.no;
+    auto row_max_sum = [&](int64_t row, int pk, int ok, float& M, float& L) {
+        M = -INFINITY;
+        for (int j = lane; j < ns; j += 32)
+            if (slot_valid(a, j, pk, ok)) M = fmaxf(M, a.part_ml[j * R + row].x);
+#pragma unroll
+        for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, off));
+        L = 0.f;
+        if (M != -INFINITY)
+            for (int j = lane; j < ns; j += 32)
+                if (slot_valid(a, j, pk, ok)) {
+                    const float2 x = a.part_ml[j * R + row];
+                    if (x.x != -INFINITY) L += x.y * exp2f(x.x - M);
+                }
+#pragma unroll
+        for (int off = 16; off; off >>= 1) L += __shfl_xor_sync(FULL_MASK, L, off);
+    };
+    if ((int)blockIdx.x < row_blocks) {
+        const int64_t row = (int64_t)blockIdx.x * 8 + warp;
+        if (row >= R) return;
+        const int t = (int)(row % a.T), h = (int)(row / a.T % a.H), s = (int)(row / a.T / a.H);
+        const int pk = prefix_len(a, prefix_of(a, s)), ok = own_len(a, s, h / a.rep);
+        float M, L;
+        row_max_sum(row, pk, ok, M, L);
+        constexpr int V = D / 32;
+        float acc[V];
+#pragma unroll
+        for (int c = 0; c < V; ++c) acc[c] = 0.f;
+        const bool some = !(M == -INFINITY);
+        const float inv = some ? 1.f / L : 0.f;
+        if (some)
+            for (int j = 0; j < ns; ++j) {
+                if (!slot_valid(a, j, pk, ok)) continue;
+                const float mj = a.part_ml[j * R + row].x;
+                const float f = mj == -INFINITY ? 0.f : exp2f(mj - M);
+                if (f == 0.f) continue;
+                const float* po = a.part_o + (j * R + row) * D + lane * V;
+#pragma unroll
+                for (int c = 0; c < V; ++c) acc[c] = fmaf(po[c], f, acc[c]);
+            }
+        T* orow = static_cast<T*>(a.out) + s * a.os[0] + h * a.os[1] + t * a.os[2] + lane * V;
+#pragma unroll
+        for (int c = 0; c < V; ++c) from_float(orow[c], acc[c] * inv);
+        if (lane == 0) {
+            const float l2 = some ? M + log2f(L) : -INFINITY;
+            if (a.lse) a.lse[row] = l2 * 0.6931471805599453f;
+            if (a.row_lse) a.row_lse[row] = l2;
+        }
+        return;
+    }
+    const int chunks = (a.cap + 255) / 256;
+    const int b = blockIdx.x - row_blocks, sh = b / chunks;
+    const int s = sh / a.Hk, hk = sh % a.Hk, rps = a.rep * a.T;
+    const int n = own_len(a, s, hk);
+    const int j0 = b % chunks * 256;
+    if (j0 >= n) return;
+    const int pk = prefix_len(a, prefix_of(a, s));
+    for (int i = warp; i < rps; i += 8) {
+        float M, L;
+        row_max_sum(row_of(a, s, hk, i), pk, n, M, L);
+        if (lane == 0) ml_s[i] = make_float2(M, M == -INFINITY ? 0.f : 1.f / L);
+    }
+    __syncthreads();
+    const int j = j0 + threadIdx.x;
+    if (j >= n) return;
+    const float* lg = a.logit + (int64_t)sh * rps * a.cap + j;
+    float sum = 0.f;
+    for (int i = 0; i < rps; ++i) {
+        const float2 x = ml_s[i];
+        if (x.x != -INFINITY) sum += exp2f(lg[(int64_t)i * a.cap] - x.x) * x.y;
+    }
+    a.weight[(int64_t)sh * a.cap + j] += sum;
+}
+
+// ---------------------------------------------------------------------------
+// accumulated weights of many rows: the logits once more, summed by key
+// ---------------------------------------------------------------------------
+
+// One block per (sequence, KV head, 32 keys): lane = key, warp w takes rows
+// 4w .. 4w + 3 of every tile of 16; a key's weight 2^(x - lse) over the rows
+// that see it, per tile, then over the tiles, then over the warps.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) column_sums_simt_kernel(View a) {
+    extern __shared__ __align__(16) unsigned char raw[];
+    SimtSmem<D>& sm = *reinterpret_cast<SimtSmem<D>*>(raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int chunks = (a.cap + KT - 1) / KT;
+    const int sh = blockIdx.x / chunks, k0 = blockIdx.x % chunks * KT;
+    const int s = sh / a.Hk, hk = sh % a.Hk, rps = a.rep * a.T;
+    const int n = own_len(a, s, hk);
+    if (k0 >= n) return;
+    const T* kb = static_cast<const T*>(a.k) + s * a.ks[0] + hk * a.ks[1];
+    for (int e = tid; e < KT * (D / 4); e += 128) {
+        const int r = e / (D / 4), c = e % (D / 4) * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + r < n) x = load4(kb + (int64_t)(k0 + r) * a.ks[2] + c);
+        *reinterpret_cast<float4*>(&sm.k[r][c]) = x;
+    }
+    // the first row that sees key k0: n - T + t + 1 > k0
+    const int t0 = max(0, k0 - (n - a.T));
+    const int key = k0 + lane;
+    float total = 0.f;
+    for (int f = t0 * a.rep / RT * RT; f < rps; f += RT) {
+        __syncthreads();
+        const int rows = min(RT, rps - f);
+        for (int e = tid; e < RT * (D / 4); e += 128) {
+            const int r = e / (D / 4), c = e % (D / 4) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < rows) {
+                const int i = f + r;
+                x = load4(static_cast<const T*>(a.q) + s * a.qs[0] + (hk * a.rep + i % a.rep) * a.qs[1] +
+                          i / a.rep * a.qs[2] + c);
+            }
+            sm.q[r][c] = x.x * a.qscale;
+            sm.q[r][c + 1] = x.y * a.qscale;
+            sm.q[r][c + 2] = x.z * a.qscale;
+            sm.q[r][c + 3] = x.w * a.qscale;
+        }
+        __syncthreads();
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int c = 0; c < D; c += 4) {
+            const float4 kk = *reinterpret_cast<const float4*>(&sm.k[lane][c]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float4 qq = *reinterpret_cast<const float4*>(&sm.q[warp * 4 + u][c]);
+                x[u] = fmaf(kk.x, qq.x, fmaf(kk.y, qq.y, fmaf(kk.z, qq.z, fmaf(kk.w, qq.w, x[u]))));
+            }
+        }
+        float tile = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int r = warp * 4 + u;
+            if (r >= rows) continue;
+            const float e = a.row_lse[row_of(a, s, hk, f + r)];
+            if (key < n && key < own_limit(a, n, f + r) && e != -INFINITY) tile += exp2f(x[u] - e);
+        }
+        total += tile;
+    }
+    __syncthreads();
+    float* red = &sm.p[0][0];
+    red[warp * 32 + lane] = total;
+    __syncthreads();
+    if (warp == 0 && key < n)
+        a.weight[(int64_t)sh * a.cap + key] += (red[lane] + red[32 + lane]) + (red[64 + lane] + red[96 + lane]);
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+
+namespace {
+
+template <typename F> cudaError_t by_type(int dtype, int d, F&& f) {
+    using I64 = std::integral_constant<int, 64>;
+    using I128 = std::integral_constant<int, 128>;
+    if (dtype == HKV_DTYPE_F32) return d == 64 ? f(float(), I64()) : f(float(), I128());
+    return d == 64 ? f(__nv_bfloat16(), I64()) : f(__nv_bfloat16(), I128());
+}
+
+}  // namespace
+
+cudaError_t launch_attend_simt(const View& a, int dtype, int d, cudaStream_t st) {
+    const int rps = a.rep * a.T, otiles = (rps + RT - 1) / RT;
+    const int64_t ptiles = a.np ? max_prefix_tiles(a.S, a.G, rps, RT) : 0;
+    const int64_t blocks = ptiles * a.Hk * a.np + (int64_t)a.S * a.Hk * otiles * a.no;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    return by_type(dtype, d, [&](auto tag, auto dim) {
+        using E = decltype(tag);
+        constexpr int D = decltype(dim)::value;
+        const size_t sm = sizeof(SimtSmem<D>) + (size_t)a.G * 4;
+        attend_simt_kernel<E, D><<<(int)blocks, 128, sm, st>>>(a, (int)ptiles, otiles);
+        return cudaGetLastError();
+    });
+}
+
+cudaError_t launch_combine(const View& a, int dtype, int d, cudaStream_t st) {
+    const int64_t R = (int64_t)a.S * a.H * a.T, rb = (R + 7) / 8;
+    const int64_t blocks = rb + (a.logit ? (int64_t)a.S * a.Hk * ((a.cap + 255) / 256) : 0);
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    return by_type(dtype, d, [&](auto tag, auto dim) {
+        using E = decltype(tag);
+        combine_kernel<E, decltype(dim)::value><<<(int)blocks, 256, 0, st>>>(a, (int)rb);
+        return cudaGetLastError();
+    });
+}
+
+cudaError_t launch_column_sums_simt(const View& a, int dtype, int d, cudaStream_t st) {
+    const int64_t blocks = (int64_t)a.S * a.Hk * ((a.cap + KT - 1) / KT);
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    return by_type(dtype, d, [&](auto tag, auto dim) {
+        using E = decltype(tag);
+        constexpr int D = decltype(dim)::value;
+        column_sums_simt_kernel<E, D><<<(int)blocks, 128, sizeof(SimtSmem<D>), st>>>(a);
+        return cudaGetLastError();
+    });
+}
+
+}  // namespace shared
+}  // namespace hkv

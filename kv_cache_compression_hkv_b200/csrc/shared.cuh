@@ -1,0 +1,167 @@
+// shared.cuh -- device view of a shared-prefix cache and what its kernels
+// agree on: how rows are numbered, how key ranges are split, and the partial
+// results that the combining kernel joins.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/hkv.h"
+#include "hkv_internal.cuh"
+
+namespace hkv {
+namespace shared {
+
+constexpr int KEY_STEP = 64;     // key ranges start at multiples of this
+constexpr int MAX_SPLITS = 64;   // splits of the own keys, and of the prefix keys
+constexpr int MAX_PREFIXES = 1024;
+// Own tokens of at most this many query rows (query heads of a KV head x
+// queries) are streamed once with every row's logits kept for the
+// accumulated weights; more rows recompute the logits for them.
+constexpr int STREAM_ROWS = 16;
+
+// The cache and one call's tensors, by value.
+struct View {
+    int32_t S, H, Hk, rep, cap, G, pcap, T;
+    void *k, *v;
+    int64_t ks[3], vs[3];
+    int32_t* pos;
+    float* weight;
+    int32_t* len;
+    int32_t* next_pos;
+    const void *pk, *pv;
+    int64_t pks[3], pvs[3];
+    const int32_t* plen;
+    const int32_t* pof;
+    int32_t* status;
+    const void* q;
+    void* out;
+    int64_t qs[3], os[3];
+    float* lse;
+    float qscale;     // scale * log2(e): logits are in the exp2 domain
+    int32_t accumulate;
+    // partial results of a row: slots [0, np) the prefix's splits, [np, np + no) its own keys'
+    int32_t np, no;
+    float2* part_ml;  // [np + no][R] (max, sum)
+    float* part_o;    // [np + no][R][d]
+    float* logit;     // [S][Hk][rep T][cap] exp2-domain logits of the own keys (stream path, accumulate)
+    float* row_lse;   // [R] log2 of the row sums (tile path, accumulate)
+};
+
+__device__ __forceinline__ int clamp_len(int n, int cap) { return n < 0 ? 0 : (n > cap ? cap : n); }
+__device__ __forceinline__ int own_len(const View& a, int s, int hk) {
+    return clamp_len(a.len[(size_t)s * a.Hk + hk], a.cap);
+}
+// Prefix of a sequence (-1: none) and its length.
+__device__ __forceinline__ int prefix_of(const View& a, int s) {
+    if (a.G == 0) return -1;
+    const int g = a.pof[s];
+    return (unsigned)g < (unsigned)a.G ? g : -1;
+}
+__device__ __forceinline__ int prefix_len(const View& a, int g) {
+    return g < 0 ? 0 : clamp_len(a.plen[g], a.pcap);
+}
+// Split j of n keys cut in ns: [lo, hi), empty when lo >= hi.
+__device__ __forceinline__ int split_size(int n, int ns) {
+    const int c = (n + ns - 1) / ns;
+    return (c + KEY_STEP - 1) / KEY_STEP * KEY_STEP;
+}
+__device__ __forceinline__ void split_range(int n, int ns, int j, int& lo, int& hi) {
+    const int64_t c = split_size(n, ns);
+    lo = (int)min((int64_t)n, c * j);
+    hi = (int)min((int64_t)n, c * (j + 1));
+}
+// Row of (sequence, query head, query) in lse and the partial arrays.
+__device__ __forceinline__ int64_t row_index(const View& a, int s, int h, int t) {
+    return ((int64_t)s * a.H + h) * a.T + t;
+}
+// Rows of one (sequence, KV head) are numbered i = t * rep + (query head within the KV head).
+__device__ __forceinline__ int64_t row_of(const View& a, int s, int hk, int i) {
+    return row_index(a, s, hk * a.rep + i % a.rep, i / a.rep);
+}
+// Own slots row i sees: those before len - T + t + 1.
+__device__ __forceinline__ int own_limit(const View& a, int n, int i) {
+    const int lim = n - a.T + i / a.rep + 1;
+    return lim < 0 ? 0 : lim;
+}
+
+// Finds the `tile`-th tile of `rt` rows among the prefixes' row lists: the
+// rows of prefix g are those of the sequences that continue it (ascending),
+// rep * T each, and every prefix starts a new tile.  Gives the prefix, the
+// first row and the number of rows, and in `list` the sequences of the rows:
+// list[o - first / (rep T)] for the o-th sequence of the prefix (at most rt
+// + 1 of them).  False: there is no such tile.  Called by the whole block;
+// cnt: G ints of shared memory, res: four.
+__device__ inline bool find_prefix_tile(const View& a, int tile, int rt, int& g, int& first, int& rows,
+                                        int* cnt, int* res, int* list) {
+    const int tid = threadIdx.x, rps = a.rep * a.T;
+    for (int i = tid; i < a.G; i += blockDim.x) cnt[i] = 0;
+    if (tid < 4) res[tid] = -1;
+    __syncthreads();
+    for (int i = tid; i < a.S; i += blockDim.x) {
+        const int p = prefix_of(a, i);
+        if (p >= 0) atomicAdd(cnt + p, 1);
+    }
+    __syncthreads();
+    if (tid < 32) {
+        // running tile counts over the prefixes, 32 at a time
+        int base = 0;
+        for (int g0 = 0; g0 < a.G; g0 += 32) {
+            const int gi = g0 + tid;
+            const int64_t r = gi < a.G ? (int64_t)cnt[gi] * rps : 0;
+            const int nt = (int)((r + rt - 1) / rt);
+            int incl = nt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(FULL_MASK, incl, o);
+                if (tid >= o) incl += y;
+            }
+            const int lo = base + incl - nt;
+            if (tile >= lo && tile < lo + nt) {
+                res[0] = gi;
+                res[1] = (tile - lo) * rt;
+                res[2] = (int)min((int64_t)rt, r - (int64_t)(tile - lo) * rt);
+            }
+            base += __shfl_sync(FULL_MASK, incl, 31);
+            if (base > tile) break;
+        }
+        __syncwarp();
+        if (res[0] >= 0) {
+            const int gg = res[0], o0 = res[1] / rps, o1 = (res[1] + res[2] - 1) / rps;
+            int ord = 0;
+            for (int i0 = 0; i0 < a.S && ord <= o1; i0 += 32) {
+                const int i = i0 + tid;
+                const bool mine = i < a.S && prefix_of(a, i) == gg;
+                const unsigned b = __ballot_sync(FULL_MASK, mine);
+                const int o = ord + __popc(b & ((1u << tid) - 1));
+                if (mine && o >= o0 && o <= o1) list[o - o0] = i;
+                ord += __popc(b);
+            }
+        }
+    }
+    __syncthreads();
+    g = res[0];
+    first = res[1];
+    rows = res[2];
+    return g >= 0;
+}
+
+// Upper bound of the prefix tiles of a call (the groups are on the device).
+inline int64_t max_prefix_tiles(int S, int G, int rows_per_seq, int rt) {
+    if (G == 0) return 0;
+    const int64_t full = (int64_t)S * rows_per_seq / rt;
+    return full + (G < S ? G : S);
+}
+
+// launchers (host)
+cudaError_t launch_append(const View& a, int dtype, int d, const void* k_t, const int64_t* kts, const void* v_t,
+                          const int64_t* vts, const float* w_t, cudaStream_t st);
+cudaError_t launch_attend_simt(const View& a, int dtype, int d, cudaStream_t st);
+cudaError_t launch_combine(const View& a, int dtype, int d, cudaStream_t st);
+cudaError_t launch_column_sums_simt(const View& a, int dtype, int d, cudaStream_t st);
+cudaError_t launch_evict(const View& a, int dtype, int d, const int32_t* budget, int recent, int slack,
+                         int32_t* holes, cudaStream_t st);
+
+}  // namespace shared
+}  // namespace hkv

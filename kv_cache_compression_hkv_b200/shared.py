@@ -1,0 +1,242 @@
+"""Shared-prefix cache: binding of the hkv_shared_* calls (include/hkv.h).
+
+A batch whose sequences continue shared prompts (the images of one prompt,
+the unconditional streams of all of them) holds each prompt's keys and values
+once; every sequence adds its own tokens, whose attention weights accumulate
+and decide what an eviction drops.  This module marshals arguments only.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes as C
+from dataclasses import dataclass
+
+import torch
+
+from ._lib import DTYPE_BF16, DTYPE_F32, _check, lib
+
+
+class _Cache(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in (
+        "dtype", "head_dim", "num_seqs", "num_heads", "num_kv_heads", "capacity", "num_prefixes",
+        "prefix_capacity")] + [
+        ("k", C.c_void_p), ("v", C.c_void_p), ("k_stride", C.c_int64 * 3), ("v_stride", C.c_int64 * 3),
+        ("pos", C.c_void_p), ("weight", C.c_void_p), ("len", C.c_void_p), ("next_pos", C.c_void_p),
+        ("prefix_k", C.c_void_p), ("prefix_v", C.c_void_p), ("prefix_k_stride", C.c_int64 * 3),
+        ("prefix_v_stride", C.c_int64 * 3), ("prefix_len", C.c_void_p), ("prefix_of", C.c_void_p),
+        ("status", C.c_void_p)]
+
+
+_Strides = C.c_int64 * 3
+
+
+@dataclass
+class SharedConfig:
+    num_seqs: int
+    num_heads: int          # query heads, a multiple of num_kv_heads
+    num_kv_heads: int
+    head_dim: int           # 64 or 128
+    capacity: int           # own slots of each (sequence, KV head)
+    num_prefixes: int = 0   # prompts shared by the sequences
+    prefix_capacity: int = 0
+    dtype: int = DTYPE_BF16
+
+    @property
+    def torch_dtype(self):
+        return torch.float32 if self.dtype == DTYPE_F32 else torch.bfloat16
+
+
+class SharedPrefixCache:
+    """Keys and values of a batch: prompts held once, and each sequence's own
+    tokens with the attention weight they have received.
+
+    The buffers are ordinary tensors, allocated here or given by the caller
+    (any strides with unit stride in d and 16-byte rows for the four row
+    buffers), and may be read and written between calls:
+      k, v                [S, Hkv, capacity, d]       own rows
+      pos, weight         [S, Hkv, capacity]          int32, float32
+      lens, next_pos      [S, Hkv]                    int32
+      prefix_k, prefix_v  [G, Hkv, prefix_capacity, d]
+      prefix_lens         [G]                         int32
+      prefix_of           [S]                         int32; outside 0..G-1: no prompt
+    Calls only enqueue on the stream (the current one of the cache's device
+    unless given) and must be ordered when they write the same buffers.
+    Scratch is allocated per call from the stream's memory pool, so calls on
+    several streams and captured graphs never share it.
+    """
+
+    def __init__(self, cfg: SharedConfig, device=None, *, k=None, v=None, pos=None, weight=None, lens=None,
+                 next_pos=None, prefix_k=None, prefix_v=None, prefix_lens=None, prefix_of=None):
+        self.cfg = cfg
+        dev = torch.device(device if device is not None else "cuda")
+        if dev.type != "cuda":
+            raise ValueError(f"device: expected a CUDA device, got {dev}")
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device = dev
+        S, Hk, d, cap, G = cfg.num_seqs, cfg.num_kv_heads, cfg.head_dim, cfg.capacity, cfg.num_prefixes
+        if cfg.dtype not in (DTYPE_F32, DTYPE_BF16) or d not in (64, 128) or S < 1 or Hk < 1 or \
+                cfg.num_heads < 1 or cfg.num_heads % Hk or cap < 1 or G < 0 or (G > 0 and cfg.prefix_capacity < 1):
+            raise ValueError(f"unusable config {cfg}")
+        dt = cfg.torch_dtype
+
+        def own(x, name, shape, dtype, rows=False):
+            if x is None:
+                return torch.zeros(shape, dtype=dtype, device=dev)
+            if not isinstance(x, torch.Tensor) or x.device != dev or x.dtype != dtype or tuple(x.shape) != shape:
+                raise ValueError(f"{name}: expected a {dtype} tensor {list(shape)} on {dev}")
+            if rows:
+                self._rows(x, name)
+            elif not x.is_contiguous():
+                raise ValueError(f"{name}: expected a contiguous tensor")
+            return x
+
+        i32, f32 = torch.int32, torch.float32
+        self.k = own(k, "k", (S, Hk, cap, d), dt, True)
+        self.v = own(v, "v", (S, Hk, cap, d), dt, True)
+        self.pos = own(pos, "pos", (S, Hk, cap), i32)
+        self.weight = own(weight, "weight", (S, Hk, cap), f32)
+        self.lens = own(lens, "lens", (S, Hk), i32)
+        self.next_pos = own(next_pos, "next_pos", (S, Hk), i32)
+        self.prefix_k = self.prefix_v = self.prefix_lens = self.prefix_of = None
+        if G:
+            P = cfg.prefix_capacity
+            self.prefix_k = own(prefix_k, "prefix_k", (G, Hk, P, d), dt, True)
+            self.prefix_v = own(prefix_v, "prefix_v", (G, Hk, P, d), dt, True)
+            self.prefix_lens = own(prefix_lens, "prefix_lens", (G,), i32)
+            self.prefix_of = own(prefix_of, "prefix_of", (S,), i32)
+        self.status = torch.zeros(2, dtype=i32, device=dev)
+
+        c = _Cache(cfg.dtype, d, S, cfg.num_heads, Hk, cap, G, cfg.prefix_capacity if G else 0)
+        c.k, c.v = self.k.data_ptr(), self.v.data_ptr()
+        c.k_stride, c.v_stride = _Strides(*self.k.stride()[:3]), _Strides(*self.v.stride()[:3])
+        c.pos, c.weight = self.pos.data_ptr(), self.weight.data_ptr()
+        c.len, c.next_pos = self.lens.data_ptr(), self.next_pos.data_ptr()
+        if G:
+            c.prefix_k, c.prefix_v = self.prefix_k.data_ptr(), self.prefix_v.data_ptr()
+            c.prefix_k_stride = _Strides(*self.prefix_k.stride()[:3])
+            c.prefix_v_stride = _Strides(*self.prefix_v.stride()[:3])
+            c.prefix_len, c.prefix_of = self.prefix_lens.data_ptr(), self.prefix_of.data_ptr()
+        c.status = self.status.data_ptr()
+        self._c = c
+        self._ref = C.byref(c)
+        n = C.c_size_t()
+        _check(lib().hkv_shared_evict_bytes(self._ref, C.byref(n)), "hkv_shared_evict_bytes")
+        self._evict_bytes = n.value
+        self._attend_bytes = {}  # (T, accumulate) -> scratch bytes
+
+    # -- argument checks -----------------------------------------------------
+    def _rows(self, x, name):
+        st = x.stride()
+        es = 4 if self.cfg.dtype == DTYPE_F32 else 2
+        if st[3] != 1 or any(s < 0 or s * es % 16 for s in st[:3]) or x.data_ptr() % 16:
+            raise ValueError(f"{name}: rows of d contiguous elements on 16-byte boundaries, got strides {st}")
+
+    def _tensor(self, x, name, heads):
+        c = self.cfg
+        if not isinstance(x, torch.Tensor) or x.device != self.device or x.dtype != c.torch_dtype or \
+                x.dim() != 4 or x.shape[0] != c.num_seqs or x.shape[1] != heads or x.shape[3] != c.head_dim:
+            raise ValueError(f"{name}: expected a {c.torch_dtype} tensor [{c.num_seqs}, {heads}, T, {c.head_dim}] "
+                             f"on {self.device}")
+        self._rows(x, name)
+
+    def _on(self, stream):
+        """(context, stream handle): allocations and launches on `stream`."""
+        if stream is None:
+            h = torch.cuda.current_stream(self.device).cuda_stream
+            if torch.cuda.current_device() == self.device.index:
+                return contextlib.nullcontext(), h
+            return torch.cuda.device(self.device), h
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        return torch.cuda.stream(stream), stream.cuda_stream
+
+    # -- calls ---------------------------------------------------------------
+    def append(self, k_t, v_t, weight_t=None, stream=None):
+        """Adds T tokens to every head: k_t, v_t [S, Hkv, T, d]; weight_t
+        [S, Hkv, T] fp32, their accumulated weights (default 0).  A head
+        without T free slots is left as it was (see check)."""
+        c = self.cfg
+        self._tensor(k_t, "k_t", c.num_kv_heads)
+        self._tensor(v_t, "v_t", c.num_kv_heads)
+        T = k_t.shape[2]
+        if v_t.shape[2] != T or T > c.capacity:
+            raise ValueError("k_t, v_t: as many tokens each, at most the capacity")
+        if weight_t is not None and (weight_t.dtype != torch.float32 or weight_t.device != self.device or
+                                     tuple(weight_t.shape) != (c.num_seqs, c.num_kv_heads, T) or
+                                     not weight_t.is_contiguous()):
+            raise ValueError("weight_t: expected a contiguous float32 [S, Hkv, T] tensor on the device")
+        if T == 0:
+            return
+        ctx, h = self._on(stream)
+        with ctx:
+            _check(lib().hkv_shared_append(self._ref, k_t.data_ptr(), _Strides(*k_t.stride()[:3]), v_t.data_ptr(),
+                                           _Strides(*v_t.stride()[:3]),
+                                           None if weight_t is None else weight_t.data_ptr(), T, h),
+                   "hkv_shared_append")
+
+    def attend(self, q, out=None, lse=None, accumulate=True, scale=None, stream=None):
+        """Attention of each sequence's newest T tokens (appended before):
+        q [S, H, T, d] over the sequence's prompt and own tokens, query t
+        seeing the own slots before len - T + t + 1.  Returns (out
+        [S, H, T, d], lse float32 [S, H, T]); a query that sees nothing gets
+        zeros and -inf.  accumulate adds to `weight` the softmax weights each
+        own token received.  scale of the logits: 1 / sqrt(d) by default."""
+        c = self.cfg
+        self._tensor(q, "q", c.num_heads)
+        T = q.shape[2]
+        if T < 1 or T > c.capacity:
+            raise ValueError("q: between 1 token and the capacity")
+        if scale is not None and not (scale != 0 and abs(scale) < float("inf")):
+            raise ValueError("scale: a finite number other than 0")
+        if out is not None:
+            self._tensor(out, "out", c.num_heads)
+            if out.shape != q.shape or 0 in out.stride():
+                raise ValueError("out: expected q's shape, no repeated rows")
+        if lse is not None and (lse.dtype != torch.float32 or lse.device != self.device or
+                                tuple(lse.shape) != tuple(q.shape[:3]) or not lse.is_contiguous()):
+            raise ValueError("lse: expected a contiguous float32 [S, H, T] tensor on the device")
+        key = (T, bool(accumulate))
+        need = self._attend_bytes.get(key)
+        if need is None:
+            n = C.c_size_t()
+            _check(lib().hkv_shared_attend_bytes(self._ref, T, int(key[1]), C.byref(n)), "hkv_shared_attend_bytes")
+            need = self._attend_bytes[key] = n.value
+        ctx, h = self._on(stream)
+        with ctx:
+            if out is None:
+                out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+            if lse is None:
+                lse = torch.empty(q.shape[:3], dtype=torch.float32, device=self.device)
+            scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
+            _check(lib().hkv_shared_attend(self._ref, q.data_ptr(), _Strides(*q.stride()[:3]), out.data_ptr(),
+                                           _Strides(*out.stride()[:3]), lse.data_ptr(), T,
+                                           0.0 if scale is None else float(scale), int(key[1]), scratch.data_ptr(),
+                                           need, h), "hkv_shared_attend")
+        return out, lse
+
+    def evict(self, budgets, recent: int = 0, slack: int = 1, stream=None):
+        """Brings every head holding at least budget + slack tokens back to
+        its budget (int32 [S, Hkv] on the device): the tokens lowest in
+        (recent, weight, position, slot) go, `recent` being those less than
+        that many positions behind the newest; survivors behind the budget
+        move into the holes before it."""
+        c = self.cfg
+        if not isinstance(budgets, torch.Tensor) or budgets.dtype != torch.int32 or budgets.device != self.device or \
+                tuple(budgets.shape) != (c.num_seqs, c.num_kv_heads) or not budgets.is_contiguous():
+            raise ValueError("budgets: expected a contiguous int32 [S, Hkv] tensor on the device")
+        if recent < 0 or slack < 1:
+            raise ValueError("recent at least 0, slack at least 1")
+        ctx, h = self._on(stream)
+        with ctx:
+            scratch = torch.empty(self._evict_bytes, dtype=torch.uint8, device=self.device)
+            _check(lib().hkv_shared_evict(self._ref, budgets.data_ptr(), recent, slack, scratch.data_ptr(),
+                                          self._evict_bytes, h), "hkv_shared_evict")
+
+    def check(self):
+        """(code, detail) of the first error latched on the device (waits)."""
+        code, detail = self.status.tolist()
+        return code, detail
+
+    def clear_error(self):
+        self.status.zero_()
