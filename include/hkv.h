@@ -303,7 +303,8 @@ HKV_API hkv_status hkv_ste_select_batch(const float* score, const int32_t* pos, 
  * key head h / (H / Hkv).  Strides are in elements, of (sequence, KV head,
  * slot) and, for prefixes, (prefix, KV head, slot); the d elements of a row
  * are contiguous.  k, v and prefix rows start on 16-byte boundaries (bases
- * and strides).  Rows of two slots may not overlap.
+ * and strides).  Rows of two slots may not overlap, and strides of held rows
+ * are positive (of a dimension of one: anything).
  * Integers read on the device are taken in range: a len outside
  * [0, capacity] or a prefix_len outside [0, prefix_capacity] as the nearer
  * bound, a prefix_of outside [0, num_prefixes) as no prefix. */
@@ -359,10 +360,10 @@ HKV_API hkv_status hkv_shared_attend_bytes(const hkv_shared_cache* cache, int32_
  * earlier ones whatever an eviction did to their order, and the new ones up
  * to itself).  A query that sees nothing gets zeros and lse = -inf.
  *  q, out: [S][H][T][d] by strides (sequence, head, query), 16-byte aligned
- *          rows; out must not overlap any input.
+ *          rows, no repeated ones; out must not overlap any input.
  *  lse:    fp32 [S][H][T] contiguous, log of each row's sum of exp(scale *
  *          q.k); or NULL.
- *  scale:  of the logits; 0 means 1 / sqrt(d).
+ *  scale:  of the logits, 1e-30 to 1e30 in magnitude; 0 means 1 / sqrt(d).
  *  accumulate: 1 adds to weight[slot] the softmax weights the slot received,
  *          summed over the T queries and the H / Hkv query heads of its KV
  *          head, in a fixed order (the same inputs give the same bits).

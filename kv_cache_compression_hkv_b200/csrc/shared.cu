@@ -297,15 +297,6 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(View a, int ptiles, in
 // joining the partial results; accumulated weights from kept logits
 // ---------------------------------------------------------------------------
 
-// (max, 1 / sum) of a row over its valid partial slots, by the calling warp;
-// the weight of slot j (lane j % 32, register j / 32) in f.
-__device__ __forceinline__ bool slot_valid(const View& a, int j, int np_keys, int own_keys) {
-    int lo, hi;
-    if (j < a.np) split_range(np_keys, a.np, j, lo, hi);
-    else split_range(own_keys, a.no, j - a.np, lo, hi);
-    return lo < hi;
-}
-
 // Blocks [0, row_blocks): one warp per row joins its slots and writes the
 // output.  Blocks beyond: one (sequence, KV head, 256 slots) each, weight +=
 // the kept logits' weights over the rows, in row order.
@@ -476,9 +467,9 @@ template <typename F> cudaError_t by_type(int dtype, int d, F&& f) {
 
 }  // namespace
 
-cudaError_t launch_attend_simt(const View& a, int dtype, int d, cudaStream_t st) {
+cudaError_t launch_attend_simt(const View& a, int dtype, int d, bool skip_prefix, cudaStream_t st) {
     const int rps = a.rep * a.T, otiles = (rps + RT - 1) / RT;
-    const int64_t ptiles = a.np ? max_prefix_tiles(a.S, a.G, rps, RT) : 0;
+    const int64_t ptiles = a.np && !skip_prefix ? max_prefix_tiles(a.S, a.G, rps, RT) : 0;
     const int64_t blocks = ptiles * a.Hk * a.np + (int64_t)a.S * a.Hk * otiles * a.no;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     return by_type(dtype, d, [&](auto tag, auto dim) {

@@ -43,6 +43,8 @@ struct View {
     int32_t accumulate;
     // partial results of a row: slots [0, np) the prefix's splits, [np, np + no) its own keys'
     int32_t np, no;
+    // 1: the slots are no pieces of one list of 64-key tiles, the prefix's and then the own ones (np is 0)
+    int32_t listed;
     float2* part_ml;  // [np + no][R] (max, sum)
     float* part_o;    // [np + no][R][d]
     float* logit;     // [S][Hk][rep T][cap] exp2-domain logits of the own keys (stream path, accumulate)
@@ -71,6 +73,18 @@ __device__ __forceinline__ void split_range(int n, int ns, int j, int& lo, int& 
     const int64_t c = split_size(n, ns);
     lo = (int)min((int64_t)n, c * j);
     hi = (int)min((int64_t)n, c * (j + 1));
+}
+// Whether slot j of the partial results of a row with pk prefix keys and ok own keys was written.
+__device__ __forceinline__ bool slot_valid(const View& a, int j, int pk, int ok) {
+    int lo, hi;
+    if (a.listed) {
+        const int all = (pk + KEY_STEP - 1) / KEY_STEP + (ok + KEY_STEP - 1) / KEY_STEP;
+        const int64_t per = (all + a.no - 1) / a.no;
+        return per * j < all;
+    }
+    if (j < a.np) split_range(pk, a.np, j, lo, hi);
+    else split_range(ok, a.no, j - a.np, lo, hi);
+    return lo < hi;
 }
 // Row of (sequence, query head, query) in lse and the partial arrays.
 __device__ __forceinline__ int64_t row_index(const View& a, int s, int h, int t) {
@@ -154,10 +168,18 @@ inline int64_t max_prefix_tiles(int S, int G, int rows_per_seq, int rt) {
     return full + (G < S ? G : S);
 }
 
+// Row tiles of 128 that a tensor-core block takes: two as soon as one (sequence, KV head) has them.
+inline int umma_row_tiles(int64_t rows_per_seq) { return rows_per_seq > 128 ? 2 : 1; }
+
 // launchers (host)
+cudaError_t prepare_shared_umma();
+cudaError_t launch_attend_umma(const View& a, int d, cudaStream_t st);
+cudaError_t launch_column_sums_umma(const View& a, int d, cudaStream_t st);
+cudaError_t launch_prefix_umma(const View& a, int d, cudaStream_t st);
 cudaError_t launch_append(const View& a, int dtype, int d, const void* k_t, const int64_t* kts, const void* v_t,
                           const int64_t* vts, const float* w_t, cudaStream_t st);
-cudaError_t launch_attend_simt(const View& a, int dtype, int d, cudaStream_t st);
+// skip_prefix: the prefix's partial results come from another launch
+cudaError_t launch_attend_simt(const View& a, int dtype, int d, bool skip_prefix, cudaStream_t st);
 cudaError_t launch_combine(const View& a, int dtype, int d, cudaStream_t st);
 cudaError_t launch_column_sums_simt(const View& a, int dtype, int d, cudaStream_t st);
 cudaError_t launch_evict(const View& a, int dtype, int d, const int32_t* budget, int recent, int slack,

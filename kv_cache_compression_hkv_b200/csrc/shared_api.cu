@@ -3,6 +3,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "kernels.h"
 #include "shared.cuh"
 
@@ -12,18 +14,22 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr int kMaxSlots = 1 << 24;    // capacity, prefix_capacity
+constexpr int64_t kMaxStride = (int64_t)1 << 37;  // elements
 constexpr int kMaxRows = 1 << 24;     // S * Hkv, and query rows of one (sequence, KV head)
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
-// Row bases and strides on 16-byte boundaries (a negative or zero stride is
-// the caller's: a zero one repeats rows, which only inputs may).
+// Row bases and strides on 16-byte boundaries.
 bool rows_ok(const void* p, const int64_t* st, int64_t es) {
     if (!p || !aligned(p, 16)) return false;
     for (int i = 0; i < 3; ++i)
-        if (st[i] * es % 16 != 0 || st[i] < 0) return false;
+        if (st[i] < 0 || st[i] > kMaxStride || st[i] * es % 16 != 0) return false;
     return true;
+}
+// The same for rows that are held: no dimension of more than one element repeats its rows.
+bool held_ok(const void* p, const int64_t* st, int64_t es, int n0, int n1, int n2) {
+    return rows_ok(p, st, es) && (n0 == 1 || st[0] > 0) && (n1 == 1 || st[1] > 0) && (n2 == 1 || st[2] > 0);
 }
 
 bool cache_ok(const hkv_shared_cache* c) {
@@ -35,14 +41,18 @@ bool cache_ok(const hkv_shared_cache* c) {
     if (c->capacity < 1 || c->capacity > kMaxSlots) return false;
     if (c->num_prefixes < 0 || c->num_prefixes > hkv::shared::MAX_PREFIXES) return false;
     const int64_t es = c->dtype == HKV_DTYPE_F32 ? 4 : 2;
-    if (!rows_ok(c->k, c->k_stride, es) || !rows_ok(c->v, c->v_stride, es)) return false;
-    if (c->k_stride[2] < c->head_dim || c->v_stride[2] < c->head_dim) return false;
+    if (!held_ok(c->k, c->k_stride, es, c->num_seqs, c->num_kv_heads, c->capacity) ||
+        !held_ok(c->v, c->v_stride, es, c->num_seqs, c->num_kv_heads, c->capacity))
+        return false;
+    if (c->capacity > 1 && (c->k_stride[2] < c->head_dim || c->v_stride[2] < c->head_dim)) return false;
     if (!c->len || !aligned(c->len, 4) || !aligned(c->pos, 4) || !aligned(c->weight, 4) || !aligned(c->next_pos, 4) ||
         !aligned(c->status, 4))
         return false;
     if (c->num_prefixes > 0) {
         if (c->prefix_capacity < 1 || c->prefix_capacity > kMaxSlots) return false;
-        if (!rows_ok(c->prefix_k, c->prefix_k_stride, es) || !rows_ok(c->prefix_v, c->prefix_v_stride, es)) return false;
+        if (!held_ok(c->prefix_k, c->prefix_k_stride, es, c->num_prefixes, c->num_kv_heads, c->prefix_capacity) ||
+            !held_ok(c->prefix_v, c->prefix_v_stride, es, c->num_prefixes, c->num_kv_heads, c->prefix_capacity))
+            return false;
         if (!c->prefix_len || !c->prefix_of || !aligned(c->prefix_len, 4) || !aligned(c->prefix_of, 4)) return false;
     }
     return true;
@@ -64,33 +74,74 @@ View view_of(const hkv_shared_cache* c) {
     return a;
 }
 
-// How an attention call is split, and its scratch carved from `base` (sizes
-// alone when base is null).
-size_t plan_attend(View& a, int d, int T, int accumulate, unsigned char* base) {
+// The kernels of an attention call, and how its keys are split over blocks:
+//   fp32       CUDA cores, whatever the rows;
+//   bf16       rows of one (sequence, KV head) up to STREAM_ROWS: own keys on
+//              the CUDA cores, the prefixes' for all their sequences' rows on
+//              the tensor cores; more rows: tensor cores, prefix and own keys
+//              in one pass, cut only where there are too few row tiles.
+struct Plan {
+    bool umma_prefix, umma_rows;
+    size_t bytes;
+};
+
+Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char* base) {
     a.T = T;
     a.accumulate = accumulate;
-    const int64_t rps = (int64_t)a.rep * T, R = (int64_t)a.S * a.H * T;
+    const int64_t rps = (int64_t)a.rep * T, R = (int64_t)a.S * a.H * T, heads = (int64_t)a.S * a.Hk;
     const bool stream = rps <= hkv::shared::STREAM_ROWS;
-    // enough blocks for every SM to hold several, ranges of 64 keys at least
-    auto splits = [&](int64_t tiles, int64_t keys) {
-        int64_t n = (148 * 6 + tiles - 1) / tiles;
-        n = n < (keys + 127) / 128 ? n : (keys + 127) / 128;
+    Plan p;
+    p.umma_rows = dtype == HKV_DTYPE_BF16 && !stream;
+    p.umma_prefix = dtype == HKV_DTYPE_BF16 && stream && a.G > 0;
+    // `want` blocks over `tiles`, at least `least` keys a split
+    auto splits = [&](int64_t want, int64_t tiles, int64_t keys, int64_t least) {
+        int64_t n = (want + tiles - 1) / tiles, most = (keys + least - 1) / least;
+        n = n < most ? n : most;
         return (int)(n < 1 ? 1 : n > hkv::shared::MAX_SPLITS ? hkv::shared::MAX_SPLITS : n);
     };
-    a.no = splits((int64_t)a.S * a.Hk * ((rps + 15) / 16), a.cap);
-    a.np = a.G ? splits(a.Hk * ((int64_t)a.S * rps / 16 + 1), a.pcap) : 0;
+    a.np = 0;
+    a.listed = 0;
+    if (p.umma_rows) {
+        const int nt = hkv::shared::umma_row_tiles(rps);
+        const int64_t items = heads * ((rps + 128 * nt - 1) / (128 * nt));
+        a.listed = 1;
+        a.no = items >= 148 ? 1 : splits(nt == 2 ? 148 : 296, items, (int64_t)a.cap + (a.G ? a.pcap : 0), 256);
+    } else {
+        a.no = splits(148 * 6, heads * ((rps + 15) / 16), a.cap, 128);
+        if (a.G) {
+            const int64_t tiles = (a.S * rps + 127) / 128, groups = a.G < a.S ? a.G : a.S;
+            a.np = p.umma_prefix ? splits(296, a.Hk * (tiles > groups ? tiles : groups), a.pcap, 128)
+                                 : splits(148 * 6, a.Hk * (a.S * rps / 16 + 1), a.pcap, 128);
+        }
+    }
     size_t o = 0;
     auto take = [&](size_t bytes) {
-        unsigned char* p = base ? base + o : nullptr;
+        unsigned char* q = base ? base + o : nullptr;
         o = align_up(o + bytes);
-        return p;
+        return q;
     };
     const size_t ns = a.np + a.no;
-    a.part_ml = (float2*)take(ns * R * sizeof(float2));
-    a.part_o = (float*)take(ns * R * d * sizeof(float));
-    if (accumulate && stream) a.logit = (float*)take((size_t)a.S * a.Hk * rps * a.cap * 4);
+    if (!p.umma_rows || ns > 1) {
+        a.part_ml = (float2*)take(ns * R * sizeof(float2));
+        a.part_o = (float*)take(ns * R * d * sizeof(float));
+    }
+    if (accumulate && stream) a.logit = (float*)take((size_t)heads * rps * a.cap * 4);
     if (accumulate && !stream) a.row_lse = (float*)take((size_t)R * 4);
-    return o;
+    p.bytes = o;
+    return p;
+}
+
+// Raises the kernels' shared-memory limits, once per device.
+cudaError_t prepare() {
+    static std::atomic<unsigned long long> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (ready.load() & bit) return cudaSuccess;
+    e = hkv::shared::prepare_shared_umma();
+    if (e == cudaSuccess && dev < 64) ready.fetch_or(bit);
+    return e;
 }
 
 bool queries_ok(const hkv_shared_cache* c, int T) {
@@ -121,7 +172,7 @@ hkv_status hkv_shared_attend_bytes(const hkv_shared_cache* c, int32_t num_querie
     if (!bytes || !cache_ok(c) || !queries_ok(c, num_queries) || (accumulate != 0 && accumulate != 1))
         return HKV_ERR_INVALID_ARG;
     View a = view_of(c);
-    *bytes = plan_attend(a, c->head_dim, num_queries, accumulate, nullptr);
+    *bytes = plan_attend(a, c->dtype, c->head_dim, num_queries, accumulate, nullptr).bytes;
     return HKV_OK;
 }
 
@@ -132,11 +183,16 @@ hkv_status hkv_shared_attend(const hkv_shared_cache* c, const void* q, const int
         (accumulate != 0 && accumulate != 1) || (accumulate && !c->weight) || !isfinite(scale))
         return HKV_ERR_INVALID_ARG;
     const int64_t es = c->dtype == HKV_DTYPE_F32 ? 4 : 2;
-    if (!rows_ok(q, q_stride, es) || !rows_ok(out, out_stride, es)) return HKV_ERR_INVALID_ARG;
+    if (!held_ok(q, q_stride, es, c->num_seqs, c->num_heads, num_queries) ||
+        !held_ok(out, out_stride, es, c->num_seqs, c->num_heads, num_queries))
+        return HKV_ERR_INVALID_ARG;
     View a = view_of(c);
-    if (scratch_bytes < plan_attend(a, c->head_dim, num_queries, accumulate, nullptr)) return HKV_ERR_CAPACITY;
-    if (!scratch || !aligned(scratch, kAlign)) return HKV_ERR_INVALID_ARG;
-    plan_attend(a, c->head_dim, num_queries, accumulate, (unsigned char*)scratch);
+    const double sc = (scale == 0.0 ? 1.0 / sqrt((double)c->head_dim) : scale) * 1.4426950408889634;
+    if (!(fabs(sc) >= 1e-30 && fabs(sc) <= 1e30)) return HKV_ERR_INVALID_ARG;
+    const Plan p = plan_attend(a, c->dtype, c->head_dim, num_queries, accumulate, nullptr);
+    if (scratch_bytes < p.bytes) return HKV_ERR_CAPACITY;
+    if (p.bytes && (!scratch || !aligned(scratch, kAlign))) return HKV_ERR_INVALID_ARG;
+    plan_attend(a, c->dtype, c->head_dim, num_queries, accumulate, p.bytes ? (unsigned char*)scratch : nullptr);
     a.q = q;
     a.out = out;
     a.lse = lse;
@@ -144,11 +200,17 @@ hkv_status hkv_shared_attend(const hkv_shared_cache* c, const void* q, const int
         a.qs[i] = q_stride[i];
         a.os[i] = out_stride[i];
     }
-    a.qscale = (float)((scale == 0.0 ? 1.0 / sqrt((double)c->head_dim) : scale) * 1.4426950408889634);
+    a.qscale = (float)sc;
     cudaStream_t st = (cudaStream_t)stream;
-    cudaError_t e = hkv::shared::launch_attend_simt(a, c->dtype, c->head_dim, st);
-    if (e == cudaSuccess) e = hkv::shared::launch_combine(a, c->dtype, c->head_dim, st);
-    if (e == cudaSuccess && a.row_lse) e = hkv::shared::launch_column_sums_simt(a, c->dtype, c->head_dim, st);
+    cudaError_t e = prepare();
+    const int d = c->head_dim;
+    if (e == cudaSuccess && p.umma_rows) e = hkv::shared::launch_attend_umma(a, d, st);
+    if (e == cudaSuccess && p.umma_prefix) e = hkv::shared::launch_prefix_umma(a, d, st);
+    if (e == cudaSuccess && !p.umma_rows) e = hkv::shared::launch_attend_simt(a, c->dtype, d, p.umma_prefix, st);
+    if (e == cudaSuccess && a.part_ml) e = hkv::shared::launch_combine(a, c->dtype, d, st);
+    if (e == cudaSuccess && a.row_lse)
+        e = p.umma_rows ? hkv::shared::launch_column_sums_umma(a, d, st)
+                        : hkv::shared::launch_column_sums_simt(a, c->dtype, d, st);
     return cuda_status(e);
 }
 

@@ -1,0 +1,704 @@
+// shared_umma.cu -- shared-prefix attention of many query rows on the
+// 5th-generation tensor cores (tcgen05), bf16.
+//
+// A block takes NT tiles of 128 query rows that share their keys and walks a
+// list of 64-key tiles, prefix first, then own keys up to the rows' causal
+// limit.  Per (row tile X, key tile j):
+//   S = Q_X K_j^T   (M 128, N 64, fp32 in TMEM; two slots a row tile)
+//   P = 2^(c S - m) as bf16 over the first half of S's slot, in TMEM
+//   O_X += P V_j    (A from TMEM, V as the MN-major operand, fp32 in TMEM)
+// Rows: thread = query row = TMEM lane.  m is a reference maximum that is
+// raised (and O rescaled in TMEM) only when a logit passes it by more than
+// 16, so weights stay below 2^16 and bf16's relative rounding is unaffected;
+// the sum l is of the unrounded weights in fp32.
+// Roles: 4 NT softmax warps; a copy warp (TMA into a ring of K and V tiles,
+// in the order K0, K1 V0, K2 V1, ... in which they are used); an MMA warp.
+// S of tile j + 1 is issued before the weights of tile j are waited for, into
+// the other slot, so a row tile's softmax always finds its next logits ready,
+// and with NT = 2 the tensor cores work for one row tile while the other's
+// rows compute.
+#include <math.h>
+
+#include "kernels.h"
+#include "ptx.cuh"
+#include "shared.cuh"
+#include "umma.cuh"
+
+namespace hkv {
+namespace shared {
+
+namespace {
+
+using ptx::mbar_expect_tx;
+using ptx::mbar_init;
+using ptx::mbar_wait;
+using ptx::smem_u32;
+
+constexpr int QT = 128;
+constexpr int UK = 64;  // keys of a tile
+constexpr float RAISE = 16.f;
+constexpr uint64_t WAIT_NS = 2000000000ull;
+
+template <int D, int NT> struct Shape {
+    static constexpr int NS = NT == 2 ? (D == 128 ? 8 : 12) : (D == 128 ? 4 : 6);  // K / V tiles in the ring
+    static constexpr int ROWS = 128 * NT;
+    static constexpr int THREADS = ROWS + 64;
+    static constexpr int COPY_WARP = 4 * NT, MMA_WARP = 4 * NT + 1;
+    static constexpr uint32_t O_COL = 128 * NT;  // S: two slots of 64 columns a row tile
+    static constexpr uint32_t TMEM = NT == 2 ? 512 : 256;
+    static constexpr int Q_BYTES = QT * D * 2, KV_BYTES = UK * D * 2;
+    enum { B_Q, B_FULL, B_FREE = B_FULL + NS, B_S = B_FREE + NS, B_P = B_S + 2 * NT, B_PV = B_P + 2 * NT,
+           B_COUNT = B_PV + 2 * NT };
+    static constexpr int TAIL = B_COUNT * 8 + 16 + 16 + (QT + 1) * 4 + 12;
+    static constexpr int SMEM = 1024 + NT * Q_BYTES + NS * KV_BYTES + TAIL;
+};
+
+}  // namespace
+
+// MODE 0: every key of a row tile of one (sequence, KV head): prefix, then
+//         own, cut in `splits` pieces of the tile list; with one piece the
+//         results are final, else partial (slot = piece).
+// MODE 1: rows of all sequences of a prefix over the prefix's keys, cut in
+//         a.np ranges; partial results (slot = range).
+template <int D, int NT, int MODE>
+__global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
+    attend_umma_kernel(const __grid_constant__ View a, const __grid_constant__ CUtensorMap km,
+                       const __grid_constant__ CUtensorMap vm, const __grid_constant__ CUtensorMap pkm,
+                       const __grid_constant__ CUtensorMap pvm, int row_tiles, int splits) {
+    using C = Shape<D, NT>;
+    extern __shared__ unsigned char raw[];
+    unsigned char* base = reinterpret_cast<unsigned char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    unsigned char* q_s = base;
+    unsigned char* ring = q_s + NT * C::Q_BYTES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(ring + C::NS * C::KV_BYTES);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::B_COUNT);
+    int* res = reinterpret_cast<int*>(tmem_slot + 4);
+    int* list = res + 4;
+    constexpr int NSUB = D / 64;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rps = a.rep * a.T;
+    const int64_t R = (int64_t)a.S * a.H * a.T;
+
+    // what this block works on
+    int hk, s = 0, g, first, rows, piece, p_tiles, t0, t1, p_len, n_own = 0, p_lo = 0;
+    if constexpr (MODE == 0) {
+        // longest row tiles (the last queries) first
+        const int b = blockIdx.x, per = a.S * a.Hk * splits;
+        const int tile = row_tiles - 1 - b / per;
+        piece = b % per % splits;
+        const int sh = b % per / splits;
+        s = sh / a.Hk;
+        hk = sh % a.Hk;
+        first = tile * C::ROWS;
+        rows = min(C::ROWS, rps - first);
+        g = prefix_of(a, s);
+        p_len = prefix_len(a, g);
+        n_own = own_len(a, s, hk);
+        p_tiles = (p_len + UK - 1) / UK;
+        const int all = p_tiles + (n_own + UK - 1) / UK;
+        const int per_piece = (all + splits - 1) / splits;
+        t0 = min(all, piece * per_piece);
+        t1 = min(all, t0 + per_piece);
+        if (splits > 1 && t0 >= t1) return;  // combine_kernel knows
+    } else {
+        const int b = blockIdx.x;
+        piece = b % a.np;
+        hk = b / a.np % a.Hk;
+        if (!find_prefix_tile(a, b / a.np / a.Hk, C::ROWS, g, first, rows, reinterpret_cast<int*>(ring), res, list))
+            return;
+        p_len = prefix_len(a, g);
+        int lo, hi;
+        split_range(p_len, a.np, piece, lo, hi);
+        if (lo >= hi) return;
+        p_lo = lo;
+        p_len = hi;
+        ptx::fence_proxy_async();  // (the ring held the counts just now)
+        t0 = 0;
+        t1 = p_tiles = (hi - lo + UK - 1) / UK;
+    }
+    // key tiles of each row tile within [t0, t1)
+    int nx[NT], n = 0;
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+        const int last = min(rows, (x + 1) * QT) - 1;
+        nx[x] = 0;
+        if (last >= x * QT) {
+            const int vis = MODE == 0 ? p_tiles + (own_limit(a, n_own, first + last) + UK - 1) / UK : t1;
+            nx[x] = max(0, min(vis, t1) - t0);
+        }
+        n = max(n, nx[x]);
+    }
+
+    if (warp == 0) tc::alloc(tmem_slot, C::TMEM);
+    if (tid == 0) {
+        for (int i = 0; i < C::B_COUNT; ++i)
+            mbar_init(bars + i, i == C::B_Q ? 4 * NT : (i >= C::B_P && i < C::B_PV) ? 4 : 1);
+        ptx::fence_mbar_init();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool fail = false;
+
+    // list tile t0 + j: where its keys start, and how many of 64 are keys
+    auto tile_at = [&](int j, bool& pre, int& k0, int& valid) {
+        const int t = t0 + j;
+        pre = t < p_tiles;
+        k0 = pre ? p_lo + t * UK : (t - p_tiles) * UK;
+        valid = min(UK, (pre ? p_len : n_own) - k0);
+    };
+    // ring index of K_j and V_j
+    auto k_idx = [](int j) { return j == 0 ? 0 : 2 * j - 1; };
+    auto v_idx = [&](int j) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; };
+
+    if (warp == C::COPY_WARP) {
+        if (lane == 0) {
+            int issued = 0;
+            for (int i = 0; i < 2 * n; ++i) {
+                const int slot = i % C::NS, use = i / C::NS;
+                if (use > 0 && !mbar_wait(bars + C::B_FREE + slot, (use - 1) & 1, WAIT_NS)) { fail = true; break; }
+                // i = 0: K0; odd i < 2n - 1: K_{(i+1)/2}; even: V_{i/2 - 1}; 2n - 1: V_{n-1}
+                const bool is_k = i == 0 || ((i & 1) && i < 2 * n - 1);
+                const int j = i == 0 ? 0 : is_k ? (i + 1) / 2 : i == 2 * n - 1 ? n - 1 : i / 2 - 1;
+                bool pre;
+                int k0, valid;
+                tile_at(j, pre, k0, valid);
+                const CUtensorMap* m = is_k ? (pre ? &pkm : &km) : (pre ? &pvm : &vm);
+                mbar_expect_tx(bars + C::B_FULL + slot, C::KV_BYTES);
+                for (int sub = 0; sub < NSUB; ++sub)
+                    tc::tma_load_4d(ring + slot * C::KV_BYTES + sub * UK * 128, m, bars + C::B_FULL + slot, sub * 64, k0,
+                                    hk, pre ? g : s);
+                issued = i + 1;
+            }
+            if (fail)  // the block's own copies land before its shared memory goes
+                for (int i = max(0, issued - C::NS); i < issued; ++i)
+                    mbar_wait(bars + C::B_FULL + i % C::NS, (i / C::NS) & 1, WAIT_NS);
+        }
+    } else if (warp == C::MMA_WARP) {
+        // The whole warp waits; lane 0 issues.
+        constexpr uint32_t IS = tc::idesc_bf16(UK, false), IO = tc::idesc_bf16(D, true);
+        auto ok = [&](bool w) { return !__any_sync(FULL_MASK, !w); };
+        auto full = [&](int i) { return ok(mbar_wait(bars + C::B_FULL + i % C::NS, (i / C::NS) & 1, WAIT_NS)); };
+        auto issue_s = [&](int x, int j) {
+            if (lane == 0) {
+                const uint32_t kb = smem_u32(ring + (k_idx(j) % C::NS) * C::KV_BYTES), qb = smem_u32(q_s + x * C::Q_BYTES);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc::mma_ss(tmem + x * 128 + (j & 1) * UK, tc::sw128_desc(qb + (kk / 4) * (QT * 128) + (kk % 4) * 32, 16, 1024),
+                               tc::sw128_desc(kb + (kk / 4) * (UK * 128) + (kk % 4) * 32, 16, 1024), IS, kk > 0);
+                tc::commit(bars + C::B_S + 2 * x + (j & 1));
+            }
+            __syncwarp();
+        };
+        int s_done[NT], pv_done[NT];
+#pragma unroll
+        for (int x = 0; x < NT; ++x) s_done[x] = pv_done[x] = -1;
+        if (n > 0) {
+            if (!ok(mbar_wait(bars + C::B_Q, 0, WAIT_NS)) || !full(0)) fail = true;
+            tc::fence_after();
+            if (!fail) {
+#pragma unroll
+                for (int x = 0; x < NT; ++x)
+                    if (nx[x] > 0) { issue_s(x, 0); s_done[x] = 0; }
+                if (lane == 0) tc::commit(bars + C::B_FREE + 0);
+            }
+        }
+        for (int j = 0; j < n && !fail; ++j) {
+            const bool more = j + 1 < n;
+            const int vi = v_idx(j);
+            bool v_ready = false;
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                if (fail) break;
+                if (j + 1 < nx[x]) {
+                    // slot (j + 1) % 2 still holds P_{j-1} until its product is done
+                    if (!full(k_idx(j + 1)) ||
+                        (j >= 1 && !ok(mbar_wait(bars + C::B_PV + 2 * x + ((j - 1) & 1), ((j - 1) >> 1) & 1, WAIT_NS)))) {
+                        fail = true;
+                        break;
+                    }
+                    tc::fence_after();
+                    issue_s(x, j + 1);
+                    s_done[x] = j + 1;
+                }
+                if (x == NT - 1 && more && lane == 0) tc::commit(bars + C::B_FREE + k_idx(j + 1) % C::NS);
+                if (j < nx[x]) {
+                    if (!v_ready) {
+                        if (!full(vi)) { fail = true; break; }
+                        bool pre;
+                        int k0, valid;
+                        tile_at(j, pre, k0, valid);
+                        if (valid < UK) {
+                            // rows past the last key hold whatever the memory held: 0 x NaN must not be formed
+                            unsigned char* vt = ring + (vi % C::NS) * C::KV_BYTES;
+                            for (int e = lane; e < (UK - valid) * 8 * NSUB; e += 32) {
+                                const int sub = e / ((UK - valid) * 8), w = e % ((UK - valid) * 8);
+                                *reinterpret_cast<uint4*>(vt + sub * UK * 128 + valid * 128 + w * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                            ptx::fence_proxy_async();
+                            __syncwarp();
+                        }
+                        v_ready = true;
+                    }
+                    if (!ok(mbar_wait(bars + C::B_P + 2 * x + (j & 1), (j >> 1) & 1, WAIT_NS))) { fail = true; break; }
+                    tc::fence_after();
+                    if (lane == 0) {
+                        const uint32_t vb = smem_u32(ring + (vi % C::NS) * C::KV_BYTES);
+#pragma unroll
+                        for (int kk = 0; kk < UK / 16; ++kk)
+                            tc::mma_ts(tmem + C::O_COL + x * D, tmem + x * 128 + (j & 1) * UK + kk * 8,
+                                       tc::sw128_desc(vb + kk * 16 * 128, UK * 128, 1024), IO, (j > 0 || kk > 0));
+                        tc::commit(bars + C::B_PV + 2 * x + (j & 1));
+                    }
+                    __syncwarp();
+                    pv_done[x] = j;
+                }
+            }
+            if (!fail && lane == 0) tc::commit(bars + C::B_FREE + vi % C::NS);
+        }
+        // The tensor cores finish what was issued before TMEM is freed, and
+        // the last commits' arrivals land before the shared memory goes.
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            if (s_done[x] > pv_done[x]) mbar_wait(bars + C::B_S + 2 * x + (s_done[x] & 1), (s_done[x] >> 1) & 1, WAIT_NS);
+            if (pv_done[x] >= 0)
+                mbar_wait(bars + C::B_PV + 2 * x + (pv_done[x] & 1), (pv_done[x] >> 1) & 1, WAIT_NS);
+        }
+        if (!fail && n > 0) {
+            const int vi = v_idx(n - 1);
+            mbar_wait(bars + C::B_FREE + vi % C::NS, (vi / C::NS) & 1, WAIT_NS);
+        }
+    } else {
+        // --- rows ----------------------------------------------------------
+        const int x = warp >> 2, r = tid;  // row tile; row of the block
+        const bool live = r < rows;
+        int sq = s, i = 0;
+        if (live) {
+            if constexpr (MODE == 0) {
+                i = first + r;
+            } else {
+                const int f = first + r;
+                sq = list[f / rps - first / rps];
+                i = f % rps;
+            }
+        }
+        const int h = hk * a.rep + i % a.rep, t = i / a.rep;
+        {
+            // Q into the swizzled tile (negated where the scale is negative:
+            // exact, and the reference maximum is then of the scaled logits)
+            const uint32_t flip = a.qscale < 0.f ? 0x80008000u : 0u;
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + sq * a.qs[0] +
+                                                              h * a.qs[1] + t * a.qs[2]);
+            const int row = r & 127;
+            unsigned char* dst = q_s + x * C::Q_BYTES + row * 128;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                uint4 w = live ? src[c] : make_uint4(0, 0, 0, 0);
+                w.x ^= flip; w.y ^= flip; w.z ^= flip; w.w ^= flip;
+                *reinterpret_cast<uint4*>(dst + (c / 8) * (QT * 128) + (((c & 7) ^ (row & 7)) << 4)) = w;
+            }
+            ptx::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) tc::arrive(bars + C::B_Q);
+        }
+        const float c = fabsf(a.qscale);
+        const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t t_s = t_lane + x * 128, t_o = t_lane + C::O_COL + x * D;
+        // own keys this row sees; rows past the last one compute on zeros
+        const int lim = MODE == 0 ? (live ? own_limit(a, n_own, i) : 0x7fffffff) : 0;
+        const int lim_warp = __shfl_sync(FULL_MASK, lim, 0);  // the least of the warp's
+        const int nt = NT == 2 ? (x == 0 ? nx[0] : nx[NT - 1]) : nx[0];
+        float m = -INFINITY, l = 0.f;  // reference maximum (times c) and sum
+        // every branch around the warp-wide TMEM accesses is taken by the whole warp
+        for (int j = 0; j < nt; ++j) {
+            const uint32_t ts = t_s + (j & 1) * UK;
+            if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_S + 2 * x + (j & 1), (j >> 1) & 1, WAIT_NS))) { fail = true; break; }
+            tc::fence_after();
+            uint32_t sr[2][32];
+            tc::ld32(ts, sr[0]);
+            tc::ld32(ts + 32, sr[1]);
+            bool pre;
+            int k0, valid;
+            tile_at(j, pre, k0, valid);
+            tc::ld_wait();
+            if (valid < UK || (!pre && k0 + UK > lim_warp)) {
+                const int end = pre ? valid : min(valid, lim - k0);
+#pragma unroll
+                for (int u = 0; u < UK; ++u)
+                    if (u >= end) sr[u >> 5][u & 31] = 0xff800000u;  // -inf
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int u = 0; u < UK; ++u) mx[u & 3] = fmaxf(mx[u & 3], __uint_as_float(sr[u >> 5][u & 31]));
+            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+            if (__any_sync(FULL_MASK, mt > m + RAISE)) {
+                const float mn = fmaxf(m, mt);
+                const float alpha = mn == -INFINITY ? 1.f : exp2f(m - mn);
+                if (j > 0) {
+                    const int jp = j - 1;
+                    if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_PV + 2 * x + (jp & 1), (jp >> 1) & 1, WAIT_NS))) {
+                        fail = true;
+                        break;
+                    }
+                    tc::fence_after();
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[32];
+                        tc::ld32(t_o + c0, o);
+                        tc::ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tc::st32(t_o + c0, o);
+                    }
+                    tc::st_wait();
+                }
+                l *= alpha;
+                m = mn;
+            }
+            const float mb = m == -INFINITY ? 0.f : m;
+            uint32_t w[32];
+            float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int u = 0; u < 32; ++u) {
+                const float p0 = tc::ex2(fmaf(__uint_as_float(sr[(2 * u) >> 5][(2 * u) & 31]), c, -mb));
+                const float p1 = tc::ex2(fmaf(__uint_as_float(sr[(2 * u + 1) >> 5][(2 * u + 1) & 31]), c, -mb));
+                ls[u & 3] += p0 + p1;
+                __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+                w[u] = *reinterpret_cast<uint32_t*>(&h2);
+            }
+            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+            tc::st32(ts, w);
+            tc::st_wait();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::arrive(bars + C::B_P + 2 * x + (j & 1));
+        }
+        if (!fail && nt > 0) {
+            const int jl = nt - 1;
+            if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_PV + 2 * x + (jl & 1), (jl >> 1) & 1, WAIT_NS))) fail = true;
+        }
+        if (!fail) {
+            tc::fence_after();
+            const int64_t row = live ? row_index(a, sq, h, t) : 0;
+            const bool some = nt > 0 && !(m == -INFINITY && l == 0.f);
+            const bool final = MODE == 0 && splits == 1;
+            const float f = !final ? 1.f : some ? 1.f / l : 0.f;
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t o[32];
+                if (nt > 0) {
+                    tc::ld32(t_o + c0, o);
+                    tc::ld_wait();
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = some ? __float_as_uint(__uint_as_float(o[e]) * f) : 0u;
+                if (!live) continue;
+                if (final) {
+                    __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) + sq * a.os[0] + h * a.os[1] + t * a.os[2] + c0;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * u]), __uint_as_float(o[e + 2 * u + 1]));
+                            w[u] = *reinterpret_cast<uint32_t*>(&h2);
+                        }
+                        *reinterpret_cast<uint4*>(orow + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+                    uint4* po = reinterpret_cast<uint4*>(a.part_o + (piece * R + row) * D + c0);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) po[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                }
+            }
+            if (live) {
+                if (final) {
+                    const float l2 = some ? m + log2f(l) : -INFINITY;
+                    if (a.lse) a.lse[row] = l2 * 0.6931471805599453f;
+                    if (a.row_lse) a.row_lse[row] = l2;
+                } else {
+                    a.part_ml[piece * R + row] = make_float2(l != l && m == -INFINITY ? 0.f : m, l);
+                }
+            }
+        }
+    }
+    tc::fence_before();
+    if (__syncthreads_or(fail)) {
+        if (tid == 0 && a.status && atomicCAS(a.status, 0, HKV_ERR_TIMEOUT) == 0) atomicExch(a.status + 1, (int)blockIdx.x);
+    }
+    tc::fence_after();
+    if (warp == 0) tc::dealloc(tmem, C::TMEM);
+}
+
+// ---------------------------------------------------------------------------
+// accumulated weights of many rows
+// ---------------------------------------------------------------------------
+
+namespace {
+
+template <int D> struct SumShape {
+    static constexpr int KB = 128;      // keys of a block (MMA M)
+    static constexpr int QN = 64;       // queries of a tile (MMA N)
+    static constexpr int NS = 4;        // query tiles in flight: shared memory and S slots in TMEM alike
+    static constexpr int THREADS = 256 + 64, COPY_WARP = 8, MMA_WARP = 9;
+    static constexpr uint32_t TMEM = NS * QN;
+    static constexpr int K_BYTES = KB * D * 2, Q_BYTES = QN * D * 2;
+    enum { B_K, B_FULL, B_FREE = B_FULL + NS, B_S = B_FREE + NS, B_COUNT = B_S + NS };
+    static constexpr int SMEM = 1024 + K_BYTES + NS * Q_BYTES + NS * QN * 4 + KB * 4 + B_COUNT * 8 + 16;
+};
+
+}  // namespace
+
+// weight[key] += sum over rows of 2^(c q.k - lse2[row]), the log2 of the row
+// sums being known: the logits once more, keys on the M side, so that a
+// thread owns a key (TMEM lane) and sums along its own columns.  One block
+// per (sequence, KV head, 128 keys) walks 64-query tiles of each query head
+// in turn, from the first query that sees its first key on; two groups of
+// four warps take every other tile.  A row that is not to be counted has
+// -lse2 = -inf there.
+template <int D>
+__global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
+    column_sums_umma_kernel(const __grid_constant__ View a, const __grid_constant__ CUtensorMap km,
+                            const __grid_constant__ CUtensorMap qm) {
+    using C = SumShape<D>;
+    extern __shared__ unsigned char raw[];
+    unsigned char* k_s = reinterpret_cast<unsigned char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    unsigned char* q_s = k_s + C::K_BYTES;
+    float* nl_s = reinterpret_cast<float*>(q_s + C::NS * C::Q_BYTES);  // [NS][QN]
+    float* half = nl_s + C::NS * C::QN;                                // [KB]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(half + C::KB);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::B_COUNT);
+    constexpr int NSUB = D / 64;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the first keys, which the most queries see, first
+    const int heads = a.S * a.Hk, sh = blockIdx.x % heads, k0 = blockIdx.x / heads * C::KB;
+    const int s = sh / a.Hk, hk = sh % a.Hk;
+    const int n = own_len(a, s, hk);
+    if (k0 >= n) return;
+    // key j is seen by the queries t >= j - (n - T)
+    const int shift = n - a.T;
+    const int tile0 = max(0, k0 - shift) / C::QN, per_head = (a.T + C::QN - 1) / C::QN - tile0;
+    const int tiles = per_head * a.rep;
+
+    if (warp == 0) tc::alloc(tmem_slot, C::TMEM);
+    if (tid == 0) {
+        for (int i = 0; i < C::B_COUNT; ++i) mbar_init(bars + i, i >= C::B_FREE && i < C::B_S ? 5 : 1);
+        ptx::fence_mbar_init();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool fail = false;
+    float total = 0.f;
+
+    if (warp == C::COPY_WARP) {
+        if (lane == 0) {
+            mbar_expect_tx(bars + C::B_K, C::K_BYTES);
+            for (int sub = 0; sub < NSUB; ++sub) tc::tma_load_4d(k_s + sub * C::KB * 128, &km, bars + C::B_K, sub * 64, k0, hk, s);
+        }
+        int issued = 0;
+        for (int j = 0; j < tiles; ++j) {
+            const int slot = j % C::NS, use = j / C::NS;
+            if (use > 0 && __any_sync(FULL_MASK, !mbar_wait(bars + C::B_FREE + slot, (use - 1) & 1, WAIT_NS))) { fail = true; break; }
+            const int h = hk * a.rep + j / per_head, t0 = (tile0 + j % per_head) * C::QN;
+            const float* src = a.row_lse + row_index(a, s, h, 0);
+#pragma unroll
+            for (int u = 0; u < C::QN; u += 32) {
+                const int t = t0 + u + lane;
+                const float e = t < a.T ? src[t] : -INFINITY;
+                nl_s[slot * C::QN + u + lane] = e == -INFINITY ? -INFINITY : -e;
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_expect_tx(bars + C::B_FULL + slot, C::Q_BYTES);
+                for (int sub = 0; sub < NSUB; ++sub)
+                    tc::tma_load_4d(q_s + slot * C::Q_BYTES + sub * C::QN * 128, &qm, bars + C::B_FULL + slot, sub * 64, t0, h, s);
+            }
+            issued = j + 1;
+        }
+        if (fail && lane == 0) {
+            mbar_wait(bars + C::B_K, 0, WAIT_NS);
+            for (int j = max(0, issued - C::NS); j < issued; ++j)
+                mbar_wait(bars + C::B_FULL + j % C::NS, (j / C::NS) & 1, WAIT_NS);
+        }
+    } else if (warp == C::MMA_WARP) {
+        if (lane == 0) {
+            constexpr uint32_t IS = tc::idesc_bf16(C::QN, false);
+            int done = -1;
+            if (!mbar_wait(bars + C::B_K, 0, WAIT_NS)) fail = true;
+            for (int j = 0; j < tiles && !fail; ++j) {
+                const int slot = j % C::NS;
+                if (!mbar_wait(bars + C::B_FULL + slot, (j / C::NS) & 1, WAIT_NS)) { fail = true; break; }
+                tc::fence_after();
+                const uint32_t kb = smem_u32(k_s), qb = smem_u32(q_s + slot * C::Q_BYTES);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc::mma_ss(tmem + slot * C::QN, tc::sw128_desc(kb + (kk / 4) * (C::KB * 128) + (kk % 4) * 32, 16, 1024),
+                               tc::sw128_desc(qb + (kk / 4) * (C::QN * 128) + (kk % 4) * 32, 16, 1024), IS, kk > 0);
+                tc::commit(bars + C::B_S + slot);
+                tc::commit(bars + C::B_FREE + slot);
+                done = j;
+            }
+            if (done >= 0) {
+                mbar_wait(bars + C::B_S + done % C::NS, (done / C::NS) & 1, WAIT_NS);
+                // (the row warps' arrivals complete the other barrier's phase)
+                if (!fail) mbar_wait(bars + C::B_FREE + done % C::NS, (done / C::NS) & 1, WAIT_NS);
+            }
+        }
+    } else {
+        const int grp = warp >> 2, key = k0 + (tid & 127);
+        const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const float c = a.qscale;
+        const int last = __shfl_sync(FULL_MASK, key, 31) - shift;  // first query that the warp's last key is seen by
+        for (int j = grp; j < tiles; j += 2) {
+            const int slot = j % C::NS, t0 = (tile0 + j % per_head) * C::QN;
+            if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_S + slot, (j / C::NS) & 1, WAIT_NS))) { fail = true; break; }
+            tc::fence_after();
+            uint32_t sr[2][32];
+            tc::ld32(t_lane + slot * C::QN, sr[0]);
+            tc::ld32(t_lane + slot * C::QN + 32, sr[1]);
+            const float* nl = nl_s + slot * C::QN;
+            tc::ld_wait();
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            if (t0 >= last) {
+#pragma unroll
+                for (int u = 0; u < C::QN; u += 4) {
+                    const float4 e = *reinterpret_cast<const float4*>(nl + u);
+                    acc[0] += tc::ex2(fmaf(__uint_as_float(sr[u >> 5][u & 31]), c, e.x));
+                    acc[1] += tc::ex2(fmaf(__uint_as_float(sr[u >> 5][(u & 31) + 1]), c, e.y));
+                    acc[2] += tc::ex2(fmaf(__uint_as_float(sr[u >> 5][(u & 31) + 2]), c, e.z));
+                    acc[3] += tc::ex2(fmaf(__uint_as_float(sr[u >> 5][(u & 31) + 3]), c, e.w));
+                }
+            } else {
+                const int from = key - shift - t0;  // columns before it do not see the key
+#pragma unroll
+                for (int u = 0; u < C::QN; ++u) {
+                    const float p = tc::ex2(fmaf(__uint_as_float(sr[u >> 5][u & 31]), c, nl[u]));
+                    acc[u & 3] += u >= from ? p : 0.f;
+                }
+            }
+            total += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::arrive(bars + C::B_FREE + slot);
+        }
+        if (grp == 1) half[tid & 127] = total;
+    }
+    tc::fence_before();
+    if (__syncthreads_or(fail)) {
+        if (tid == 0 && a.status && atomicCAS(a.status, 0, HKV_ERR_TIMEOUT) == 0) atomicExch(a.status + 1, (int)blockIdx.x);
+    } else if (tid < C::KB && k0 + tid < n) {
+        a.weight[(int64_t)sh * a.cap + k0 + tid] += total + half[tid];
+    }
+    tc::fence_after();
+    if (warp == 0) tc::dealloc(tmem, C::TMEM);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
+
+// bf16 rows [n2][n1][n0] of d elements at strides st (elements: outermost,
+// middle, row); boxes of 64 columns x box rows, 128-byte swizzle.
+static bool make_map(CUtensorMap* m, const void* ptr, int d, int n0, int n1, int n2, const int64_t* st, int box) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    // a dimension of one element may come with any stride: give it a lawful one
+    auto bytes = [&](int n, int64_t e) { return (cuuint64_t)(n == 1 ? (int64_t)d * 2 : e * 2); };
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)n0, (cuuint64_t)n1, (cuuint64_t)n2};
+    cuuint64_t strides[3] = {bytes(n0, st[2]), bytes(n1, st[1]), bytes(n2, st[0])};
+    cuuint32_t bx[4] = {64, (cuuint32_t)box, 1, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, bx, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NT, int MODE>
+static cudaError_t go(const View& a, const CUtensorMap* m, int64_t blocks, int row_tiles, int splits, cudaStream_t st) {
+    using C = Shape<D, NT>;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    attend_umma_kernel<D, NT, MODE><<<(int)blocks, C::THREADS, C::SMEM, st>>>(a, m[0], m[1], m[2], m[3], row_tiles, splits);
+    return cudaGetLastError();
+}
+
+static bool cache_maps(const View& a, int d, CUtensorMap* m) {
+    if (!make_map(m, a.k, d, a.cap, a.Hk, a.S, a.ks, UK) || !make_map(m + 1, a.v, d, a.cap, a.Hk, a.S, a.vs, UK)) return false;
+    if (a.G == 0) {
+        m[2] = m[0];
+        m[3] = m[1];
+        return true;
+    }
+    return make_map(m + 2, a.pk, d, a.pcap, a.Hk, a.G, a.pks, UK) && make_map(m + 3, a.pv, d, a.pcap, a.Hk, a.G, a.pvs, UK);
+}
+
+cudaError_t launch_attend_umma(const View& a, int d, cudaStream_t st) {
+    CUtensorMap m[4];
+    if (!cache_maps(a, d, m)) return cudaErrorInvalidValue;
+    const int rps = a.rep * a.T, nt = umma_row_tiles(rps), splits = a.no;
+    const int tiles = (rps + QT * nt - 1) / (QT * nt);
+    const int64_t blocks = (int64_t)tiles * a.S * a.Hk * splits;
+    if (d == 128)
+        return nt == 2 ? go<128, 2, 0>(a, m, blocks, tiles, splits, st) : go<128, 1, 0>(a, m, blocks, tiles, splits, st);
+    return nt == 2 ? go<64, 2, 0>(a, m, blocks, tiles, splits, st) : go<64, 1, 0>(a, m, blocks, tiles, splits, st);
+}
+
+cudaError_t launch_prefix_umma(const View& a, int d, cudaStream_t st) {
+    CUtensorMap m[4];
+    if (!cache_maps(a, d, m)) return cudaErrorInvalidValue;
+    const int rps = a.rep * a.T;
+    const int64_t tiles = max_prefix_tiles(a.S, a.G, rps, QT);
+    const int64_t blocks = tiles * a.Hk * a.np;
+    return d == 128 ? go<128, 1, 1>(a, m, blocks, (int)tiles, 1, st) : go<64, 1, 1>(a, m, blocks, (int)tiles, 1, st);
+}
+
+cudaError_t launch_column_sums_umma(const View& a, int d, cudaStream_t st) {
+    CUtensorMap km, qm;
+    if (!make_map(&km, a.k, d, a.cap, a.Hk, a.S, a.ks, 128) || !make_map(&qm, a.q, d, a.T, a.H, a.S, a.qs, 64))
+        return cudaErrorInvalidValue;
+    const int64_t blocks = (int64_t)a.S * a.Hk * ((a.cap + 127) / 128);
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    if (d == 128)
+        column_sums_umma_kernel<128><<<(int)blocks, SumShape<128>::THREADS, SumShape<128>::SMEM, st>>>(a, km, qm);
+    else
+        column_sums_umma_kernel<64><<<(int)blocks, SumShape<64>::THREADS, SumShape<64>::SMEM, st>>>(a, km, qm);
+    return cudaGetLastError();
+}
+
+cudaError_t prepare_shared_umma() {
+    cudaError_t e = cudaSuccess;
+    auto set = [&](auto kernel, int smem) {
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    };
+    set(attend_umma_kernel<128, 2, 0>, Shape<128, 2>::SMEM);
+    set(attend_umma_kernel<128, 1, 0>, Shape<128, 1>::SMEM);
+    set(attend_umma_kernel<128, 1, 1>, Shape<128, 1>::SMEM);
+    set(attend_umma_kernel<64, 2, 0>, Shape<64, 2>::SMEM);
+    set(attend_umma_kernel<64, 1, 0>, Shape<64, 1>::SMEM);
+    set(attend_umma_kernel<64, 1, 1>, Shape<64, 1>::SMEM);
+    set(column_sums_umma_kernel<128>, SumShape<128>::SMEM);
+    set(column_sums_umma_kernel<64>, SumShape<64>::SMEM);
+    return e;
+}
+
+}  // namespace shared
+}  // namespace hkv

@@ -187,6 +187,8 @@ class SharedPrefixCache:
         T = q.shape[2]
         if T < 1 or T > c.capacity:
             raise ValueError("q: between 1 token and the capacity")
+        if 0 in q.stride():
+            raise ValueError("q: no repeated rows")
         if scale is not None and not (scale != 0 and abs(scale) < float("inf")):
             raise ValueError("scale: a finite number other than 0")
         if out is not None:

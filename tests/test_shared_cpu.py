@@ -41,7 +41,7 @@ BAD = [dict(dtype=2), dict(head_dim=96), dict(num_seqs=0), dict(num_heads=7), di
        dict(prefix_capacity=0), dict(prefix_capacity=1 << 25), dict(k=None), dict(v=0x10008), dict(len=None),
        dict(len=0x10002), dict(prefix_k=None), dict(prefix_v=0x10001), dict(prefix_len=None), dict(prefix_of=None),
        dict(k_stride=ST(0, 64, 4)), dict(v_stride=ST(12288, 6144, 60)), dict(k_stride=ST(12288, -6144, 64)),
-       dict(prefix_k_stride=ST(5120, 2560, 68 + 1)), dict(pos=0x10002), dict(status=0x10001),
+       dict(prefix_k_stride=ST(5120, 2560, 68 + 1)), dict(v_stride=ST(12288, 0, 64)), dict(prefix_v_stride=ST(0, 2560, 64)), dict(pos=0x10002), dict(status=0x10001),
        dict(num_seqs=1 << 30)]
 
 
@@ -73,7 +73,7 @@ def test_bad_arguments_refused():
     ok = dict(q=0x1000, qs=st, out=0x2000, os=st, lse=None, T=1, scale=0.0, acc=1, ws=0x10000, n=1 << 40)
     for kw, code in ((dict(q=None), 1), (dict(q=0x1004), 1), (dict(qs=odd), 1), (dict(qs=None), 1), (dict(out=None), 1),
                      (dict(os=odd), 1), (dict(lse=0x1001), 1), (dict(T=0), 1), (dict(T=97), 1),
-                     (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(acc=2), 1), (dict(ws=None), 1),
+                     (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(scale=1e-40), 1), (dict(scale=-1e40), 1), (dict(acc=2), 1), (dict(ws=None), 1),
                      (dict(ws=0x10010), 1), (dict(n=16), 3)):
         a = {**ok, **kw}
         assert L.hkv_shared_attend(r, a["q"], a["qs"], a["out"], a["os"], a["lse"], a["T"], a["scale"], a["acc"],
