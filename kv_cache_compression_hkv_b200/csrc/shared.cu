@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(View a, int ptiles, in
         for (int c = 0; c < V; ++c) o[u][c] = 0.f;
         lim[u] = r >= rows ? 0 : (is_prefix ? hi : own_limit(a, n_own, first + r));
         lrow[u] = !is_prefix && a.logit && r < rows
-                      ? a.logit + ((int64_t)(s * a.Hk + hk) * rps + first + r) * a.cap : nullptr;
+                      ? a.logit + ((int64_t)(s * a.Hk + hk) * rps + first + r) * a.lcap : nullptr;
     }
     int stop = hi;
     if (!is_prefix) stop = min(hi, own_limit(a, n_own, first + rows - 1));
@@ -301,11 +301,12 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(View a, int ptiles, in
 // output.  Blocks beyond: one (sequence, KV head, 256 slots) each, weight +=
 // the kept logits' weights over the rows, in row order.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) combine_kernel(View a, int row_blocks) {
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ View a, int row_blocks) {
     __shared__ float2 ml_s[STREAM_ROWS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t R = (int64_t)a.S * a.H * a.T;
     const int ns = a.np + a.no;
+    ptx::grid_dep_wait();
     auto row_max_sum = [&](int64_t row, int pk, int ok, float& M, float& L) {
         M = -INFINITY;
         for (int j = lane; j < ns; j += 32)
@@ -370,11 +371,11 @@ __global__ void __launch_bounds__(256) combine_kernel(View a, int row_blocks) {
     __syncthreads();
     const int j = j0 + threadIdx.x;
     if (j >= n) return;
-    const float* lg = a.logit + (int64_t)sh * rps * a.cap + j;
+    const float* lg = a.logit + (int64_t)sh * rps * a.lcap + j;
     float sum = 0.f;
     for (int i = 0; i < rps; ++i) {
         const float2 x = ml_s[i];
-        if (x.x != -INFINITY) sum += exp2f(lg[(int64_t)i * a.cap] - x.x) * x.y;
+        if (x.x != -INFINITY) sum += exp2f(lg[(int64_t)i * a.lcap] - x.x) * x.y;
     }
     a.weight[(int64_t)sh * a.cap + j] += sum;
 }
@@ -467,9 +468,9 @@ template <typename F> cudaError_t by_type(int dtype, int d, F&& f) {
 
 }  // namespace
 
-cudaError_t launch_attend_simt(const View& a, int dtype, int d, bool skip_prefix, cudaStream_t st) {
+cudaError_t launch_attend_simt(const View& a, int dtype, int d, cudaStream_t st) {
     const int rps = a.rep * a.T, otiles = (rps + RT - 1) / RT;
-    const int64_t ptiles = a.np && !skip_prefix ? max_prefix_tiles(a.S, a.G, rps, RT) : 0;
+    const int64_t ptiles = a.np ? max_prefix_tiles(a.S, a.G, rps, RT) : 0;
     const int64_t blocks = ptiles * a.Hk * a.np + (int64_t)a.S * a.Hk * otiles * a.no;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     return by_type(dtype, d, [&](auto tag, auto dim) {
@@ -481,14 +482,22 @@ cudaError_t launch_attend_simt(const View& a, int dtype, int d, bool skip_prefix
     });
 }
 
-cudaError_t launch_combine(const View& a, int dtype, int d, cudaStream_t st) {
+cudaError_t launch_combine(const View& a, int dtype, int d, bool dependent, cudaStream_t st) {
     const int64_t R = (int64_t)a.S * a.H * a.T, rb = (R + 7) / 8;
     const int64_t blocks = rb + (a.logit ? (int64_t)a.S * a.Hk * ((a.cap + 255) / 256) : 0);
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     return by_type(dtype, d, [&](auto tag, auto dim) {
         using E = decltype(tag);
-        combine_kernel<E, decltype(dim)::value><<<(int)blocks, 256, 0, st>>>(a, (int)rb);
-        return cudaGetLastError();
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)blocks);
+        cfg.blockDim = dim3(256);
+        cfg.stream = st;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = dependent ? 1 : 0;
+        return cudaLaunchKernelEx(&cfg, combine_kernel<E, decltype(dim)::value>, a, (int)rb);
     });
 }
 

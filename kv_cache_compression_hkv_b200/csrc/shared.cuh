@@ -47,7 +47,8 @@ struct View {
     int32_t listed;
     float2* part_ml;  // [np + no][R] (max, sum)
     float* part_o;    // [np + no][R][d]
-    float* logit;     // [S][Hk][rep T][cap] exp2-domain logits of the own keys (stream path, accumulate)
+    float* logit;     // [S][Hk][rep T][lcap] exp2-domain logits of the own keys (few rows, accumulate)
+    int32_t lcap;     // capacity rounded up to 4
     float* row_lse;   // [R] log2 of the row sums (tile path, accumulate)
 };
 
@@ -178,9 +179,12 @@ cudaError_t launch_column_sums_umma(const View& a, int d, cudaStream_t st);
 cudaError_t launch_prefix_umma(const View& a, int d, cudaStream_t st);
 cudaError_t launch_append(const View& a, int dtype, int d, const void* k_t, const int64_t* kts, const void* v_t,
                           const int64_t* vts, const float* w_t, cudaStream_t st);
-// skip_prefix: the prefix's partial results come from another launch
-cudaError_t launch_attend_simt(const View& a, int dtype, int d, bool skip_prefix, cudaStream_t st);
-cudaError_t launch_combine(const View& a, int dtype, int d, cudaStream_t st);
+cudaError_t launch_attend_simt(const View& a, int dtype, int d, cudaStream_t st);
+cudaError_t prepare_shared_stream();
+// dependent: launched beside the prefixes' kernel, whose end this launch's end includes
+cudaError_t launch_stream(const View& a, int d, int warps_per_head, bool dependent, cudaStream_t st);
+// dependent: may be set up before the launch in front of it has ended
+cudaError_t launch_combine(const View& a, int dtype, int d, bool dependent, cudaStream_t st);
 cudaError_t launch_column_sums_simt(const View& a, int dtype, int d, cudaStream_t st);
 cudaError_t launch_evict(const View& a, int dtype, int d, const int32_t* budget, int recent, int slack,
                          int32_t* holes, cudaStream_t st);

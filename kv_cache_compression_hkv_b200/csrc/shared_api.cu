@@ -76,12 +76,13 @@ View view_of(const hkv_shared_cache* c) {
 
 // The kernels of an attention call, and how its keys are split over blocks:
 //   fp32       CUDA cores, whatever the rows;
-//   bf16       rows of one (sequence, KV head) up to STREAM_ROWS: own keys on
-//              the CUDA cores, the prefixes' for all their sequences' rows on
-//              the tensor cores; more rows: tensor cores, prefix and own keys
+//   bf16       rows of one (sequence, KV head) up to STREAM_ROWS: own keys by
+//              the streaming kernel, the prefixes' for all their sequences'
+//              rows on the tensor cores; more rows: tensor cores, prefix and own keys
 //              in one pass, cut only where there are too few row tiles.
 struct Plan {
-    bool umma_prefix, umma_rows;
+    bool umma_prefix, umma_rows, stream;
+    int warps_per_head;  // of the stream kernel
     size_t bytes;
 };
 
@@ -91,6 +92,8 @@ Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char
     const int64_t rps = (int64_t)a.rep * T, R = (int64_t)a.S * a.H * T, heads = (int64_t)a.S * a.Hk;
     const bool stream = rps <= hkv::shared::STREAM_ROWS;
     Plan p;
+    p.stream = dtype == HKV_DTYPE_BF16 && stream;
+    p.warps_per_head = 1;
     p.umma_rows = dtype == HKV_DTYPE_BF16 && !stream;
     p.umma_prefix = dtype == HKV_DTYPE_BF16 && stream && a.G > 0;
     // `want` blocks over `tiles`, at least `least` keys a split
@@ -101,13 +104,22 @@ Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char
     };
     a.np = 0;
     a.listed = 0;
+    a.lcap = (a.cap + 3) & ~3;
     if (p.umma_rows) {
         const int nt = hkv::shared::umma_row_tiles(rps);
         const int64_t items = heads * ((rps + 128 * nt - 1) / (128 * nt));
         a.listed = 1;
         a.no = items >= 148 ? 1 : splits(nt == 2 ? 148 : 296, items, (int64_t)a.cap + (a.G ? a.pcap : 0), 256);
+    } else if (p.stream) {
+        // eight warps fit an SM: a head goes to as many as fill the GPU, one or several blocks of four
+        const int64_t warps = (148 * 8 + heads - 1) / heads, most = ((int64_t)a.cap + 31) / 32;
+        const int64_t n = warps < most ? warps : most;
+        p.warps_per_head = n > 1 ? 4 : 1;
+        a.no = n > 4 ? splits((n + 3) / 4, 1, a.cap, 64) : 1;
     } else {
         a.no = splits(148 * 6, heads * ((rps + 15) / 16), a.cap, 128);
+    }
+    if (!p.umma_rows) {
         if (a.G) {
             const int64_t tiles = (a.S * rps + 127) / 128, groups = a.G < a.S ? a.G : a.S;
             a.np = p.umma_prefix ? splits(296, a.Hk * (tiles > groups ? tiles : groups), a.pcap, 128)
@@ -125,7 +137,7 @@ Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char
         a.part_ml = (float2*)take(ns * R * sizeof(float2));
         a.part_o = (float*)take(ns * R * d * sizeof(float));
     }
-    if (accumulate && stream) a.logit = (float*)take((size_t)heads * rps * a.cap * 4);
+    if (accumulate && stream) a.logit = (float*)take((size_t)heads * rps * a.lcap * 4);
     if (accumulate && !stream) a.row_lse = (float*)take((size_t)R * 4);
     p.bytes = o;
     return p;
@@ -140,6 +152,7 @@ cudaError_t prepare() {
     const unsigned long long bit = 1ull << (dev & 63);
     if (ready.load() & bit) return cudaSuccess;
     e = hkv::shared::prepare_shared_umma();
+    if (e == cudaSuccess) e = hkv::shared::prepare_shared_stream();
     if (e == cudaSuccess && dev < 64) ready.fetch_or(bit);
     return e;
 }
@@ -206,8 +219,9 @@ hkv_status hkv_shared_attend(const hkv_shared_cache* c, const void* q, const int
     const int d = c->head_dim;
     if (e == cudaSuccess && p.umma_rows) e = hkv::shared::launch_attend_umma(a, d, st);
     if (e == cudaSuccess && p.umma_prefix) e = hkv::shared::launch_prefix_umma(a, d, st);
-    if (e == cudaSuccess && !p.umma_rows) e = hkv::shared::launch_attend_simt(a, c->dtype, d, p.umma_prefix, st);
-    if (e == cudaSuccess && a.part_ml) e = hkv::shared::launch_combine(a, c->dtype, d, st);
+    if (e == cudaSuccess && p.stream) e = hkv::shared::launch_stream(a, d, p.warps_per_head, p.umma_prefix, st);
+    if (e == cudaSuccess && !p.umma_rows && !p.stream) e = hkv::shared::launch_attend_simt(a, c->dtype, d, st);
+    if (e == cudaSuccess && a.part_ml) e = hkv::shared::launch_combine(a, c->dtype, d, p.stream || p.umma_rows, st);
     if (e == cudaSuccess && a.row_lse)
         e = p.umma_rows ? hkv::shared::launch_column_sums_umma(a, d, st)
                         : hkv::shared::launch_column_sums_simt(a, c->dtype, d, st);

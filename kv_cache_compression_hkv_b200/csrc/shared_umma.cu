@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
     const int rps = a.rep * a.T;
     const int64_t R = (int64_t)a.S * a.H * a.T;
 
+    ptx::grid_dep_trigger();
     // what this block works on
     int hk, s = 0, g, first, rows, piece, p_tiles, t0, t1, p_len, n_own = 0, p_lo = 0;
     if constexpr (MODE == 0) {
@@ -641,19 +642,22 @@ static cudaError_t go(const View& a, const CUtensorMap* m, int64_t blocks, int r
     return cudaGetLastError();
 }
 
-static bool cache_maps(const View& a, int d, CUtensorMap* m) {
-    if (!make_map(m, a.k, d, a.cap, a.Hk, a.S, a.ks, UK) || !make_map(m + 1, a.v, d, a.cap, a.Hk, a.S, a.vs, UK)) return false;
-    if (a.G == 0) {
-        m[2] = m[0];
-        m[3] = m[1];
-        return true;
-    }
-    return make_map(m + 2, a.pk, d, a.pcap, a.Hk, a.G, a.pks, UK) && make_map(m + 3, a.pv, d, a.pcap, a.Hk, a.G, a.pvs, UK);
+static bool own_maps(const View& a, int d, CUtensorMap* m) {
+    return make_map(m, a.k, d, a.cap, a.Hk, a.S, a.ks, UK) && make_map(m + 1, a.v, d, a.cap, a.Hk, a.S, a.vs, UK);
+}
+static bool prefix_maps(const View& a, int d, CUtensorMap* m) {
+    return make_map(m, a.pk, d, a.pcap, a.Hk, a.G, a.pks, UK) && make_map(m + 1, a.pv, d, a.pcap, a.Hk, a.G, a.pvs, UK);
 }
 
 cudaError_t launch_attend_umma(const View& a, int d, cudaStream_t st) {
     CUtensorMap m[4];
-    if (!cache_maps(a, d, m)) return cudaErrorInvalidValue;
+    if (!own_maps(a, d, m)) return cudaErrorInvalidValue;
+    if (a.G == 0) {  // never read
+        m[2] = m[0];
+        m[3] = m[1];
+    } else if (!prefix_maps(a, d, m + 2)) {
+        return cudaErrorInvalidValue;
+    }
     const int rps = a.rep * a.T, nt = umma_row_tiles(rps), splits = a.no;
     const int tiles = (rps + QT * nt - 1) / (QT * nt);
     const int64_t blocks = (int64_t)tiles * a.S * a.Hk * splits;
@@ -664,7 +668,9 @@ cudaError_t launch_attend_umma(const View& a, int d, cudaStream_t st) {
 
 cudaError_t launch_prefix_umma(const View& a, int d, cudaStream_t st) {
     CUtensorMap m[4];
-    if (!cache_maps(a, d, m)) return cudaErrorInvalidValue;
+    if (!prefix_maps(a, d, m + 2)) return cudaErrorInvalidValue;
+    m[0] = m[2];  // never read
+    m[1] = m[3];
     const int rps = a.rep * a.T;
     const int64_t tiles = max_prefix_tiles(a.S, a.G, rps, QT);
     const int64_t blocks = tiles * a.Hk * a.np;
