@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
     int* list = res + 4;
     constexpr int NSUB = D / 64;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tc::uniform(tid >> 5), lane = tid & 31;
     const int rps = a.rep * a.T;
     const int64_t R = (int64_t)a.S * a.H * a.T;
 
@@ -178,17 +178,27 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                     mbar_wait(bars + C::B_FULL + i % C::NS, (i / C::NS) & 1, WAIT_NS);
         }
     } else if (warp == C::MMA_WARP) {
-        // The whole warp waits; lane 0 issues.
+        // The whole warp waits; one lane issues.  All that an MMA's operands
+        // come from is made uniform first: with addresses in per-thread
+        // registers an issue took 84 cycles, three times what the product takes.
         constexpr uint32_t IS = tc::idesc_bf16(UK, false), IO = tc::idesc_bf16(D, true);
+        const bool leader = tc::elect();
+        const uint32_t tm = tc::uniform(tmem);
+        n = tc::uniform(n);
+#pragma unroll
+        for (int x = 0; x < NT; ++x) nx[x] = tc::uniform(nx[x]);
+        const uint32_t ring_u = tc::uniform(smem_u32(ring)), q_u = tc::uniform(smem_u32(q_s));
+        const uint64_t q_desc = tc::sw128_desc(q_u, 16, 1024), k_desc = tc::sw128_desc(ring_u, 16, 1024),
+                       v_desc = tc::sw128_desc(ring_u, UK * 128, 1024);
         auto ok = [&](bool w) { return !__any_sync(FULL_MASK, !w); };
         auto full = [&](int i) { return ok(mbar_wait(bars + C::B_FULL + i % C::NS, (i / C::NS) & 1, WAIT_NS)); };
         auto issue_s = [&](int x, int j) {
-            if (lane == 0) {
-                const uint32_t kb = smem_u32(ring + (k_idx(j) % C::NS) * C::KV_BYTES), qb = smem_u32(q_s + x * C::Q_BYTES);
+            if (leader) {
+                const uint64_t qd = q_desc + x * (C::Q_BYTES / 16), kd = k_desc + (k_idx(j) % C::NS) * (C::KV_BYTES / 16);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc::mma_ss(tmem + x * 128 + (j & 1) * UK, tc::sw128_desc(qb + (kk / 4) * (QT * 128) + (kk % 4) * 32, 16, 1024),
-                               tc::sw128_desc(kb + (kk / 4) * (UK * 128) + (kk % 4) * 32, 16, 1024), IS, kk > 0);
+                for (int kk = 0; kk < D / 16; ++kk)  // descriptors count 16-byte units
+                    tc::mma_ss(tm + x * 128 + (j & 1) * UK, qd + (kk / 4) * (QT * 8) + (kk % 4) * 2,
+                               kd + (kk / 4) * (UK * 8) + (kk % 4) * 2, IS, kk > 0);
                 tc::commit(bars + C::B_S + 2 * x + (j & 1));
             }
             __syncwarp();
@@ -203,7 +213,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
 #pragma unroll
                 for (int x = 0; x < NT; ++x)
                     if (nx[x] > 0) { issue_s(x, 0); s_done[x] = 0; }
-                if (lane == 0) tc::commit(bars + C::B_FREE + 0);
+                if (leader) tc::commit(bars + C::B_FREE + 0);
+                __syncwarp();
             }
         }
         for (int j = 0; j < n && !fail; ++j) {
@@ -224,7 +235,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                     issue_s(x, j + 1);
                     s_done[x] = j + 1;
                 }
-                if (x == NT - 1 && more && lane == 0) tc::commit(bars + C::B_FREE + k_idx(j + 1) % C::NS);
+                if (x == NT - 1 && more) {
+                    if (leader) tc::commit(bars + C::B_FREE + k_idx(j + 1) % C::NS);
+                    __syncwarp();
+                }
                 if (j < nx[x]) {
                     if (!v_ready) {
                         if (!full(vi)) { fail = true; break; }
@@ -245,19 +259,22 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                     }
                     if (!ok(mbar_wait(bars + C::B_P + 2 * x + (j & 1), (j >> 1) & 1, WAIT_NS))) { fail = true; break; }
                     tc::fence_after();
-                    if (lane == 0) {
-                        const uint32_t vb = smem_u32(ring + (vi % C::NS) * C::KV_BYTES);
+                    if (leader) {
+                        const uint64_t vd = v_desc + (vi % C::NS) * (C::KV_BYTES / 16);
 #pragma unroll
                         for (int kk = 0; kk < UK / 16; ++kk)
-                            tc::mma_ts(tmem + C::O_COL + x * D, tmem + x * 128 + (j & 1) * UK + kk * 8,
-                                       tc::sw128_desc(vb + kk * 16 * 128, UK * 128, 1024), IO, (j > 0 || kk > 0));
+                            tc::mma_ts(tm + C::O_COL + x * D, tm + x * 128 + (j & 1) * UK + kk * 8, vd + kk * 128, IO,
+                                       (j > 0 || kk > 0));
                         tc::commit(bars + C::B_PV + 2 * x + (j & 1));
                     }
                     __syncwarp();
                     pv_done[x] = j;
                 }
             }
-            if (!fail && lane == 0) tc::commit(bars + C::B_FREE + vi % C::NS);
+            if (!fail) {
+                if (leader) tc::commit(bars + C::B_FREE + vi % C::NS);
+                __syncwarp();
+            }
         }
         // The tensor cores finish what was issued before TMEM is freed, and
         // the last commits' arrivals land before the shared memory goes.
@@ -472,7 +489,7 @@ __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
     uint64_t* bars = reinterpret_cast<uint64_t*>(half + C::KB);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::B_COUNT);
     constexpr int NSUB = D / 64;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tc::uniform(tid >> 5), lane = tid & 31;
     // the first keys, which the most queries see, first
     const int heads = a.S * a.Hk, sh = blockIdx.x % heads, k0 = blockIdx.x / heads * C::KB;
     const int s = sh / a.Hk, hk = sh % a.Hk;
@@ -526,28 +543,35 @@ __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
                 mbar_wait(bars + C::B_FULL + j % C::NS, (j / C::NS) & 1, WAIT_NS);
         }
     } else if (warp == C::MMA_WARP) {
-        if (lane == 0) {
-            constexpr uint32_t IS = tc::idesc_bf16(C::QN, false);
-            int done = -1;
-            if (!mbar_wait(bars + C::B_K, 0, WAIT_NS)) fail = true;
-            for (int j = 0; j < tiles && !fail; ++j) {
-                const int slot = j % C::NS;
-                if (!mbar_wait(bars + C::B_FULL + slot, (j / C::NS) & 1, WAIT_NS)) { fail = true; break; }
-                tc::fence_after();
-                const uint32_t kb = smem_u32(k_s), qb = smem_u32(q_s + slot * C::Q_BYTES);
+        constexpr uint32_t IS = tc::idesc_bf16(C::QN, false);
+        const bool leader = tc::elect();
+        const uint32_t tm = tc::uniform(tmem);
+        const uint64_t k_desc = tc::sw128_desc(tc::uniform(smem_u32(k_s)), 16, 1024),
+                       q_desc = tc::sw128_desc(tc::uniform(smem_u32(q_s)), 16, 1024);
+        auto ok = [&](bool w) { return !__any_sync(FULL_MASK, !w); };
+        const int nt = tc::uniform(tiles);
+        int done = -1;
+        if (!ok(mbar_wait(bars + C::B_K, 0, WAIT_NS))) fail = true;
+        for (int j = 0; j < nt && !fail; ++j) {
+            const int slot = j % C::NS;
+            if (!ok(mbar_wait(bars + C::B_FULL + slot, (j / C::NS) & 1, WAIT_NS))) { fail = true; break; }
+            tc::fence_after();
+            if (leader) {
+                const uint64_t qd = q_desc + slot * (C::Q_BYTES / 16);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    tc::mma_ss(tmem + slot * C::QN, tc::sw128_desc(kb + (kk / 4) * (C::KB * 128) + (kk % 4) * 32, 16, 1024),
-                               tc::sw128_desc(qb + (kk / 4) * (C::QN * 128) + (kk % 4) * 32, 16, 1024), IS, kk > 0);
+                    tc::mma_ss(tm + slot * C::QN, k_desc + (kk / 4) * (C::KB * 8) + (kk % 4) * 2,
+                               qd + (kk / 4) * (C::QN * 8) + (kk % 4) * 2, IS, kk > 0);
                 tc::commit(bars + C::B_S + slot);
                 tc::commit(bars + C::B_FREE + slot);
-                done = j;
             }
-            if (done >= 0) {
-                mbar_wait(bars + C::B_S + done % C::NS, (done / C::NS) & 1, WAIT_NS);
-                // (the row warps' arrivals complete the other barrier's phase)
-                if (!fail) mbar_wait(bars + C::B_FREE + done % C::NS, (done / C::NS) & 1, WAIT_NS);
-            }
+            __syncwarp();
+            done = j;
+        }
+        if (done >= 0) {
+            mbar_wait(bars + C::B_S + done % C::NS, (done / C::NS) & 1, WAIT_NS);
+            // (the row warps' arrivals complete the other barrier's phase)
+            if (!fail) mbar_wait(bars + C::B_FREE + done % C::NS, (done / C::NS) & 1, WAIT_NS);
         }
     } else {
         const int grp = warp >> 2, key = k0 + (tid & 127);

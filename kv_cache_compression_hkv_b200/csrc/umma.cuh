@@ -95,6 +95,15 @@ __device__ __forceinline__ void dealloc(uint32_t tmem, uint32_t cols) {
 __device__ __forceinline__ void arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// One lane of the (converged) warp, the same on every call.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// A value that all lanes hold alike, told to the compiler: what follows from
+// it stays in uniform registers, where an MMA's operands have to be.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 // 2^x by the SFU (relative error about 2^-22, results below 2^-126 flushed to zero).
 __device__ __forceinline__ float ex2(float x) {
     float y;
