@@ -4,8 +4,8 @@
 // A block takes NT tiles of 128 query rows that share their keys and walks a
 // list of 64-key tiles, prefix first, then own keys up to the rows' causal
 // limit.  Per (row tile X, key tile j):
-//   S = Q_X K_j^T   (M 128, N 64, fp32 in TMEM; two slots a row tile)
-//   P = 2^(c S - m) as bf16 over the first half of S's slot, in TMEM
+//   S = Q_X K_j^T   (M 128, N 64, fp32 in TMEM)
+//   P = 2^(c S - m) as bf16 in TMEM, two slots a row tile
 //   O_X += P V_j    (A from TMEM, V as the MN-major operand, fp32 in TMEM)
 // Rows: thread = query row = TMEM lane.  m is a reference maximum that is
 // raised (and O rescaled in TMEM) only when a logit passes it by more than
@@ -13,10 +13,10 @@
 // the sum l is of the unrounded weights in fp32.
 // Roles: 4 NT softmax warps; a copy warp (TMA into a ring of K and V tiles,
 // in the order K0, K1 V0, K2 V1, ... in which they are used); an MMA warp.
-// S of tile j + 1 is issued before the weights of tile j are waited for, into
-// the other slot, so a row tile's softmax always finds its next logits ready,
-// and with NT = 2 the tensor cores work for one row tile while the other's
-// rows compute.
+// S of tile j + 1 is issued as soon as the rows hold S of tile j in registers,
+// so a softmax warp finds its next logits ready.  (With P over S's own place
+// and two such places, S of tile j + 2 had to wait for the product of tile j
+// behind the other row tile's: 2150 cycles a tile against <CYC>.)
 #include <math.h>
 
 #include "kernels.h"
@@ -44,10 +44,10 @@ template <int D, int NT> struct Shape {
     static constexpr int ROWS = 128 * NT;
     static constexpr int THREADS = ROWS + 64;
     static constexpr int COPY_WARP = 4 * NT, MMA_WARP = 4 * NT + 1;
-    static constexpr uint32_t O_COL = 128 * NT;  // S: two slots of 64 columns a row tile
+    static constexpr uint32_t O_COL = 128 * NT;  // before it, a row tile: 64 columns of S, two times 32 of P
     static constexpr uint32_t TMEM = NT == 2 ? 512 : 256;
     static constexpr int Q_BYTES = QT * D * 2, KV_BYTES = UK * D * 2;
-    enum { B_Q, B_FULL, B_FREE = B_FULL + NS, B_S = B_FREE + NS, B_P = B_S + 2 * NT, B_PV = B_P + 2 * NT,
+    enum { B_Q, B_FULL, B_FREE = B_FULL + NS, B_S = B_FREE + NS, B_SF = B_S + NT, B_P = B_SF + NT, B_PV = B_P + 2 * NT,
            B_COUNT = B_PV + 2 * NT };
     static constexpr int TAIL = B_COUNT * 8 + 16 + 16 + (QT + 1) * 4 + 12;
     static constexpr int SMEM = 1024 + NT * Q_BYTES + NS * KV_BYTES + TAIL;
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
     if (warp == 0) tc::alloc(tmem_slot, C::TMEM);
     if (tid == 0) {
         for (int i = 0; i < C::B_COUNT; ++i)
-            mbar_init(bars + i, i == C::B_Q ? 4 * NT : (i >= C::B_P && i < C::B_PV) ? 4 : 1);
+            mbar_init(bars + i, i == C::B_Q ? 4 * NT : (i >= C::B_SF && i < C::B_PV) ? 4 : 1);
         ptx::fence_mbar_init();
     }
     tc::fence_before();
@@ -197,9 +197,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                 const uint64_t qd = q_desc + x * (C::Q_BYTES / 16), kd = k_desc + (k_idx(j) % C::NS) * (C::KV_BYTES / 16);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)  // descriptors count 16-byte units
-                    tc::mma_ss(tm + x * 128 + (j & 1) * UK, qd + (kk / 4) * (QT * 8) + (kk % 4) * 2,
+                    tc::mma_ss(tm + x * 128, qd + (kk / 4) * (QT * 8) + (kk % 4) * 2,
                                kd + (kk / 4) * (UK * 8) + (kk % 4) * 2, IS, kk > 0);
-                tc::commit(bars + C::B_S + 2 * x + (j & 1));
+                tc::commit(bars + C::B_S + x);
             }
             __syncwarp();
         };
@@ -221,24 +221,23 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
             const bool more = j + 1 < n;
             const int vi = v_idx(j);
             bool v_ready = false;
+            if (more) {
 #pragma unroll
-            for (int x = 0; x < NT; ++x) {
-                if (fail) break;
-                if (j + 1 < nx[x]) {
-                    // slot (j + 1) % 2 still holds P_{j-1} until its product is done
-                    if (!full(k_idx(j + 1)) ||
-                        (j >= 1 && !ok(mbar_wait(bars + C::B_PV + 2 * x + ((j - 1) & 1), ((j - 1) >> 1) & 1, WAIT_NS)))) {
-                        fail = true;
-                        break;
-                    }
+                for (int x = 0; x < NT; ++x) {
+                    if (fail || j + 1 >= nx[x]) continue;
+                    if (!full(k_idx(j + 1)) || !ok(mbar_wait(bars + C::B_SF + x, j & 1, WAIT_NS))) { fail = true; continue; }
                     tc::fence_after();
                     issue_s(x, j + 1);
                     s_done[x] = j + 1;
                 }
-                if (x == NT - 1 && more) {
+                if (!fail) {
                     if (leader) tc::commit(bars + C::B_FREE + k_idx(j + 1) % C::NS);
                     __syncwarp();
                 }
+            }
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                if (fail) break;
                 if (j < nx[x]) {
                     if (!v_ready) {
                         if (!full(vi)) { fail = true; break; }
@@ -263,7 +262,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                         const uint64_t vd = v_desc + (vi % C::NS) * (C::KV_BYTES / 16);
 #pragma unroll
                         for (int kk = 0; kk < UK / 16; ++kk)
-                            tc::mma_ts(tm + C::O_COL + x * D, tm + x * 128 + (j & 1) * UK + kk * 8, vd + kk * 128, IO,
+                            tc::mma_ts(tm + C::O_COL + x * D, tm + x * 128 + UK + (j & 1) * 32 + kk * 8, vd + kk * 128, IO,
                                        (j > 0 || kk > 0));
                         tc::commit(bars + C::B_PV + 2 * x + (j & 1));
                     }
@@ -280,7 +279,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
         // the last commits' arrivals land before the shared memory goes.
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-            if (s_done[x] > pv_done[x]) mbar_wait(bars + C::B_S + 2 * x + (s_done[x] & 1), (s_done[x] >> 1) & 1, WAIT_NS);
+            if (s_done[x] > pv_done[x]) mbar_wait(bars + C::B_S + x, s_done[x] & 1, WAIT_NS);
             if (pv_done[x] >= 0)
                 mbar_wait(bars + C::B_PV + 2 * x + (pv_done[x] & 1), (pv_done[x] >> 1) & 1, WAIT_NS);
         }
@@ -331,16 +330,18 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
         float m = -INFINITY, l = 0.f;  // reference maximum (times c) and sum
         // every branch around the warp-wide TMEM accesses is taken by the whole warp
         for (int j = 0; j < nt; ++j) {
-            const uint32_t ts = t_s + (j & 1) * UK;
-            if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_S + 2 * x + (j & 1), (j >> 1) & 1, WAIT_NS))) { fail = true; break; }
+            if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_S + x, j & 1, WAIT_NS))) { fail = true; break; }
             tc::fence_after();
             uint32_t sr[2][32];
-            tc::ld32(ts, sr[0]);
-            tc::ld32(ts + 32, sr[1]);
+            tc::ld32(t_s, sr[0]);
+            tc::ld32(t_s + 32, sr[1]);
             bool pre;
             int k0, valid;
             tile_at(j, pre, k0, valid);
             tc::ld_wait();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::arrive(bars + C::B_SF + x);
             if (valid < UK || (!pre && k0 + UK > lim_warp)) {
                 const int end = pre ? valid : min(valid, lim - k0);
 #pragma unroll
@@ -387,7 +388,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                 w[u] = *reinterpret_cast<uint32_t*>(&h2);
             }
             l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-            tc::st32(ts, w);
+            // P's slot is free once the product of tile j - 2 is done
+            if (j >= 2 && __any_sync(FULL_MASK, !mbar_wait(bars + C::B_PV + 2 * x + (j & 1), ((j >> 1) - 1) & 1, WAIT_NS))) {
+                fail = true;
+                break;
+            }
+            tc::fence_after();
+            tc::st32(t_s + UK + (j & 1) * 32, w);
             tc::st_wait();
             tc::fence_before();
             __syncwarp();
