@@ -11,12 +11,13 @@
 // raised (and O rescaled in TMEM) only when a logit passes it by more than
 // 16, so weights stay below 2^16 and bf16's relative rounding is unaffected;
 // the sum l is of the unrounded weights in fp32.
-// Roles: 4 NT softmax warps; a copy warp (TMA into a ring of K and V tiles,
-// in the order K0, K1 V0, K2 V1, ... in which they are used); an MMA warp.
+// Roles: 4 NT softmax warps; a copy warp (TMA into a ring of pairs K0, V0 K1,
+// V1 K2, ... as they are used together); an MMA warp, one lane of which waits
+// and issues.
 // S of tile j + 1 is issued as soon as the rows hold S of tile j in registers,
 // so a softmax warp finds its next logits ready.  (With P over S's own place
 // and two such places, S of tile j + 2 had to wait for the product of tile j
-// behind the other row tile's: 2150 cycles a tile against <CYC>.)
+// behind the other row tile's: 2150 cycles a tile.)
 #include <math.h>
 
 #include "kernels.h"
@@ -40,7 +41,7 @@ constexpr float RAISE = 16.f;
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
 template <int D, int NT> struct Shape {
-    static constexpr int NS = NT == 2 ? (D == 128 ? 8 : 12) : (D == 128 ? 4 : 6);  // K / V tiles in the ring
+    static constexpr int NS = NT == 2 ? (D == 128 ? 4 : 6) : (D == 128 ? 2 : 3);  // (V, K) pairs in the ring
     static constexpr int ROWS = 128 * NT;
     static constexpr int THREADS = ROWS + 64;
     static constexpr int COPY_WARP = 4 * NT, MMA_WARP = 4 * NT + 1;
@@ -50,7 +51,7 @@ template <int D, int NT> struct Shape {
     enum { B_Q, B_FULL, B_FREE = B_FULL + NS, B_S = B_FREE + NS, B_SF = B_S + NT, B_P = B_SF + NT, B_PV = B_P + 2 * NT,
            B_COUNT = B_PV + 2 * NT };
     static constexpr int TAIL = B_COUNT * 8 + 16 + 16 + (QT + 1) * 4 + 12;
-    static constexpr int SMEM = 1024 + NT * Q_BYTES + NS * KV_BYTES + TAIL;
+    static constexpr int SMEM = 1024 + NT * Q_BYTES + NS * 2 * KV_BYTES + TAIL;
 };
 
 }  // namespace
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
     unsigned char* base = reinterpret_cast<unsigned char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     unsigned char* q_s = base;
     unsigned char* ring = q_s + NT * C::Q_BYTES;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(ring + C::NS * C::KV_BYTES);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(ring + C::NS * 2 * C::KV_BYTES);  // a pair: V, then K
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::B_COUNT);
     int* res = reinterpret_cast<int*>(tmem_slot + 4);
     int* list = res + 4;
@@ -150,27 +151,29 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
         k0 = pre ? p_lo + t * UK : (t - p_tiles) * UK;
         valid = min(UK, (pre ? p_len : n_own) - k0);
     };
-    // ring index of K_j and V_j
-    auto k_idx = [](int j) { return j == 0 ? 0 : 2 * j - 1; };
-    auto v_idx = [&](int j) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; };
-
     if (warp == C::COPY_WARP) {
         if (lane == 0) {
+            // pair i: V of tile i - 1 and K of tile i
             int issued = 0;
-            for (int i = 0; i < 2 * n; ++i) {
+            for (int i = 0; i <= n && n > 0; ++i) {
                 const int slot = i % C::NS, use = i / C::NS;
                 if (use > 0 && !mbar_wait(bars + C::B_FREE + slot, (use - 1) & 1, WAIT_NS)) { fail = true; break; }
-                // i = 0: K0; odd i < 2n - 1: K_{(i+1)/2}; even: V_{i/2 - 1}; 2n - 1: V_{n-1}
-                const bool is_k = i == 0 || ((i & 1) && i < 2 * n - 1);
-                const int j = i == 0 ? 0 : is_k ? (i + 1) / 2 : i == 2 * n - 1 ? n - 1 : i / 2 - 1;
+                unsigned char* dst = ring + slot * 2 * C::KV_BYTES;
+                mbar_expect_tx(bars + C::B_FULL + slot, (i > 0 && i < n ? 2 : 1) * C::KV_BYTES);
                 bool pre;
                 int k0, valid;
-                tile_at(j, pre, k0, valid);
-                const CUtensorMap* m = is_k ? (pre ? &pkm : &km) : (pre ? &pvm : &vm);
-                mbar_expect_tx(bars + C::B_FULL + slot, C::KV_BYTES);
-                for (int sub = 0; sub < NSUB; ++sub)
-                    tc::tma_load_4d(ring + slot * C::KV_BYTES + sub * UK * 128, m, bars + C::B_FULL + slot, sub * 64, k0,
-                                    hk, pre ? g : s);
+                if (i < n) {
+                    tile_at(i, pre, k0, valid);
+                    for (int sub = 0; sub < NSUB; ++sub)
+                        tc::tma_load_4d(dst + C::KV_BYTES + sub * UK * 128, pre ? &pkm : &km, bars + C::B_FULL + slot,
+                                        sub * 64, k0, hk, pre ? g : s);
+                }
+                if (i > 0) {
+                    tile_at(i - 1, pre, k0, valid);
+                    for (int sub = 0; sub < NSUB; ++sub)
+                        tc::tma_load_4d(dst + sub * UK * 128, pre ? &pvm : &vm, bars + C::B_FULL + slot, sub * 64, k0, hk,
+                                        pre ? g : s);
+                }
                 issued = i + 1;
             }
             if (fail)  // the block's own copies land before its shared memory goes
@@ -178,115 +181,98 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                     mbar_wait(bars + C::B_FULL + i % C::NS, (i / C::NS) & 1, WAIT_NS);
         }
     } else if (warp == C::MMA_WARP) {
-        // The whole warp waits; one lane issues.  All that an MMA's operands
-        // come from is made uniform first: with addresses in per-thread
-        // registers an issue took 84 cycles, three times what the product takes.
+        // All that an MMA's operands come from is made uniform first (with
+        // addresses in per-thread registers an issue took 84 cycles, up to
+        // three times the product), and one lane does the waiting too (votes
+        // of the warp around each wait idled the tensor cores: a tile of two
+        // row tiles took 2150 cycles, of which the products are 1260).
         constexpr uint32_t IS = tc::idesc_bf16(UK, false), IO = tc::idesc_bf16(D, true);
-        const bool leader = tc::elect();
         const uint32_t tm = tc::uniform(tmem);
-        n = tc::uniform(n);
+        const int nn = tc::uniform(n);
+        int nu[NT];
 #pragma unroll
-        for (int x = 0; x < NT; ++x) nx[x] = tc::uniform(nx[x]);
+        for (int x = 0; x < NT; ++x) nu[x] = tc::uniform(nx[x]);
         const uint32_t ring_u = tc::uniform(smem_u32(ring)), q_u = tc::uniform(smem_u32(q_s));
-        const uint64_t q_desc = tc::sw128_desc(q_u, 16, 1024), k_desc = tc::sw128_desc(ring_u, 16, 1024),
+        const uint64_t q_desc = tc::sw128_desc(q_u, 16, 1024), k_desc = tc::sw128_desc(ring_u + C::KV_BYTES, 16, 1024),
                        v_desc = tc::sw128_desc(ring_u, UK * 128, 1024);
-        auto ok = [&](bool w) { return !__any_sync(FULL_MASK, !w); };
-        auto full = [&](int i) { return ok(mbar_wait(bars + C::B_FULL + i % C::NS, (i / C::NS) & 1, WAIT_NS)); };
-        auto issue_s = [&](int x, int j) {
-            if (leader) {
-                const uint64_t qd = q_desc + x * (C::Q_BYTES / 16), kd = k_desc + (k_idx(j) % C::NS) * (C::KV_BYTES / 16);
+        if (tc::elect()) {
+            // What is ready goes: P V(x, j) once pair j + 1 is there and the
+            // weights are written; S(x, j) once pair j is there, the rows have
+            // read S(x, j - 1) and P V(x, j - 2) was issued (the commit behind S
+            // then covers it, which tells the rows that P's slot is free).  (In
+            // a fixed order S of one row tile waited for the weights of the
+            // other.)
+            int sj[NT], pj[NT];  // next tile of each
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)  // descriptors count 16-byte units
-                    tc::mma_ss(tm + x * 128, qd + (kk / 4) * (QT * 8) + (kk % 4) * 2,
-                               kd + (kk / 4) * (UK * 8) + (kk % 4) * 2, IS, kk > 0);
-                tc::commit(bars + C::B_S + x);
-            }
-            __syncwarp();
-        };
-        int s_done[NT], pv_done[NT];
+            for (int x = 0; x < NT; ++x) sj[x] = pj[x] = 0;
+            int there = 0, freed = 0;  // pairs known to have landed; pairs given back
+            auto landed = [&](int i) {
+                if (i < there) return true;
+                if (!ptx::mbar_test(bars + C::B_FULL + there % C::NS, (there / C::NS) & 1)) return false;
+                ++there;
+                return i < there;
+            };
+            // pair i is done with S of tile i and P V of tile i - 1
+            auto used = [&](int i) {
+                bool done = i <= nn;
 #pragma unroll
-        for (int x = 0; x < NT; ++x) s_done[x] = pv_done[x] = -1;
-        if (n > 0) {
-            if (!ok(mbar_wait(bars + C::B_Q, 0, WAIT_NS)) || !full(0)) fail = true;
-            tc::fence_after();
-            if (!fail) {
-#pragma unroll
-                for (int x = 0; x < NT; ++x)
-                    if (nx[x] > 0) { issue_s(x, 0); s_done[x] = 0; }
-                if (leader) tc::commit(bars + C::B_FREE + 0);
-                __syncwarp();
-            }
-        }
-        for (int j = 0; j < n && !fail; ++j) {
-            const bool more = j + 1 < n;
-            const int vi = v_idx(j);
-            bool v_ready = false;
-            if (more) {
+                for (int x = 0; x < NT; ++x) done = done && sj[x] > min(i, nu[x] - 1) && pj[x] >= min(i, nu[x]);
+                return done;
+            };
+            if (!mbar_wait(bars + C::B_Q, 0, WAIT_NS)) fail = true;
+            uint32_t idle = 0;
+            uint64_t since = 0;
+            while (!fail && freed <= nn && nn > 0) {
+                bool went = false;
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
-                    if (fail || j + 1 >= nx[x]) continue;
-                    if (!full(k_idx(j + 1)) || !ok(mbar_wait(bars + C::B_SF + x, j & 1, WAIT_NS))) { fail = true; continue; }
-                    tc::fence_after();
-                    issue_s(x, j + 1);
-                    s_done[x] = j + 1;
-                }
-                if (!fail) {
-                    if (leader) tc::commit(bars + C::B_FREE + k_idx(j + 1) % C::NS);
-                    __syncwarp();
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < NT; ++x) {
-                if (fail) break;
-                if (j < nx[x]) {
-                    if (!v_ready) {
-                        if (!full(vi)) { fail = true; break; }
-                        bool pre;
-                        int k0, valid;
-                        tile_at(j, pre, k0, valid);
-                        if (valid < UK) {
-                            // rows past the last key hold whatever the memory held: 0 x NaN must not be formed
-                            unsigned char* vt = ring + (vi % C::NS) * C::KV_BYTES;
-                            for (int e = lane; e < (UK - valid) * 8 * NSUB; e += 32) {
-                                const int sub = e / ((UK - valid) * 8), w = e % ((UK - valid) * 8);
-                                *reinterpret_cast<uint4*>(vt + sub * UK * 128 + valid * 128 + w * 16) = make_uint4(0, 0, 0, 0);
-                            }
-                            ptx::fence_proxy_async();
-                            __syncwarp();
-                        }
-                        v_ready = true;
-                    }
-                    if (!ok(mbar_wait(bars + C::B_P + 2 * x + (j & 1), (j >> 1) & 1, WAIT_NS))) { fail = true; break; }
-                    tc::fence_after();
-                    if (leader) {
-                        const uint64_t vd = v_desc + (vi % C::NS) * (C::KV_BYTES / 16);
+                    if (pj[x] < sj[x] && landed(pj[x] + 1) &&
+                        ptx::mbar_test(bars + C::B_P + 2 * x + (pj[x] & 1), (pj[x] >> 1) & 1)) {
+                        tc::fence_after();
+                        const uint64_t vd = v_desc + ((pj[x] + 1) % C::NS) * (2 * C::KV_BYTES / 16);
 #pragma unroll
                         for (int kk = 0; kk < UK / 16; ++kk)
-                            tc::mma_ts(tm + C::O_COL + x * D, tm + x * 128 + UK + (j & 1) * 32 + kk * 8, vd + kk * 128, IO,
-                                       (j > 0 || kk > 0));
-                        tc::commit(bars + C::B_PV + 2 * x + (j & 1));
+                            tc::mma_ts(tm + C::O_COL + x * D, tm + x * 128 + UK + (pj[x] & 1) * 32 + kk * 8, vd + kk * 128, IO,
+                                       (pj[x] > 0 || kk > 0));
+                        tc::commit(bars + C::B_PV + 2 * x + (pj[x] & 1));
+                        ++pj[x];
+                        went = true;
                     }
-                    __syncwarp();
-                    pv_done[x] = j;
+                    if (sj[x] < nu[x] && sj[x] <= pj[x] + 1 && landed(sj[x]) &&
+                        (sj[x] == 0 || ptx::mbar_test(bars + C::B_SF + x, (sj[x] - 1) & 1))) {
+                        tc::fence_after();
+                        const uint64_t qd = q_desc + x * (C::Q_BYTES / 16), kd = k_desc + (sj[x] % C::NS) * (2 * C::KV_BYTES / 16);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)  // descriptors count 16-byte units
+                            tc::mma_ss(tm + x * 128, qd + (kk / 4) * (QT * 8) + (kk % 4) * 2,
+                                       kd + (kk / 4) * (UK * 8) + (kk % 4) * 2, IS, kk > 0);
+                        tc::commit(bars + C::B_S + x);
+                        ++sj[x];
+                        went = true;
+                    }
+                }
+                if (went) {
+                    while (used(freed)) {
+                        tc::commit(bars + C::B_FREE + freed % C::NS);
+                        ++freed;
+                    }
+                    idle = 0;
+                } else if ((++idle & 1023) == 0) {
+                    const uint64_t now = ptx::globaltimer();
+                    if (idle == 1024) since = now;
+                    else if (now - since > WAIT_NS) fail = true;
                 }
             }
-            if (!fail) {
-                if (leader) tc::commit(bars + C::B_FREE + vi % C::NS);
-                __syncwarp();
-            }
-        }
-        // The tensor cores finish what was issued before TMEM is freed, and
-        // the last commits' arrivals land before the shared memory goes.
+            // The tensor cores finish what was issued before TMEM is freed, and
+            // the last commits' arrivals land before the shared memory goes.
 #pragma unroll
-        for (int x = 0; x < NT; ++x) {
-            if (s_done[x] > pv_done[x]) mbar_wait(bars + C::B_S + x, s_done[x] & 1, WAIT_NS);
-            if (pv_done[x] >= 0)
-                mbar_wait(bars + C::B_PV + 2 * x + (pv_done[x] & 1), (pv_done[x] >> 1) & 1, WAIT_NS);
+            for (int x = 0; x < NT; ++x) {
+                if (sj[x] > pj[x]) mbar_wait(bars + C::B_S + x, (sj[x] - 1) & 1, WAIT_NS);
+                if (pj[x] > 0) mbar_wait(bars + C::B_PV + 2 * x + ((pj[x] - 1) & 1), ((pj[x] - 1) >> 1) & 1, WAIT_NS);
+            }
+            if (freed > 0) mbar_wait(bars + C::B_FREE + (freed - 1) % C::NS, ((freed - 1) / C::NS) & 1, WAIT_NS);
         }
-        if (!fail && n > 0) {
-            const int vi = v_idx(n - 1);
-            mbar_wait(bars + C::B_FREE + vi % C::NS, (vi / C::NS) & 1, WAIT_NS);
-        }
+        __syncwarp();
     } else {
         // --- rows ----------------------------------------------------------
         const int x = warp >> 2, r = tid;  // row tile; row of the block
@@ -342,6 +328,21 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::arrive(bars + C::B_SF + x);
+            if (valid < UK) {
+                // V's rows past the last key hold whatever the memory held, and
+                // 0 x NaN must not be formed: they are cleared before the
+                // weights are announced (by each row tile's warps: the same zeros)
+                if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_FULL + (j + 1) % C::NS, ((j + 1) / C::NS) & 1, WAIT_NS))) {
+                    fail = true;
+                    break;
+                }
+                unsigned char* vt = ring + ((j + 1) % C::NS) * 2 * C::KV_BYTES;
+                for (int e = tid & 127; e < (UK - valid) * 8 * NSUB; e += 128) {
+                    const int sub = e / ((UK - valid) * 8), w = e % ((UK - valid) * 8);
+                    *reinterpret_cast<uint4*>(vt + sub * UK * 128 + valid * 128 + w * 16) = make_uint4(0, 0, 0, 0);
+                }
+                ptx::fence_proxy_async();
+            }
             if (valid < UK || (!pre && k0 + UK > lim_warp)) {
                 const int end = pre ? valid : min(valid, lim - k0);
 #pragma unroll
@@ -388,12 +389,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                 w[u] = *reinterpret_cast<uint32_t*>(&h2);
             }
             l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-            // P's slot is free once the product of tile j - 2 is done
-            if (j >= 2 && __any_sync(FULL_MASK, !mbar_wait(bars + C::B_PV + 2 * x + (j & 1), ((j >> 1) - 1) & 1, WAIT_NS))) {
-                fail = true;
-                break;
-            }
-            tc::fence_after();
+            // (P's slot is free: the commit behind S of tile j covers the product
+            // of tile j - 2)
             tc::st32(t_s + UK + (j & 1) * 32, w);
             tc::st_wait();
             tc::fence_before();
