@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(View a, int ptiles, in
         seq_row(r, sq, i);
         const int64_t row = row_of(a, sq, hk, i);
         // (a sum that is NaN, of NaN logits alone, must not pass for an empty row)
-        if (lane == 0) a.part_ml[slot * R + row] = make_float2(ls != ls && m[u] == -INFINITY ? 0.f : m[u], ls);
+        if (lane == 0) a.part_ml[ml_index(a, row, slot)] = make_float2(ls != ls && m[u] == -INFINITY ? 0.f : m[u], ls);
         float* po = a.part_o + (slot * R + row) * D + lane * V;
 #pragma unroll
         for (int c = 0; c < V; ++c) po[c] = o[u][c];
@@ -297,87 +297,140 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(View a, int ptiles, in
 // joining the partial results; accumulated weights from kept logits
 // ---------------------------------------------------------------------------
 
-// Blocks [0, row_blocks): one warp per row joins its slots and writes the
-// output.  Blocks beyond: one (sequence, KV head, 256 slots) each, weight +=
-// the kept logits' weights over the rows, in row order.
+// A row's partial results as the calling warp holds them: lane j % 32,
+// register j / 32 has 2^(m_j - M) of slot j (0 where it was not written).
+struct RowJoin {
+    float f[2 * MAX_SPLITS / 32];
+    float M, L;  // maximum and sum over the slots
+};
+// The loads of a row's (max, sum) pairs go out together, and with those of
+// the lengths that say which of them were written.
+__device__ __forceinline__ RowJoin join_row(const View& a, int64_t row, int pk, int ok) {
+    const int lane = threadIdx.x & 31, ns = a.np + a.no;
+    constexpr int N = 2 * MAX_SPLITS / 32;
+    float2 ml[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        const int j = u * 32 + lane;
+        ml[u] = j < ns ? a.part_ml[ml_index(a, row, j)] : make_float2(-INFINITY, 0.f);
+    }
+    RowJoin r;
+    r.M = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        if (u * 32 >= ns) break;
+        if (!slot_valid(a, u * 32 + lane, pk, ok)) ml[u] = make_float2(-INFINITY, 0.f);
+        r.M = fmaxf(r.M, ml[u].x);
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) r.M = fmaxf(r.M, __shfl_xor_sync(FULL_MASK, r.M, off));
+    r.L = 0.f;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        r.f[u] = 0.f;
+        if (u * 32 >= ns) continue;
+        if (ml[u].x != -INFINITY) {
+            r.f[u] = exp2f(ml[u].x - r.M);
+            r.L = fmaf(ml[u].y, r.f[u], r.L);
+        }
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) r.L += __shfl_xor_sync(FULL_MASK, r.L, off);
+    return r;
+}
+
+// Blocks [0, row_blocks): one warp per row joins its slots (eight slots'
+// loads in flight) and writes the output.  Blocks beyond: `per` slots of one
+// (sequence, KV head) each; weight += the kept logits' weights, in row order.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ View a, int row_blocks) {
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ View a, int row_blocks, int per) {
     __shared__ float2 ml_s[STREAM_ROWS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t R = (int64_t)a.S * a.H * a.T;
-    const int ns = a.np + a.no;
-    ptx::grid_dep_wait();
-    auto row_max_sum = [&](int64_t row, int pk, int ok, float& M, float& L) {
-        M = -INFINITY;
-        for (int j = lane; j < ns; j += 32)
-            if (slot_valid(a, j, pk, ok)) M = fmaxf(M, a.part_ml[j * R + row].x);
-#pragma unroll
-        for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, off));
-        L = 0.f;
-        if (M != -INFINITY)
-            for (int j = lane; j < ns; j += 32)
-                if (slot_valid(a, j, pk, ok)) {
-                    const float2 x = a.part_ml[j * R + row];
-                    if (x.x != -INFINITY) L += x.y * exp2f(x.x - M);
-                }
-#pragma unroll
-        for (int off = 16; off; off >>= 1) L += __shfl_xor_sync(FULL_MASK, L, off);
-    };
+    const int R = a.S * a.H * a.T, ns = a.np + a.no;
     if ((int)blockIdx.x < row_blocks) {
-        const int64_t row = (int64_t)blockIdx.x * 8 + warp;
+        const int row = blockIdx.x * 8 + warp;
+        const int t = row % a.T, sh = row / a.T, h = sh % a.H, s = sh / a.H;
+        int pk = 0, ok = 0;
+        if (row < R) {
+            pk = prefix_len(a, prefix_of(a, s));
+            ok = own_len(a, s, h / a.rep);
+        }
+        ptx::grid_dep_wait();
         if (row >= R) return;
-        const int t = (int)(row % a.T), h = (int)(row / a.T % a.H), s = (int)(row / a.T / a.H);
-        const int pk = prefix_len(a, prefix_of(a, s)), ok = own_len(a, s, h / a.rep);
-        float M, L;
-        row_max_sum(row, pk, ok, M, L);
+        const RowJoin j = join_row(a, row, pk, ok);
         constexpr int V = D / 32;
         float acc[V];
 #pragma unroll
         for (int c = 0; c < V; ++c) acc[c] = 0.f;
-        const bool some = !(M == -INFINITY);
-        const float inv = some ? 1.f / L : 0.f;
-        if (some)
-            for (int j = 0; j < ns; ++j) {
-                if (!slot_valid(a, j, pk, ok)) continue;
-                const float mj = a.part_ml[j * R + row].x;
-                const float f = mj == -INFINITY ? 0.f : exp2f(mj - M);
-                if (f == 0.f) continue;
-                const float* po = a.part_o + (j * R + row) * D + lane * V;
+        const float* po = a.part_o + (int64_t)row * D + lane * V;
 #pragma unroll
-                for (int c = 0; c < V; ++c) acc[c] = fmaf(po[c], f, acc[c]);
+        for (int u = 0; u < 2 * MAX_SPLITS / 32; ++u) {
+            if (u * 32 >= ns) break;
+            for (int e0 = 0; e0 < 32 && u * 32 + e0 < ns; e0 += 8) {
+                float x[8][V], f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    f[e] = __shfl_sync(FULL_MASK, j.f[u], e0 + e);
+                    const float* p = po + (int64_t)(u * 32 + e0 + e) * R * D;
+                    if constexpr (V == 4) {
+                        const float4 y = f[e] != 0.f ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        x[e][0] = y.x; x[e][1] = y.y; x[e][2] = y.z; x[e][3] = y.w;
+                    } else {
+                        const float2 y = f[e] != 0.f ? *reinterpret_cast<const float2*>(p) : make_float2(0.f, 0.f);
+                        x[e][0] = y.x; x[e][1] = y.y;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+#pragma unroll
+                    for (int c = 0; c < V; ++c) acc[c] = fmaf(x[e][c], f[e], acc[c]);
             }
+        }
+        const bool some = !(j.M == -INFINITY);
+        const float inv = some ? 1.f / j.L : 0.f;
         T* orow = static_cast<T*>(a.out) + s * a.os[0] + h * a.os[1] + t * a.os[2] + lane * V;
 #pragma unroll
-        for (int c = 0; c < V; ++c) from_float(orow[c], acc[c] * inv);
+        for (int c = 0; c < V; ++c) acc[c] *= inv;
+        if constexpr (sizeof(T) == 4) {
+            if constexpr (V == 4) *reinterpret_cast<float4*>(orow) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            else *reinterpret_cast<float2*>(orow) = make_float2(acc[0], acc[1]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < V; c += 2)
+                *reinterpret_cast<__nv_bfloat162*>(orow + c) = __floats2bfloat162_rn(acc[c], acc[c + 1]);
+        }
         if (lane == 0) {
-            const float l2 = some ? M + log2f(L) : -INFINITY;
+            const float l2 = some ? j.M + log2f(j.L) : -INFINITY;
             if (a.lse) a.lse[row] = l2 * 0.6931471805599453f;
             if (a.row_lse) a.row_lse[row] = l2;
         }
         return;
     }
-    const int chunks = (a.cap + 255) / 256;
+    const int chunks = (a.cap + per - 1) / per;
     const int b = blockIdx.x - row_blocks, sh = b / chunks;
     const int s = sh / a.Hk, hk = sh % a.Hk, rps = a.rep * a.T;
     const int n = own_len(a, s, hk);
-    const int j0 = b % chunks * 256;
-    if (j0 >= n) return;
     const int pk = prefix_len(a, prefix_of(a, s));
+    const int j0 = b % chunks * per;
+    ptx::grid_dep_wait();
+    if (j0 >= n) return;
     for (int i = warp; i < rps; i += 8) {
-        float M, L;
-        row_max_sum(row_of(a, s, hk, i), pk, n, M, L);
-        if (lane == 0) ml_s[i] = make_float2(M, M == -INFINITY ? 0.f : 1.f / L);
+        const RowJoin j = join_row(a, row_of(a, s, hk, i), pk, n);
+        if (lane == 0) ml_s[i] = make_float2(j.M, j.M == -INFINITY ? 0.f : 1.f / j.L);
     }
     __syncthreads();
-    const int j = j0 + threadIdx.x;
-    if (j >= n) return;
-    const float* lg = a.logit + (int64_t)sh * rps * a.lcap + j;
-    float sum = 0.f;
-    for (int i = 0; i < rps; ++i) {
-        const float2 x = ml_s[i];
-        if (x.x != -INFINITY) sum += exp2f(lg[(int64_t)i * a.lcap] - x.x) * x.y;
+    const float* lg = a.logit + (int64_t)sh * rps * a.lcap;
+    float* w = a.weight + (int64_t)sh * a.cap;
+    for (int j = j0 + threadIdx.x; j < min(n, j0 + per); j += 256) {
+        float sum = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < rps; ++i) {
+            const float x = lg[(int64_t)i * a.lcap + j];
+            const float2 y = ml_s[i];
+            if (y.x != -INFINITY) sum += exp2f(x - y.x) * y.y;
+        }
+        w[j] += sum;
     }
-    a.weight[(int64_t)sh * a.cap + j] += sum;
 }
 
 // ---------------------------------------------------------------------------
@@ -484,7 +537,8 @@ cudaError_t launch_attend_simt(const View& a, int dtype, int d, cudaStream_t st)
 
 cudaError_t launch_combine(const View& a, int dtype, int d, bool dependent, cudaStream_t st) {
     const int64_t R = (int64_t)a.S * a.H * a.T, rb = (R + 7) / 8;
-    const int64_t blocks = rb + (a.logit ? (int64_t)a.S * a.Hk * ((a.cap + 255) / 256) : 0);
+    const int per = a.cap > 1024 ? 1024 : 256;
+    const int64_t blocks = rb + (a.logit ? (int64_t)a.S * a.Hk * ((a.cap + per - 1) / per) : 0);
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     return by_type(dtype, d, [&](auto tag, auto dim) {
         using E = decltype(tag);
@@ -497,7 +551,7 @@ cudaError_t launch_combine(const View& a, int dtype, int d, bool dependent, cuda
         at[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
         cfg.numAttrs = dependent ? 1 : 0;
-        return cudaLaunchKernelEx(&cfg, combine_kernel<E, decltype(dim)::value>, a, (int)rb);
+        return cudaLaunchKernelEx(&cfg, combine_kernel<E, decltype(dim)::value>, a, (int)rb, per);
     });
 }
 

@@ -45,7 +45,7 @@ struct View {
     int32_t np, no;
     // 1: the slots are no pieces of one list of 64-key tiles, the prefix's and then the own ones (np is 0)
     int32_t listed;
-    float2* part_ml;  // [np + no][R] (max, sum)
+    float2* part_ml;  // [R][np + no] (max, sum)
     float* part_o;    // [np + no][R][d]
     float* logit;     // [S][Hk][rep T][lcap] exp2-domain logits of the own keys (few rows, accumulate)
     int32_t lcap;     // capacity rounded up to 4
@@ -91,6 +91,7 @@ __device__ __forceinline__ bool slot_valid(const View& a, int j, int pk, int ok)
 __device__ __forceinline__ int64_t row_index(const View& a, int s, int h, int t) {
     return ((int64_t)s * a.H + h) * a.T + t;
 }
+__device__ __forceinline__ int64_t ml_index(const View& a, int64_t row, int slot) { return row * (a.np + a.no) + slot; }
 // Rows of one (sequence, KV head) are numbered i = t * rep + (query head within the KV head).
 __device__ __forceinline__ int64_t row_of(const View& a, int s, int hk, int i) {
     return row_index(a, s, hk * a.rep + i % a.rep, i / a.rep);

@@ -214,16 +214,16 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
             if (l[u] != l[u] && m[u] == -INFINITY) m[u] = 0.f;
         }
     }
-    const int64_t slot = (int64_t)(a.np + j) * R;
+    const int slot = a.np + j;
     if constexpr (WPH == 1) {
         if (work) {
 #pragma unroll
             for (int u = 0; u < NT; ++u) {
                 const int i = g + 8 * u;
                 if (i >= rps) continue;
-                const int64_t row = slot + row_of(a, s, hk, i);
-                if ((lane & 3) == 0) a.part_ml[row] = make_float2(m[u], l[u]);
-                float* po = a.part_o + row * D + q2;
+                const int64_t row = row_of(a, s, hk, i);
+                if ((lane & 3) == 0) a.part_ml[ml_index(a, row, slot)] = make_float2(m[u], l[u]);
+                float* po = a.part_o + (slot * R + row) * D + q2;
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c)
                     *reinterpret_cast<float2*>(po + c * 8) = make_float2(o[c][2 * u], o[c][2 * u + 1]);
@@ -266,9 +266,9 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
                         acc.w = fmaf(z.w, f, acc.w);
                     }
                 }
-                const int64_t row = slot + row_of(a, s, hk, i);
-                *reinterpret_cast<float4*>(a.part_o + row * D + c) = acc;
-                if (c == 0) a.part_ml[row] = make_float2(M, L);
+                const int64_t row = row_of(a, s, hk, i);
+                *reinterpret_cast<float4*>(a.part_o + (slot * R + row) * D + c) = acc;
+                if (c == 0) a.part_ml[ml_index(a, row, slot)] = make_float2(M, L);
             }
         }
     }

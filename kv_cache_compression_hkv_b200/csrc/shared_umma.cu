@@ -84,6 +84,42 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
     ptx::grid_dep_trigger();
     // what this block works on
     int hk, s = 0, g, first, rows, piece, p_tiles, t0, t1, p_len, n_own = 0, p_lo = 0;
+    // this thread's row (warps of the rows): sequence, row within (sequence, KV head), query head, query
+    int sq = 0, ri = 0, h = 0, t = 0;
+    bool live = false;
+    constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte pieces of a row; rows a warp covers at once
+    // Where piece c of row r of a row tile lies in the swizzled K-major tile.
+    auto q_off = [](int r, int c) { return (c / 8) * (QT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
+    // Starts the copies of the warp's rows of Q into the swizzled tile, whole
+    // rows at a time, so that they run while the lengths are looked up.
+    auto load_q = [&]() {
+        if (warp >= 4 * NT) return;
+        live = tid < rows;
+        if (live) {
+            if constexpr (MODE == 0) {
+                sq = s;
+                ri = first + tid;
+            } else {
+                const int f = first + tid;
+                sq = list[f / rps - first / rps];
+                ri = f % rps;
+            }
+        }
+        h = hk * a.rep + ri % a.rep;
+        t = ri / a.rep;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+        const int64_t at = live ? sq * a.qs[0] + h * a.qs[1] + t * a.qs[2] : -1;
+        const uint32_t tile = smem_u32(q_s + (warp >> 2) * C::Q_BYTES);
+#pragma unroll
+        for (int e = 0; e < CH; ++e) {
+            const int r = e * RPI + lane / CH, c = lane % CH;
+            const int64_t o = __shfl_sync(FULL_MASK, at, r);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile + q_off((warp & 3) * 32 + r, c)),
+                         "l"(q + (o < 0 ? 0 : o) + c * 8), "r"(o < 0 ? 0 : 16)
+                         : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     if constexpr (MODE == 0) {
         // longest row tiles (the last queries) first
         const int b = blockIdx.x, per = a.S * a.Hk * splits;
@@ -94,6 +130,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
         hk = sh % a.Hk;
         first = tile * C::ROWS;
         rows = min(C::ROWS, rps - first);
+        load_q();
         g = prefix_of(a, s);
         p_len = prefix_len(a, g);
         n_own = own_len(a, s, hk);
@@ -102,17 +139,24 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
         const int per_piece = (all + splits - 1) / splits;
         t0 = min(all, piece * per_piece);
         t1 = min(all, t0 + per_piece);
-        if (splits > 1 && t0 >= t1) return;  // combine_kernel knows
+        if (splits > 1 && t0 >= t1) {  // combine_kernel knows
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            return;
+        }
     } else {
         const int b = blockIdx.x;
         piece = b % a.np;
         hk = b / a.np % a.Hk;
         if (!find_prefix_tile(a, b / a.np / a.Hk, C::ROWS, g, first, rows, reinterpret_cast<int*>(ring), res, list))
             return;
+        load_q();
         p_len = prefix_len(a, g);
         int lo, hi;
         split_range(p_len, a.np, piece, lo, hi);
-        if (lo >= hi) return;
+        if (lo >= hi) {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            return;
+        }
         p_lo = lo;
         p_len = hi;
         ptx::fence_proxy_async();  // (the ring held the counts just now)
@@ -275,42 +319,26 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
         __syncwarp();
     } else {
         // --- rows ----------------------------------------------------------
-        const int x = warp >> 2, r = tid;  // row tile; row of the block
-        const bool live = r < rows;
-        int sq = s, i = 0;
-        if (live) {
-            if constexpr (MODE == 0) {
-                i = first + r;
-            } else {
-                const int f = first + r;
-                sq = list[f / rps - first / rps];
-                i = f % rps;
+        const int x = warp >> 2;  // row tile
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (a.qscale < 0.f) {
+            // negated where the scale is negative (exact), so that the
+            // reference maximum is of the scaled logits: every lane the pieces it copied
+            for (int e = 0; e < CH; ++e) {
+                uint4* w = reinterpret_cast<uint4*>(q_s + x * C::Q_BYTES + q_off((warp & 3) * 32 + e * RPI + lane / CH, lane % CH));
+                uint4 y = *w;
+                y.x ^= 0x80008000u; y.y ^= 0x80008000u; y.z ^= 0x80008000u; y.w ^= 0x80008000u;
+                *w = y;
             }
         }
-        const int h = hk * a.rep + i % a.rep, t = i / a.rep;
-        {
-            // Q into the swizzled tile (negated where the scale is negative:
-            // exact, and the reference maximum is then of the scaled logits)
-            const uint32_t flip = a.qscale < 0.f ? 0x80008000u : 0u;
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + sq * a.qs[0] +
-                                                              h * a.qs[1] + t * a.qs[2]);
-            const int row = r & 127;
-            unsigned char* dst = q_s + x * C::Q_BYTES + row * 128;
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                uint4 w = live ? src[c] : make_uint4(0, 0, 0, 0);
-                w.x ^= flip; w.y ^= flip; w.z ^= flip; w.w ^= flip;
-                *reinterpret_cast<uint4*>(dst + (c / 8) * (QT * 128) + (((c & 7) ^ (row & 7)) << 4)) = w;
-            }
-            ptx::fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) tc::arrive(bars + C::B_Q);
-        }
+        ptx::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) tc::arrive(bars + C::B_Q);
         const float c = fabsf(a.qscale);
         const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t t_s = t_lane + x * 128, t_o = t_lane + C::O_COL + x * D;
         // own keys this row sees; rows past the last one compute on zeros
-        const int lim = MODE == 0 ? (live ? own_limit(a, n_own, i) : 0x7fffffff) : 0;
+        const int lim = MODE == 0 ? (live ? own_limit(a, n_own, ri) : 0x7fffffff) : 0;
         const int lim_warp = __shfl_sync(FULL_MASK, lim, 0);  // the least of the warp's
         const int nt = NT == 2 ? (x == 0 ? nx[0] : nx[NT - 1]) : nx[0];
         float m = -INFINITY, l = 0.f;  // reference maximum (times c) and sum
@@ -407,32 +435,55 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
             const bool some = nt > 0 && !(m == -INFINITY && l == 0.f);
             const bool final = MODE == 0 && splits == 1;
             const float f = !final ? 1.f : some ? 1.f / l : 0.f;
+            // The rows go out through Q's place (every product that read it is
+            // done), 2 D bytes of a row at a time, so that a warp stores whole
+            // rows and not 16 bytes of 32 of them.
+            const int64_t dst = !live ? -1 : final ? sq * a.os[0] + h * a.os[1] + t * a.os[2] : (piece * R + row) * D;
+            unsigned char* tile = q_s + x * C::Q_BYTES;
+            constexpr int FW = D / 2;  // fp32 values of a pass
 #pragma unroll
-            for (int c0 = 0; c0 < D; c0 += 32) {
-                uint32_t o[32];
-                if (nt > 0) {
-                    tc::ld32(t_o + c0, o);
-                    tc::ld_wait();
-                }
+            for (int pass = 0; pass < 2; ++pass) {
+                if (final && pass == 1) break;
+                __syncwarp();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = some ? __float_as_uint(__uint_as_float(o[e]) * f) : 0u;
-                if (!live) continue;
-                if (final) {
-                    __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) + sq * a.os[0] + h * a.os[1] + t * a.os[2] + c0;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * u]), __uint_as_float(o[e + 2 * u + 1]));
-                            w[u] = *reinterpret_cast<uint32_t*>(&h2);
-                        }
-                        *reinterpret_cast<uint4*>(orow + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    if (!final && c0 / FW != pass) continue;
+                    uint32_t o[32];
+                    if (nt > 0) {
+                        tc::ld32(t_o + c0, o);
+                        tc::ld_wait();
                     }
-                } else {
-                    uint4* po = reinterpret_cast<uint4*>(a.part_o + (piece * R + row) * D + c0);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) po[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    for (int e = 0; e < 32; ++e) o[e] = some ? __float_as_uint(__uint_as_float(o[e]) * f) : 0u;
+                    const int r = (warp & 3) * 32 + lane;
+                    if (final) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * u]), __uint_as_float(o[8 * e + 2 * u + 1]));
+                                w[u] = *reinterpret_cast<uint32_t*>(&h2);
+                            }
+                            *reinterpret_cast<uint4*>(tile + q_off(r, c0 / 8 + e)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<uint4*>(tile + q_off(r, (c0 - pass * FW) / 4 + e)) =
+                                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < CH; ++e) {
+                    const int r = e * RPI + lane / CH, c = lane % CH;
+                    const int64_t o = __shfl_sync(FULL_MASK, dst, r);
+                    const uint4 w = *reinterpret_cast<const uint4*>(tile + q_off((warp & 3) * 32 + r, c));
+                    if (o >= 0) {
+                        if (final) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + o + c * 8) = w;
+                        else *reinterpret_cast<uint4*>(a.part_o + o + pass * FW + c * 4) = w;
+                    }
                 }
             }
             if (live) {
@@ -441,7 +492,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                     if (a.lse) a.lse[row] = l2 * 0.6931471805599453f;
                     if (a.row_lse) a.row_lse[row] = l2;
                 } else {
-                    a.part_ml[piece * R + row] = make_float2(l != l && m == -INFINITY ? 0.f : m, l);
+                    a.part_ml[ml_index(a, row, piece)] = make_float2(l != l && m == -INFINITY ? 0.f : m, l);
                 }
             }
         }
