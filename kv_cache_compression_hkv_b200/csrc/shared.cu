@@ -7,7 +7,7 @@
 //     x_j = log2(e) scale q.k_j,   m = max x_j,   l = sum 2^(x_j - m),
 //     o = sum 2^(x_j - m) v_j / l,   weight_j += 2^(x_j - m) / l.
 // Keys are cut into ranges that different blocks take; each leaves (m, l,
-// sum 2^(x - m) v) of its range, all in fp32, and combine_kernel joins them:
+// sum 2^(x - m) v) of its range, all in fp32, and a last kernel joins them:
 // with M = max m_i, o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
 #include <math.h>
 
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(View a, int ptiles, in
         kst = a.ks[2];
         vst = a.vs[2];
     }
-    if (lo >= hi) return;  // combine_kernel knows
+    if (lo >= hi) return;  // the joining kernel knows
     const int o0 = first / rps;
     auto seq_row = [&](int r, int& sq, int& i) {  // row r of the tile -> sequence, row within (sequence, KV head)
         const int f = first + r;
@@ -339,16 +339,69 @@ __device__ __forceinline__ RowJoin join_row(const View& a, int64_t row, int pk, 
     return r;
 }
 
-// Blocks [0, row_blocks): one warp per row joins its slots (eight slots'
-// loads in flight) and writes the output.  Blocks beyond: `per` slots of one
-// (sequence, KV head) each; weight += the kept logits' weights, in row order.
+// The calling warp adds up the joined row's partial sums (eight slots' loads in
+// flight) and writes the row.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ View a, int row_blocks, int per) {
-    __shared__ float2 ml_s[STREAM_ROWS];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int R = a.S * a.H * a.T, ns = a.np + a.no;
+__device__ __forceinline__ void write_row(const View& a, const RowJoin& j, int64_t row, int s, int h, int t) {
+    constexpr int V = D / 32;
+    const int lane = threadIdx.x & 31, ns = a.np + a.no;
+    const int64_t R = (int64_t)a.S * a.H * a.T;
+    float acc[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) acc[c] = 0.f;
+    const float* po = a.part_o + row * D + lane * V;
+#pragma unroll
+    for (int u = 0; u < 2 * MAX_SPLITS / 32; ++u) {
+        if (u * 32 >= ns) break;
+        for (int e0 = 0; e0 < 32 && u * 32 + e0 < ns; e0 += 8) {
+            float x[8][V], f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                f[e] = __shfl_sync(FULL_MASK, j.f[u], e0 + e);
+                const float* p = po + (u * 32 + e0 + e) * R * D;
+                if constexpr (V == 4) {
+                    const float4 y = f[e] != 0.f ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    x[e][0] = y.x; x[e][1] = y.y; x[e][2] = y.z; x[e][3] = y.w;
+                } else {
+                    const float2 y = f[e] != 0.f ? *reinterpret_cast<const float2*>(p) : make_float2(0.f, 0.f);
+                    x[e][0] = y.x; x[e][1] = y.y;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int c = 0; c < V; ++c) acc[c] = fmaf(x[e][c], f[e], acc[c]);
+        }
+    }
+    const bool some = !(j.M == -INFINITY);
+    const float inv = some ? 1.f / j.L : 0.f;
+    T* orow = static_cast<T*>(a.out) + s * a.os[0] + h * a.os[1] + t * a.os[2] + lane * V;
+#pragma unroll
+    for (int c = 0; c < V; ++c) acc[c] *= inv;
+    if constexpr (sizeof(T) == 4) {
+        if constexpr (V == 4) *reinterpret_cast<float4*>(orow) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        else *reinterpret_cast<float2*>(orow) = make_float2(acc[0], acc[1]);
+    } else {
+#pragma unroll
+        for (int c = 0; c < V; c += 2) *reinterpret_cast<__nv_bfloat162*>(orow + c) = __floats2bfloat162_rn(acc[c], acc[c + 1]);
+    }
+    if (lane == 0) {
+        const float l2 = some ? j.M + log2f(j.L) : -INFINITY;
+        if (a.lse) a.lse[row] = l2 * 0.6931471805599453f;
+        if (a.row_lse) a.row_lse[row] = l2;
+    }
+}
+
+// Blocks [0, row_blocks): one warp per row.  Blocks beyond: 128 slots of one
+// (sequence, KV head) each, weight += the kept logits' weights in row order;
+// the logits are on their way while the block joins the head's rows for itself
+// (waiting for the other blocks' rows instead would cost another launch).
+template <typename T, int D, int MAXR>
+__global__ void __launch_bounds__(128, 8) combine_kernel(const __grid_constant__ View a, int row_blocks) {
+    __shared__ float2 ml_s[MAXR];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if ((int)blockIdx.x < row_blocks) {
-        const int row = blockIdx.x * 8 + warp;
+        const int R = a.S * a.H * a.T, row = blockIdx.x * 4 + warp;
         const int t = row % a.T, sh = row / a.T, h = sh % a.H, s = sh / a.H;
         int pk = 0, ok = 0;
         if (row < R) {
@@ -358,79 +411,40 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Vi
         ptx::grid_dep_wait();
         if (row >= R) return;
         const RowJoin j = join_row(a, row, pk, ok);
-        constexpr int V = D / 32;
-        float acc[V];
-#pragma unroll
-        for (int c = 0; c < V; ++c) acc[c] = 0.f;
-        const float* po = a.part_o + (int64_t)row * D + lane * V;
-#pragma unroll
-        for (int u = 0; u < 2 * MAX_SPLITS / 32; ++u) {
-            if (u * 32 >= ns) break;
-            for (int e0 = 0; e0 < 32 && u * 32 + e0 < ns; e0 += 8) {
-                float x[8][V], f[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    f[e] = __shfl_sync(FULL_MASK, j.f[u], e0 + e);
-                    const float* p = po + (int64_t)(u * 32 + e0 + e) * R * D;
-                    if constexpr (V == 4) {
-                        const float4 y = f[e] != 0.f ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        x[e][0] = y.x; x[e][1] = y.y; x[e][2] = y.z; x[e][3] = y.w;
-                    } else {
-                        const float2 y = f[e] != 0.f ? *reinterpret_cast<const float2*>(p) : make_float2(0.f, 0.f);
-                        x[e][0] = y.x; x[e][1] = y.y;
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-#pragma unroll
-                    for (int c = 0; c < V; ++c) acc[c] = fmaf(x[e][c], f[e], acc[c]);
-            }
-        }
-        const bool some = !(j.M == -INFINITY);
-        const float inv = some ? 1.f / j.L : 0.f;
-        T* orow = static_cast<T*>(a.out) + s * a.os[0] + h * a.os[1] + t * a.os[2] + lane * V;
-#pragma unroll
-        for (int c = 0; c < V; ++c) acc[c] *= inv;
-        if constexpr (sizeof(T) == 4) {
-            if constexpr (V == 4) *reinterpret_cast<float4*>(orow) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            else *reinterpret_cast<float2*>(orow) = make_float2(acc[0], acc[1]);
-        } else {
-#pragma unroll
-            for (int c = 0; c < V; c += 2)
-                *reinterpret_cast<__nv_bfloat162*>(orow + c) = __floats2bfloat162_rn(acc[c], acc[c + 1]);
-        }
-        if (lane == 0) {
-            const float l2 = some ? j.M + log2f(j.L) : -INFINITY;
-            if (a.lse) a.lse[row] = l2 * 0.6931471805599453f;
-            if (a.row_lse) a.row_lse[row] = l2;
-        }
+        write_row<T, D>(a, j, row, s, h, t);
         return;
     }
-    const int chunks = (a.cap + per - 1) / per;
+    const int chunks = (a.cap + 127) / 128;
     const int b = blockIdx.x - row_blocks, sh = b / chunks;
     const int s = sh / a.Hk, hk = sh % a.Hk, rps = a.rep * a.T;
     const int n = own_len(a, s, hk);
+    if (b % chunks * 128 >= n) {
+        ptx::grid_dep_wait();
+        return;
+    }
     const int pk = prefix_len(a, prefix_of(a, s));
-    const int j0 = b % chunks * per;
+    const int j = b % chunks * 128 + tid;
+    float* w = a.weight + (int64_t)sh * a.cap + j;
+    const float old = j < n ? *w : 0.f;
     ptx::grid_dep_wait();
-    if (j0 >= n) return;
-    for (int i = warp; i < rps; i += 8) {
-        const RowJoin j = join_row(a, row_of(a, s, hk, i), pk, n);
-        if (lane == 0) ml_s[i] = make_float2(j.M, j.M == -INFINITY ? 0.f : 1.f / j.L);
+    float x[MAXR];
+    const float* lg = a.logit + (int64_t)sh * rps * a.lcap + j;
+#pragma unroll
+    for (int i = 0; i < MAXR; ++i) x[i] = i < rps && j < n ? lg[(int64_t)i * a.lcap] : -INFINITY;
+    for (int i = warp; i < rps; i += 4) {
+        const RowJoin r = join_row(a, row_of(a, s, hk, i), pk, n);
+        if (lane == 0) ml_s[i] = make_float2(r.M, r.M == -INFINITY ? 0.f : 1.f / r.L);
     }
     __syncthreads();
-    const float* lg = a.logit + (int64_t)sh * rps * a.lcap;
-    float* w = a.weight + (int64_t)sh * a.cap;
-    for (int j = j0 + threadIdx.x; j < min(n, j0 + per); j += 256) {
-        float sum = 0.f;
-#pragma unroll 8
-        for (int i = 0; i < rps; ++i) {
-            const float x = lg[(int64_t)i * a.lcap + j];
+    if (j >= n) return;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < MAXR; ++i)
+        if (i < rps) {
             const float2 y = ml_s[i];
-            if (y.x != -INFINITY) sum += exp2f(x - y.x) * y.y;
+            if (y.x != -INFINITY) sum += exp2f(x[i] - y.x) * y.y;
         }
-        w[j] += sum;
-    }
+    *w = old + sum;
 }
 
 // ---------------------------------------------------------------------------
@@ -536,22 +550,25 @@ cudaError_t launch_attend_simt(const View& a, int dtype, int d, cudaStream_t st)
 }
 
 cudaError_t launch_combine(const View& a, int dtype, int d, bool dependent, cudaStream_t st) {
-    const int64_t R = (int64_t)a.S * a.H * a.T, rb = (R + 7) / 8;
-    const int per = a.cap > 1024 ? 1024 : 256;
-    const int64_t blocks = rb + (a.logit ? (int64_t)a.S * a.Hk * ((a.cap + per - 1) / per) : 0);
+    const int64_t R = (int64_t)a.S * a.H * a.T, rb = (R + 3) / 4;
+    const int64_t blocks = rb + (a.logit ? (int64_t)a.S * a.Hk * ((a.cap + 127) / 128) : 0);
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     return by_type(dtype, d, [&](auto tag, auto dim) {
         using E = decltype(tag);
+        constexpr int D = decltype(dim)::value;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)blocks);
-        cfg.blockDim = dim3(256);
+        cfg.blockDim = dim3(128);
         cfg.stream = st;
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
         cfg.numAttrs = dependent ? 1 : 0;
-        return cudaLaunchKernelEx(&cfg, combine_kernel<E, decltype(dim)::value>, a, (int)rb, per);
+        const int rps = a.rep * a.T;
+        if (rps == 1) return cudaLaunchKernelEx(&cfg, combine_kernel<E, D, 1>, a, (int)rb);
+        if (rps <= 8) return cudaLaunchKernelEx(&cfg, combine_kernel<E, D, 8>, a, (int)rb);
+        return cudaLaunchKernelEx(&cfg, combine_kernel<E, D, STREAM_ROWS>, a, (int)rb);
     });
 }
 

@@ -3,6 +3,7 @@
 // results that the combining kernel joins.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -172,6 +173,11 @@ inline int64_t max_prefix_tiles(int S, int G, int rows_per_seq, int rt) {
 
 // Row tiles of 128 that a tensor-core block takes: two as soon as one (sequence, KV head) has them.
 inline int umma_row_tiles(int64_t rows_per_seq) { return rows_per_seq > 128 ? 2 : 1; }
+
+// Tensor map of bf16 rows [n2][n1][n0] of d elements at strides st (elements:
+// outermost, middle, row): boxes of 64 columns x box rows, 128-byte swizzle,
+// zeros past the ends.
+bool make_map(CUtensorMap* m, const void* ptr, int d, int n0, int n1, int n2, const int64_t* st, int box);
 
 // launchers (host)
 cudaError_t prepare_shared_umma();

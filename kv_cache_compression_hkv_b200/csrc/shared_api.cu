@@ -112,10 +112,10 @@ Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char
         a.no = items >= 148 ? 1 : splits(nt == 2 ? 148 : 296, items, (int64_t)a.cap + (a.G ? a.pcap : 0), 256);
     } else if (p.stream) {
         // eight warps fit an SM: a head goes to as many as fill the GPU, one or several blocks of four
-        const int64_t warps = (148 * 8 + heads - 1) / heads, most = ((int64_t)a.cap + 31) / 32;
+        const int64_t warps = (148 * 8 + heads / 2) / heads, most = ((int64_t)a.cap + 31) / 32;
         const int64_t n = warps < most ? warps : most;
-        p.warps_per_head = n > 1 ? 4 : 1;
-        a.no = n > 4 ? splits((n + 3) / 4, 1, a.cap, 64) : 1;
+        p.warps_per_head = n > 2 ? 4 : 1;
+        a.no = splits(n > 2 ? (n + 2) / 4 : n, 1, a.cap, 64);
     } else {
         a.no = splits(148 * 6, heads * ((rps + 15) / 16), a.cap, 128);
     }

