@@ -7,7 +7,6 @@ and decide what an eviction drops.  This module marshals arguments only.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 from dataclasses import dataclass
 
@@ -91,6 +90,8 @@ class SharedPrefixCache:
                 raise ValueError(f"{name}: expected a contiguous tensor")
             return x
 
+        self._dtype = dt
+        self._off16 = 16 // dt.itemsize - 1  # bits that strides on 16-byte boundaries leave clear
         i32, f32 = torch.int32, torch.float32
         self.k = own(k, "k", (S, Hk, cap, d), dt, True)
         self.v = own(v, "v", (S, Hk, cap, d), dt, True)
@@ -125,31 +126,44 @@ class SharedPrefixCache:
         self._evict_bytes = n.value
         self._attend_bytes = {}  # (T, accumulate) -> scratch bytes
 
-    # -- argument checks -----------------------------------------------------
+    # -- argument checks (each a few hundred nanoseconds: a decode step's calls
+    #    take the GPU ten to twenty microseconds) ------------------------------
     def _rows(self, x, name):
         st = x.stride()
-        es = 4 if self.cfg.dtype == DTYPE_F32 else 2
-        if st[3] != 1 or any(s < 0 or s * es % 16 for s in st[:3]) or x.data_ptr() % 16:
+        if st[3] != 1 or (st[0] | st[1] | st[2]) & self._off16 or x.data_ptr() & 15:
             raise ValueError(f"{name}: rows of d contiguous elements on 16-byte boundaries, got strides {st}")
+        return _Strides(st[0], st[1], st[2])
 
     def _tensor(self, x, name, heads):
+        """Checks a [S, heads, T, d] tensor; its strides for the C call."""
+        if isinstance(x, torch.Tensor) and x.dtype == self._dtype and x.dim() == 4:
+            n0, n1, _, n3 = x.shape
+            c = self.cfg
+            if n0 == c.num_seqs and n1 == heads and n3 == c.head_dim and x.device == self.device:
+                return self._rows(x, name)
         c = self.cfg
-        if not isinstance(x, torch.Tensor) or x.device != self.device or x.dtype != c.torch_dtype or \
-                x.dim() != 4 or x.shape[0] != c.num_seqs or x.shape[1] != heads or x.shape[3] != c.head_dim:
-            raise ValueError(f"{name}: expected a {c.torch_dtype} tensor [{c.num_seqs}, {heads}, T, {c.head_dim}] "
-                             f"on {self.device}")
-        self._rows(x, name)
+        raise ValueError(f"{name}: expected a {c.torch_dtype} tensor [{c.num_seqs}, {heads}, T, {c.head_dim}] on "
+                         f"{self.device}")
 
-    def _on(self, stream):
-        """(context, stream handle): allocations and launches on `stream`."""
+    def _call(self, fn, what, stream, args):
+        """fn(*args, stream) with (args, scratch) = args(): allocations and
+        launches on `stream` (the current one by default) of the cache's
+        device.  The scratch is held until the launches are enqueued."""
+        index = self.device.index
         if stream is None:
-            h = torch.cuda.current_stream(self.device).cuda_stream
-            if torch.cuda.current_device() == self.device.index:
-                return contextlib.nullcontext(), h
-            return torch.cuda.device(self.device), h
+            if torch._C._cuda_getDevice() == index:
+                a, _scratch = args()
+                _check(fn(*a, torch._C._cuda_getCurrentRawStream(index)), what)
+            else:
+                with torch.cuda.device(index):
+                    a, _scratch = args()
+                    _check(fn(*a, torch._C._cuda_getCurrentRawStream(index)), what)
+            return
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-        return torch.cuda.stream(stream), stream.cuda_stream
+        with torch.cuda.stream(stream):
+            a, _scratch = args()
+            _check(fn(*a, stream.cuda_stream), what)
 
     # -- calls ---------------------------------------------------------------
     def append(self, k_t, v_t, weight_t=None, stream=None):
@@ -157,23 +171,20 @@ class SharedPrefixCache:
         [S, Hkv, T] fp32, their accumulated weights (default 0).  A head
         without T free slots is left as it was (see check)."""
         c = self.cfg
-        self._tensor(k_t, "k_t", c.num_kv_heads)
-        self._tensor(v_t, "v_t", c.num_kv_heads)
+        ks = self._tensor(k_t, "k_t", c.num_kv_heads)
+        vs = self._tensor(v_t, "v_t", c.num_kv_heads)
         T = k_t.shape[2]
         if v_t.shape[2] != T or T > c.capacity:
             raise ValueError("k_t, v_t: as many tokens each, at most the capacity")
         if weight_t is not None and (weight_t.dtype != torch.float32 or weight_t.device != self.device or
-                                     tuple(weight_t.shape) != (c.num_seqs, c.num_kv_heads, T) or
+                                     weight_t.shape != (c.num_seqs, c.num_kv_heads, T) or
                                      not weight_t.is_contiguous()):
             raise ValueError("weight_t: expected a contiguous float32 [S, Hkv, T] tensor on the device")
         if T == 0:
             return
-        ctx, h = self._on(stream)
-        with ctx:
-            _check(lib().hkv_shared_append(self._ref, k_t.data_ptr(), _Strides(*k_t.stride()[:3]), v_t.data_ptr(),
-                                           _Strides(*v_t.stride()[:3]),
-                                           None if weight_t is None else weight_t.data_ptr(), T, h),
-                   "hkv_shared_append")
+        self._call(lib().hkv_shared_append, "hkv_shared_append", stream,
+                   lambda: ((self._ref, k_t.data_ptr(), ks, v_t.data_ptr(), vs,
+                             None if weight_t is None else weight_t.data_ptr(), T), None))
 
     def attend(self, q, out=None, lse=None, accumulate=True, scale=None, stream=None):
         """Attention of each sequence's newest T tokens (appended before):
@@ -183,38 +194,42 @@ class SharedPrefixCache:
         zeros and -inf.  accumulate adds to `weight` the softmax weights each
         own token received.  scale of the logits: 1 / sqrt(d) by default."""
         c = self.cfg
-        self._tensor(q, "q", c.num_heads)
+        qs = self._tensor(q, "q", c.num_heads)
         T = q.shape[2]
         if T < 1 or T > c.capacity:
             raise ValueError("q: between 1 token and the capacity")
-        if 0 in q.stride():
+        if not (qs[0] and qs[1] and qs[2]):
             raise ValueError("q: no repeated rows")
-        if scale is not None and not (scale != 0 and abs(scale) < float("inf")):
+        if scale is None:
+            scale = 0.0
+        elif not (scale != 0 and abs(scale) < float("inf")):
             raise ValueError("scale: a finite number other than 0")
         if out is not None:
             self._tensor(out, "out", c.num_heads)
             if out.shape != q.shape or 0 in out.stride():
                 raise ValueError("out: expected q's shape, no repeated rows")
         if lse is not None and (lse.dtype != torch.float32 or lse.device != self.device or
-                                tuple(lse.shape) != tuple(q.shape[:3]) or not lse.is_contiguous()):
+                                lse.shape != q.shape[:3] or not lse.is_contiguous()):
             raise ValueError("lse: expected a contiguous float32 [S, H, T] tensor on the device")
-        key = (T, bool(accumulate))
-        need = self._attend_bytes.get(key)
+        accumulate = int(bool(accumulate))
+        need = self._attend_bytes.get((T, accumulate))
         if need is None:
             n = C.c_size_t()
-            _check(lib().hkv_shared_attend_bytes(self._ref, T, int(key[1]), C.byref(n)), "hkv_shared_attend_bytes")
-            need = self._attend_bytes[key] = n.value
-        ctx, h = self._on(stream)
-        with ctx:
+            _check(lib().hkv_shared_attend_bytes(self._ref, T, accumulate, C.byref(n)), "hkv_shared_attend_bytes")
+            need = self._attend_bytes[(T, accumulate)] = n.value
+
+        def args():
+            nonlocal out, lse
             if out is None:
-                out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+                out = q.new_empty(q.shape)
             if lse is None:
-                lse = torch.empty(q.shape[:3], dtype=torch.float32, device=self.device)
-            scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
-            _check(lib().hkv_shared_attend(self._ref, q.data_ptr(), _Strides(*q.stride()[:3]), out.data_ptr(),
-                                           _Strides(*out.stride()[:3]), lse.data_ptr(), T,
-                                           0.0 if scale is None else float(scale), int(key[1]), scratch.data_ptr(),
-                                           need, h), "hkv_shared_attend")
+                lse = self.weight.new_empty(q.shape[:3])
+            scratch = self.lens.new_empty(need // 4)
+            so = out.stride()
+            return (self._ref, q.data_ptr(), qs, out.data_ptr(), _Strides(so[0], so[1], so[2]), lse.data_ptr(), T,
+                    float(scale), accumulate, scratch.data_ptr(), need), scratch
+
+        self._call(lib().hkv_shared_attend, "hkv_shared_attend", stream, args)
         return out, lse
 
     def evict(self, budgets, recent: int = 0, slack: int = 1, stream=None):
@@ -225,15 +240,16 @@ class SharedPrefixCache:
         move into the holes before it."""
         c = self.cfg
         if not isinstance(budgets, torch.Tensor) or budgets.dtype != torch.int32 or budgets.device != self.device or \
-                tuple(budgets.shape) != (c.num_seqs, c.num_kv_heads) or not budgets.is_contiguous():
+                budgets.shape != (c.num_seqs, c.num_kv_heads) or not budgets.is_contiguous():
             raise ValueError("budgets: expected a contiguous int32 [S, Hkv] tensor on the device")
         if recent < 0 or slack < 1:
             raise ValueError("recent at least 0, slack at least 1")
-        ctx, h = self._on(stream)
-        with ctx:
-            scratch = torch.empty(self._evict_bytes, dtype=torch.uint8, device=self.device)
-            _check(lib().hkv_shared_evict(self._ref, budgets.data_ptr(), recent, slack, scratch.data_ptr(),
-                                          self._evict_bytes, h), "hkv_shared_evict")
+
+        def args():
+            scratch = self.lens.new_empty(self._evict_bytes // 4)
+            return (self._ref, budgets.data_ptr(), recent, slack, scratch.data_ptr(), self._evict_bytes), scratch
+
+        self._call(lib().hkv_shared_evict, "hkv_shared_evict", stream, args)
 
     def check(self):
         """(code, detail) of the first error latched on the device (waits)."""
