@@ -193,8 +193,10 @@ cudaError_t launch_stream(const View& a, int d, int warps_per_head, bool depende
 // dependent: may be set up before the launch in front of it has ended
 cudaError_t launch_combine(const View& a, int dtype, int d, bool dependent, cudaStream_t st);
 cudaError_t launch_column_sums_simt(const View& a, int dtype, int d, cudaStream_t st);
+cudaError_t prepare_shared_evict();
+size_t evict_bytes(int heads, int cap);
 cudaError_t launch_evict(const View& a, int dtype, int d, const int32_t* budget, int recent, int slack,
-                         int32_t* holes, cudaStream_t st);
+                         unsigned char* scratch, cudaStream_t st);
 
 }  // namespace shared
 }  // namespace hkv

@@ -153,6 +153,7 @@ cudaError_t prepare() {
     if (ready.load() & bit) return cudaSuccess;
     e = hkv::shared::prepare_shared_umma();
     if (e == cudaSuccess) e = hkv::shared::prepare_shared_stream();
+    if (e == cudaSuccess) e = hkv::shared::prepare_shared_evict();
     if (e == cudaSuccess && dev < 64) ready.fetch_or(bit);
     return e;
 }
@@ -230,7 +231,7 @@ hkv_status hkv_shared_attend(const hkv_shared_cache* c, const void* q, const int
 
 hkv_status hkv_shared_evict_bytes(const hkv_shared_cache* c, size_t* bytes) {
     if (!bytes || !cache_ok(c)) return HKV_ERR_INVALID_ARG;
-    *bytes = (size_t)c->num_seqs * c->num_kv_heads * c->capacity * 4;
+    *bytes = align_up(hkv::shared::evict_bytes(c->num_seqs * c->num_kv_heads, c->capacity));
     return HKV_OK;
 }
 
@@ -243,8 +244,11 @@ hkv_status hkv_shared_evict(const hkv_shared_cache* c, const int32_t* budget, in
     if (scratch_bytes < need) return HKV_ERR_CAPACITY;
     if (!scratch || !aligned(scratch, kAlign)) return HKV_ERR_INVALID_ARG;
     View a = view_of(c);
-    return cuda_status(hkv::shared::launch_evict(a, c->dtype, c->head_dim, budget, recent, slack, (int32_t*)scratch,
-                                                 (cudaStream_t)stream));
+    cudaError_t e = prepare();
+    if (e == cudaSuccess)
+        e = hkv::shared::launch_evict(a, c->dtype, c->head_dim, budget, recent, slack, (unsigned char*)scratch,
+                                      (cudaStream_t)stream);
+    return cuda_status(e);
 }
 
 }  // extern "C"

@@ -3,14 +3,33 @@
 // A due head (len n >= budget B + slack) loses the E = n - B tokens lowest in
 // (recent, weight, position, slot).  The first two fields fold into 32 bits
 // that order like them (ordered float bits; all recent tokens share the
-// highest value), the position into 32 more: the E-th smallest of these
-// 64-bit keys is found by a most-significant-digit radix select, and among
-// tokens with that same key the lower slots go.
+// highest value) and the position into 32 more.  The E-th smallest of these
+// 64-bit keys is found digit by digit from the top (histograms of 11 or 10
+// bits in shared memory); as soon as at most CAND tokens are left to choose
+// from they are ranked against each other by (key, slot): at once in a short
+// head, after the first or second digit in a long one whose weights differ.
+// Tokens at or below the threshold are evicted.  The head's weights and
+// positions are read once, into shared memory where they fit.
+//
+// What bounds it: a short head (a few hundred tokens) the chain of block-wide
+// steps, so one small block a head and as many heads as fit at once; a long
+// one the rows that move, which a second launch spreads over the GPU.
+#include <algorithm>
+
 #include "kernels.h"
+#include "ptx.cuh"
 #include "shared.cuh"
 
 namespace hkv {
 namespace shared {
+
+namespace {
+
+constexpr int BINS = 2048;
+constexpr int CAND = 64;        // candidates ranked against each other (256 cost short heads four times the rest)
+constexpr int LIST = 512;       // moves whose slots stay in shared memory
+constexpr int SHORT_CAP = 2048; // capacities up to this: blocks of 128 threads that also move the rows
+constexpr int HELD_CAP = 24576; // capacities up to this: weights and positions in shared memory (192 KB)
 
 // Bits that order as (recent, weight): recent tokens highest, then NaN, then
 // the numbers (-0 as +0).
@@ -21,122 +40,318 @@ __device__ __forceinline__ uint32_t class_bits(float w, bool recent) {
     return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-constexpr int ET = 256;
+template <int THREADS> struct EvictSmem {
+    // bins a thread adds up lie PER apart, and a word further each thread
+    static constexpr int PER = BINS / THREADS;
+    int hist[BINS + THREADS];
+    __device__ int& bin_at(int b) { return hist[b + b / PER]; }
+    uint64_t cand_key[CAND];
+    int cand_slot[CAND];
+    int list[2 * LIST];
+    int warp_a[THREADS / 32], warp_b[THREADS / 32];
+    int newest, digit, below, n_cand, thr_slot;
+    uint64_t thr_key;
+};
 
-__device__ __forceinline__ int block_scan(int x, int* warp_sums, int& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int incl = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(FULL_MASK, incl, o);
-        if (lane >= o) incl += y;
-    }
-    __syncthreads();
-    if (lane == 31) warp_sums[warp] = incl;
-    __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < ET / 32; ++w) {
-        const int v = warp_sums[w];
-        if (w < warp) before += v;
-        all += v;
-    }
-    total = all;
-    return before + incl - x;
-}
-
-// One block per (sequence, KV head).
-__global__ void __launch_bounds__(ET) evict_simple_kernel(View a, const int32_t* __restrict__ budget, int recent,
-                                                          int slack, int row_bytes, int es,
-                                                          int32_t* __restrict__ holes) {
-    __shared__ int hist[256];
-    __shared__ int warp_sums[ET / 32];
-    __shared__ int newest_s, digit_s, below_s;
-    const int head = blockIdx.x, s = head / a.Hk, hk = head % a.Hk, tid = threadIdx.x;
-    const int n = own_len(a, s, hk), B = max(0, budget[head]);
-    if ((int64_t)n < (int64_t)B + slack) return;
-    const int E = n - B;
-    int32_t* pos = a.pos + (int64_t)head * a.cap;
-    float* weight = a.weight + (int64_t)head * a.cap;
-    if (tid == 0) newest_s = INT32_MIN;
-    __syncthreads();
-    int nw = INT32_MIN;
-    for (int i = tid; i < n; i += ET) nw = max(nw, pos[i]);
-    atomicMax(&newest_s, nw);
-    __syncthreads();
-    const int64_t newest = newest_s;
-    auto key = [&](int i) {
-        const int p = pos[i];
-        return ((uint64_t)class_bits(weight[i], newest - p < recent) << 32) | ((uint32_t)p ^ 0x80000000u);
-    };
-    // the E-th smallest key, digit by digit
-    uint64_t prefix = 0, mask = 0;
-    int want = E;
-    for (int shift = 56; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += ET) hist[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < n; i += ET) {
-            const uint64_t k = key(i);
-            if ((k & mask) == prefix) atomicAdd(hist + (int)(k >> shift & 255), 1);
-        }
-        __syncthreads();
-        int total;
-        const int c = hist[tid], below = block_scan(c, warp_sums, total);
-        if (below < want && want <= below + c) {
-            digit_s = tid;
-            below_s = below;
-        }
-        __syncthreads();
-        want -= below_s;
-        prefix |= (uint64_t)digit_s << shift;
-        mask |= (uint64_t)255 << shift;
-    }
-    // evicted: key < prefix, or key == prefix and among the first `want` of
-    // those by slot.  Holes (evicted below B) are listed in slot order; the
-    // survivors at or above B take them in slot order.
-    int32_t* hl = holes + (int64_t)head * a.cap;
-    int eq_seen = 0, n_holes = 0, n_movers = 0;
+// Moves rows (16-byte pieces), positions and weights from movers to holes:
+// entries first, first + step, ... of the lists.
+__device__ __forceinline__ void move_rows(const View& a, int head, const int* holes, const int* movers, int count,
+                                          int first, int step, int row_bytes, int es) {
+    const int s = head / a.Hk, hk = head % a.Hk;
     unsigned char* kb = static_cast<unsigned char*>(a.k) + (s * a.ks[0] + hk * a.ks[1]) * es;
     unsigned char* vb = static_cast<unsigned char*>(a.v) + (s * a.vs[0] + hk * a.vs[1]) * es;
-    for (int i0 = 0; i0 < n; i0 += ET) {
-        const int i = i0 + tid;
-        const uint64_t k = i < n ? key(i) : ~0ull;
-        const bool eq = i < n && k == prefix;
-        int total;
-        const int er = block_scan(eq, warp_sums, total);
-        const bool gone = i < n && (k < prefix || (eq && eq_seen + er < want));
-        eq_seen += total;
-        const bool hole = gone && i < B;
-        const int hr = block_scan(hole, warp_sums, total);
-        if (hole) hl[n_holes + hr] = i;
-        n_holes += total;
-        const bool mover = i < n && !gone && i >= B;
-        const int mr = block_scan(mover, warp_sums, total);
-        if (mover) hl[B + n_movers + mr] = i;
-        n_movers += total;
+    const int64_t kst = a.ks[2] * es, vst = a.vs[2] * es;
+    int32_t* pos = a.pos + (int64_t)head * a.cap;
+    float* weight = a.weight + (int64_t)head * a.cap;
+    const int pieces = row_bytes / 16, per = (int)blockDim.x / pieces;  // rows a block moves at once
+    const int c = threadIdx.x % pieces * 16, lead = threadIdx.x / pieces;
+    // four rows' pieces in flight a thread
+    for (int i0 = first * per * 4 + lead; i0 < count; i0 += step * per * 4) {
+        uint4 x[4], y[4];
+        int to[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * per;
+            to[u] = i < count ? holes[i] : -1;
+            if (to[u] < 0) continue;
+            const int from = movers[i];
+            x[u] = *reinterpret_cast<const uint4*>(kb + from * kst + c);
+            y[u] = *reinterpret_cast<const uint4*>(vb + from * vst + c);
+            if (c == 0) {
+                pos[to[u]] = pos[from];
+                weight[to[u]] = weight[from];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (to[u] < 0) continue;
+            *reinterpret_cast<uint4*>(kb + to[u] * kst + c) = x[u];
+            *reinterpret_cast<uint4*>(vb + to[u] * vst + c) = y[u];
+        }
+    }
+}
+
+}  // namespace
+
+// One block per (sequence, KV head).  move: the block moves its rows itself;
+// otherwise it leaves the lists in `lists` (holes from 0, movers from B, the
+// counts in `counts`) for move_kernel.
+template <int THREADS, bool HELD>
+__global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__ View a,
+                                                         const int32_t* __restrict__ budget, int recent, int slack,
+                                                         int row_bytes, int es, int move, int32_t* __restrict__ lists,
+                                                         int2* __restrict__ counts) {
+    __shared__ EvictSmem<THREADS> sm;
+    extern __shared__ __align__(16) unsigned char held_raw[];
+    constexpr int WARPS = THREADS / 32;
+    const int head = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n = own_len(a, head / a.Hk, head % a.Hk), B = max(0, budget[head]);
+    if ((int64_t)n < (int64_t)B + slack) {
+        if (!move && tid == 0) counts[head] = make_int2(0, 0);
+        return;
+    }
+    const int E = n - B;
+    const int32_t* pos = a.pos + (int64_t)head * a.cap;
+    const float* weight = a.weight + (int64_t)head * a.cap;
+    if (tid == 0) {
+        sm.newest = INT32_MIN;
+        sm.n_cand = 0;
+    }
+    int32_t* hpos = reinterpret_cast<int32_t*>(held_raw);
+    float* hw = reinterpret_cast<float*>(held_raw) + a.cap;
+    int nw = INT32_MIN;
+    for (int i0 = tid; i0 < n; i0 += 4 * THREADS) {
+        int32_t p[4];
+        float w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * THREADS;
+            p[u] = i < n ? pos[i] : INT32_MIN;
+            w[u] = HELD && i < n ? weight[i] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * THREADS;
+            nw = max(nw, p[u]);
+            if (HELD && i < n) {
+                hpos[i] = p[u];
+                hw[i] = w[u];
+            }
+        }
+    }
+    nw = __reduce_max_sync(FULL_MASK, nw);
+    __syncthreads();
+    if (lane == 0) atomicMax(&sm.newest, nw);
+    __syncthreads();
+    const int64_t newest = sm.newest;
+    auto key = [&](int i) {
+        const int p = HELD ? hpos[i] : pos[i];
+        return ((uint64_t)class_bits(HELD ? hw[i] : weight[i], newest - p < recent) << 32) | ((uint32_t)p ^ 0x80000000u);
+    };
+
+    // the threshold: (thr_key, thr_slot), the last to go
+    uint64_t prefix = 0, mask = 0;
+    int want = E, found = 0, count = n;
+    for (int d = 0; d <= 6 && !found; ++d) {
+        // `count` tokens share the digits so far, `want` of them go
+        if (count == want) {
+            if (tid == 0) {
+                sm.thr_key = prefix | ~mask;
+                sm.thr_slot = INT32_MAX;
+            }
+            found = 1;
+            break;
+        }
+        if (count <= CAND) {
+            for (int i = tid; i < n; i += THREADS) {
+                const uint64_t k = key(i);
+                if ((k & mask) == prefix) {
+                    const int c = atomicAdd(&sm.n_cand, 1);
+                    sm.cand_key[c] = k;
+                    sm.cand_slot[c] = i;
+                }
+            }
+            __syncthreads();
+            for (int c = tid; c < count; c += THREADS) {
+                const uint64_t k = sm.cand_key[c];
+                const int i = sm.cand_slot[c];
+                int rank = 0;
+#pragma unroll 4
+                for (int e = 0; e < count; ++e) {
+                    const uint64_t ke = sm.cand_key[e];
+                    rank += (int)(ke < k) | ((int)(ke == k) & (int)(sm.cand_slot[e] < i));
+                }
+                if (rank == want - 1) {
+                    sm.thr_key = k;
+                    sm.thr_slot = i;
+                }
+            }
+            found = 1;
+            break;
+        }
+        if (d == 6) break;
+        // digits of 11, 11 and 10 bits in each half
+        const int bits = d == 2 || d == 5 ? 10 : 11, shift = (d < 3 ? 32 : 0) + (d % 3 == 0 ? 21 : d % 3 == 1 ? 10 : 0);
+        for (int i = tid; i < BINS + THREADS; i += THREADS) sm.hist[i] = 0;
+        __syncthreads();
+        for (int i0 = 0; i0 < n; i0 += THREADS) {
+            const int i = i0 + tid;
+            const uint64_t k = i < n ? key(i) : 0;
+            const bool in = i < n && (k & mask) == prefix;
+            const int dig = (int)(k >> shift) & ((1 << bits) - 1);
+            // lanes that share the first lane's digit count together: equal
+            // weights and recent tokens would queue up at one address
+            const unsigned on = __ballot_sync(FULL_MASK, in);
+            if (on == 0) continue;
+            const int lead = __ffs(on) - 1, ldig = __shfl_sync(FULL_MASK, dig, lead);
+            const unsigned same = __ballot_sync(FULL_MASK, in && dig == ldig);
+            if (lane == lead) atomicAdd(&sm.bin_at(ldig), __popc(same));
+            else if (in && dig != ldig) atomicAdd(&sm.bin_at(dig), 1);
+        }
+        __syncthreads();
+        constexpr int PER = EvictSmem<THREADS>::PER;
+        int own = 0;
+#pragma unroll
+        for (int u = 0; u < PER; ++u) own += sm.bin_at(tid * PER + u);
+        int incl = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(FULL_MASK, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) sm.warp_a[warp] = incl;
+        __syncthreads();
+        int before = incl - own;
+        for (int w = 0; w < warp; ++w) before += sm.warp_a[w];
+        if (before < want && want <= before + own) {
+            int u = 0;
+            while (want > before + sm.bin_at(tid * PER + u)) before += sm.bin_at(tid * PER + u++);
+            sm.digit = tid * PER + u;
+            sm.below = before;
+        }
+        __syncthreads();
+        const int digit = sm.digit;
+        count = sm.bin_at(digit);
+        want -= sm.below;
+        prefix |= (uint64_t)digit << shift;
+        mask |= (uint64_t)((1 << bits) - 1) << shift;
+        __syncthreads();  // (the bins are cleared next)
+    }
+    // slots are dealt to the warps in contiguous runs
+    const int seg = (n + WARPS * 32 - 1) / (WARPS * 32) * 32;
+    const int lo = min(n, warp * seg), hi = min(n, lo + seg);
+    if (!found) {
+        // more than CAND tokens share the key: the lowest `want` slots of them go
+        int c = 0;
+        for (int i0 = lo; i0 < hi; i0 += 32) c += __popc(__ballot_sync(FULL_MASK, i0 + lane < hi && key(i0 + lane) == prefix));
+        if (lane == 0) sm.warp_a[warp] = c;
+        __syncthreads();
+        int before = 0;
+        for (int w = 0; w < warp; ++w) before += sm.warp_a[w];
+        for (int i0 = lo; i0 < hi && before < want; i0 += 32) {
+            const bool eq = i0 + lane < hi && key(i0 + lane) == prefix;
+            const unsigned b = __ballot_sync(FULL_MASK, eq);
+            if (eq && before + __popc(b & ((1u << lane) - 1)) == want - 1) {
+                sm.thr_key = prefix;
+                sm.thr_slot = i0 + lane;
+            }
+            before += __popc(b);
+        }
     }
     __syncthreads();
-    // (as many movers as holes, at most min(B, E))
-    for (int i = tid; i < n_movers; i += ET) {
-        const int from = hl[B + i], to = hl[i];
-        pos[to] = pos[from];
-        weight[to] = weight[from];
+    const uint64_t thr_key = sm.thr_key;
+    const int thr_slot = sm.thr_slot;
+    auto gone = [&](int i) {
+        const uint64_t k = key(i);
+        return k < thr_key || (k == thr_key && i <= thr_slot);
+    };
+    // holes (evicted below B) and movers (survivors from B on) in slot order
+    int nh = 0, nm = 0;
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+        const int i = i0 + lane;
+        const bool g = i < hi && gone(i);
+        nh += __popc(__ballot_sync(FULL_MASK, g && i < B));
+        nm += __popc(__ballot_sync(FULL_MASK, i < hi && !g && i >= B));
     }
-    const int pieces = row_bytes / 16;
-    for (int e = tid; e < n_movers * pieces; e += ET) {
-        const int i = e / pieces, c = e % pieces * 16;
-        const int64_t from = hl[B + i], to = hl[i];
-        *reinterpret_cast<uint4*>(kb + to * a.ks[2] * es + c) = *reinterpret_cast<uint4*>(kb + from * a.ks[2] * es + c);
-        *reinterpret_cast<uint4*>(vb + to * a.vs[2] * es + c) = *reinterpret_cast<uint4*>(vb + from * a.vs[2] * es + c);
+    if (lane == 0) {
+        sm.warp_a[warp] = nh;
+        sm.warp_b[warp] = nm;
+    }
+    __syncthreads();
+    int bh = 0, bm = 0, moves = 0;
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) {
+            bh += sm.warp_a[w];
+            bm += sm.warp_b[w];
+        }
+        moves += sm.warp_b[w];
+    }
+    // (as many movers as holes; both lists fit a row of `lists`: B + moves <= n)
+    int* hl = move && moves <= LIST ? sm.list : lists + (int64_t)head * a.cap;
+    int* ml = move && moves <= LIST ? sm.list + LIST : hl + B;
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+        const int i = i0 + lane;
+        const bool g = i < hi && gone(i), hole = g && i < B, mover = i < hi && !g && i >= B;
+        const unsigned b = __ballot_sync(FULL_MASK, hole), m = __ballot_sync(FULL_MASK, mover);
+        const unsigned lt = (1u << lane) - 1;
+        if (hole) hl[bh + __popc(b & lt)] = i;
+        if (mover) ml[bm + __popc(m & lt)] = i;
+        bh += __popc(b);
+        bm += __popc(m);
+    }
+    __syncthreads();
+    if (move) {
+        move_rows(a, head, hl, ml, moves, 0, 1, row_bytes, es);
+    } else if (tid == 0) {
+        counts[head] = make_int2(moves, B);
     }
     if (tid == 0) a.len[head] = B;
 }
 
+// Block (head, part): every parts-th group of the head's moves.
+__global__ void __launch_bounds__(256) move_kernel(const __grid_constant__ View a, int parts, int row_bytes, int es,
+                                                   const int32_t* __restrict__ lists, const int2* __restrict__ counts) {
+    const int head = blockIdx.x / parts;
+    ptx::grid_dep_wait();
+    const int2 c = counts[head];
+    const int32_t* hl = lists + (int64_t)head * a.cap;
+    move_rows(a, head, hl, hl + c.y, c.x, blockIdx.x % parts, parts, row_bytes, es);
+}
+
+cudaError_t prepare_shared_evict() {
+    return cudaFuncSetAttribute(select_kernel<1024, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, HELD_CAP * 8);
+}
+
+size_t evict_bytes(int heads, int cap) {
+    return (size_t)heads * cap * 4 + ((size_t)heads * 8 + 255) / 256 * 256;
+}
+
 cudaError_t launch_evict(const View& a, int dtype, int d, const int32_t* budget, int recent, int slack,
-                         int32_t* holes, cudaStream_t st) {
-    const int es = dtype == HKV_DTYPE_F32 ? 4 : 2;
-    evict_simple_kernel<<<a.S * a.Hk, ET, 0, st>>>(a, budget, recent, slack, d * es, es, holes);
-    return cudaGetLastError();
+                         unsigned char* scratch, cudaStream_t st) {
+    const int es = dtype == HKV_DTYPE_F32 ? 4 : 2, heads = a.S * a.Hk, row = d * es;
+    int2* counts = reinterpret_cast<int2*>(scratch);
+    int32_t* lists = reinterpret_cast<int32_t*>(scratch + ((size_t)heads * 8 + 255) / 256 * 256);
+    if (a.cap <= SHORT_CAP) {
+        select_kernel<128, true><<<heads, 128, (size_t)a.cap * 8, st>>>(a, budget, recent, slack, row, es, 1, lists, counts);
+        return cudaGetLastError();
+    }
+    if (a.cap <= HELD_CAP)
+        select_kernel<1024, true><<<heads, 1024, (size_t)a.cap * 8, st>>>(a, budget, recent, slack, row, es, 0, lists, counts);
+    else
+        select_kernel<1024, false><<<heads, 1024, 0, st>>>(a, budget, recent, slack, row, es, 0, lists, counts);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int parts = (int)std::max<int64_t>(1, (148 * 8 + heads - 1) / heads);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(heads * parts));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, move_kernel, a, parts, row, es, (const int32_t*)lists, (const int2*)counts);
 }
 
 }  // namespace shared
