@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(256) append_rows_kernel(View a, const T* __res
                                                           int n_new, int slices) {
     const int head = blockIdx.x / slices, part = blockIdx.x % slices;
     const int s = head / a.Hk, hk = head % a.Hk;
+    ptx::grid_dep_wait();
     const int len = own_len(a, s, hk), np0 = a.next_pos ? a.next_pos[head] : 0;
     if (n_new > a.cap - len) {
         if (a.status && part == 0 && threadIdx.x == 0 && atomicCAS(a.status, 0, HKV_ERR_CAPACITY) == 0)
@@ -83,6 +84,7 @@ __global__ void __launch_bounds__(256) append_rows_kernel(View a, const T* __res
 
 __global__ void bump_kernel(View a, int n_new) {
     const int head = blockIdx.x * blockDim.x + threadIdx.x;
+    ptx::grid_dep_wait();
     if (head >= a.S * a.Hk) return;
     const int len = clamp_len(a.len[head], a.cap);
     if (n_new > a.cap - len) return;
@@ -98,18 +100,15 @@ cudaError_t launch_append(const View& a, int dtype, int d, const void* k_t, cons
     auto go = [&](auto tag, auto dim) {
         using E = decltype(tag);
         constexpr int D = decltype(dim)::value;
-        append_rows_kernel<E, D><<<heads * slices, 256, 0, st>>>(a, (const E*)k_t, ks[0], ks[1], ks[2], (const E*)v_t,
-                                                                 vs[0], vs[1], vs[2], w_t, n_new, slices);
+        return launch(append_rows_kernel<E, D>, (int64_t)heads * slices, 256, 0, st, a, (const E*)k_t, ks[0], ks[1], ks[2],
+                      (const E*)v_t, vs[0], vs[1], vs[2], w_t, n_new, slices);
     };
     using I64 = std::integral_constant<int, 64>;
     using I128 = std::integral_constant<int, 128>;
-    if (dtype == HKV_DTYPE_F32) d == 64 ? go(float(), I64()) : go(float(), I128());
-    else d == 64 ? go(__nv_bfloat16(), I64()) : go(__nv_bfloat16(), I128());
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && slices > 1) {
-        bump_kernel<<<(heads + 255) / 256, 256, 0, st>>>(a, n_new);
-        e = cudaGetLastError();
-    }
+    cudaError_t e;
+    if (dtype == HKV_DTYPE_F32) e = d == 64 ? go(float(), I64()) : go(float(), I128());
+    else e = d == 64 ? go(__nv_bfloat16(), I64()) : go(__nv_bfloat16(), I128());
+    if (e == cudaSuccess && slices > 1) e = launch(bump_kernel, (heads + 255) / 256, 256, 0, st, a, n_new);
     return e;
 }
 
@@ -141,6 +140,8 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(View a, int ptiles, in
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rps = a.rep * a.T;
     const int64_t R = (int64_t)a.S * a.H * a.T;
+    ptx::grid_dep_wait();
+    ptx::grid_dep_trigger();
     const int n_prefix = ptiles * a.Hk * a.np;
     const bool is_prefix = (int)blockIdx.x < n_prefix;
     const T *kb, *vb;
@@ -462,6 +463,7 @@ __global__ void __launch_bounds__(128) column_sums_simt_kernel(View a) {
     const int chunks = (a.cap + KT - 1) / KT;
     const int sh = blockIdx.x / chunks, k0 = blockIdx.x % chunks * KT;
     const int s = sh / a.Hk, hk = sh % a.Hk, rps = a.rep * a.T;
+    ptx::grid_dep_wait();
     const int n = own_len(a, s, hk);
     if (k0 >= n) return;
     const T* kb = static_cast<const T*>(a.k) + s * a.ks[0] + hk * a.ks[1];
@@ -539,47 +541,33 @@ cudaError_t launch_attend_simt(const View& a, int dtype, int d, cudaStream_t st)
     const int rps = a.rep * a.T, otiles = (rps + RT - 1) / RT;
     const int64_t ptiles = a.np ? max_prefix_tiles(a.S, a.G, rps, RT) : 0;
     const int64_t blocks = ptiles * a.Hk * a.np + (int64_t)a.S * a.Hk * otiles * a.no;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     return by_type(dtype, d, [&](auto tag, auto dim) {
         using E = decltype(tag);
         constexpr int D = decltype(dim)::value;
         const size_t sm = sizeof(SimtSmem<D>) + (size_t)a.G * 4;
-        attend_simt_kernel<E, D><<<(int)blocks, 128, sm, st>>>(a, (int)ptiles, otiles);
-        return cudaGetLastError();
+        return launch(attend_simt_kernel<E, D>, blocks, 128, sm, st, a, (int)ptiles, otiles);
     });
 }
 
-cudaError_t launch_combine(const View& a, int dtype, int d, bool dependent, cudaStream_t st) {
+cudaError_t launch_combine(const View& a, int dtype, int d, cudaStream_t st) {
     const int64_t R = (int64_t)a.S * a.H * a.T, rb = (R + 3) / 4;
     const int64_t blocks = rb + (a.logit ? (int64_t)a.S * a.Hk * ((a.cap + 127) / 128) : 0);
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     return by_type(dtype, d, [&](auto tag, auto dim) {
         using E = decltype(tag);
         constexpr int D = decltype(dim)::value;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)blocks);
-        cfg.blockDim = dim3(128);
-        cfg.stream = st;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = dependent ? 1 : 0;
         const int rps = a.rep * a.T;
-        if (rps == 1) return cudaLaunchKernelEx(&cfg, combine_kernel<E, D, 1>, a, (int)rb);
-        if (rps <= 8) return cudaLaunchKernelEx(&cfg, combine_kernel<E, D, 8>, a, (int)rb);
-        return cudaLaunchKernelEx(&cfg, combine_kernel<E, D, STREAM_ROWS>, a, (int)rb);
+        if (rps == 1) return launch(combine_kernel<E, D, 1>, blocks, 128, 0, st, a, (int)rb);
+        if (rps <= 8) return launch(combine_kernel<E, D, 8>, blocks, 128, 0, st, a, (int)rb);
+        return launch(combine_kernel<E, D, STREAM_ROWS>, blocks, 128, 0, st, a, (int)rb);
     });
 }
 
 cudaError_t launch_column_sums_simt(const View& a, int dtype, int d, cudaStream_t st) {
     const int64_t blocks = (int64_t)a.S * a.Hk * ((a.cap + KT - 1) / KT);
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     return by_type(dtype, d, [&](auto tag, auto dim) {
         using E = decltype(tag);
         constexpr int D = decltype(dim)::value;
-        column_sums_simt_kernel<E, D><<<(int)blocks, 128, sizeof(SimtSmem<D>), st>>>(a);
-        return cudaGetLastError();
+        return launch(column_sums_simt_kernel<E, D>, blocks, 128, sizeof(SimtSmem<D>), st, a);
     });
 }
 

@@ -174,6 +174,27 @@ inline int64_t max_prefix_tiles(int S, int G, int rows_per_seq, int rt) {
 // Row tiles of 128 that a tensor-core block takes: two as soon as one (sequence, KV head) has them.
 inline int umma_row_tiles(int64_t rows_per_seq) { return rows_per_seq > 128 ? 2 : 1; }
 
+// Launches a kernel as a programmatic dependent: its blocks may be set up while
+// the kernel in front of it in the stream drains, so it executes
+// griddepcontrol.wait before it touches memory, and lets the next launch begin
+// only after that.  (The streaming kernel beside the prefixes' one is the
+// exception: it starts on that kernel's word.)
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), int64_t blocks, int threads, size_t smem, cudaStream_t st, A... args) {
+    if (blocks < 1 || blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // Tensor map of bf16 rows [n2][n1][n0] of d elements at strides st (elements:
 // outermost, middle, row): boxes of 64 columns x box rows, 128-byte swizzle,
 // zeros past the ends.
@@ -188,10 +209,9 @@ cudaError_t launch_append(const View& a, int dtype, int d, const void* k_t, cons
                           const int64_t* vts, const float* w_t, cudaStream_t st);
 cudaError_t launch_attend_simt(const View& a, int dtype, int d, cudaStream_t st);
 cudaError_t prepare_shared_stream();
-// dependent: launched beside the prefixes' kernel, whose end this launch's end includes
-cudaError_t launch_stream(const View& a, int d, int warps_per_head, bool dependent, cudaStream_t st);
-// dependent: may be set up before the launch in front of it has ended
-cudaError_t launch_combine(const View& a, int dtype, int d, bool dependent, cudaStream_t st);
+// beside: launched right behind the prefixes' kernel, whose end this launch's end includes
+cudaError_t launch_stream(const View& a, int d, int warps_per_head, bool beside, cudaStream_t st);
+cudaError_t launch_combine(const View& a, int dtype, int d, cudaStream_t st);
 cudaError_t launch_column_sums_simt(const View& a, int dtype, int d, cudaStream_t st);
 cudaError_t prepare_shared_evict();
 size_t evict_bytes(int heads, int cap);

@@ -222,7 +222,7 @@ hkv_status hkv_shared_attend(const hkv_shared_cache* c, const void* q, const int
     if (e == cudaSuccess && p.umma_prefix) e = hkv::shared::launch_prefix_umma(a, d, st);
     if (e == cudaSuccess && p.stream) e = hkv::shared::launch_stream(a, d, p.warps_per_head, p.umma_prefix, st);
     if (e == cudaSuccess && !p.umma_rows && !p.stream) e = hkv::shared::launch_attend_simt(a, c->dtype, d, st);
-    if (e == cudaSuccess && a.part_ml) e = hkv::shared::launch_combine(a, c->dtype, d, p.stream || p.umma_rows, st);
+    if (e == cudaSuccess && a.part_ml) e = hkv::shared::launch_combine(a, c->dtype, d, st);
     if (e == cudaSuccess && a.row_lse)
         e = p.umma_rows ? hkv::shared::launch_column_sums_umma(a, d, st)
                         : hkv::shared::launch_column_sums_simt(a, c->dtype, d, st);

@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
     extern __shared__ __align__(16) unsigned char held_raw[];
     constexpr int WARPS = THREADS / 32;
     const int head = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    ptx::grid_dep_wait();
     const int n = own_len(a, head / a.Hk, head % a.Hk), B = max(0, budget[head]);
     if ((int64_t)n < (int64_t)B + slack) {
         if (!move && tid == 0) counts[head] = make_int2(0, 0);
@@ -331,27 +332,16 @@ cudaError_t launch_evict(const View& a, int dtype, int d, const int32_t* budget,
     const int es = dtype == HKV_DTYPE_F32 ? 4 : 2, heads = a.S * a.Hk, row = d * es;
     int2* counts = reinterpret_cast<int2*>(scratch);
     int32_t* lists = reinterpret_cast<int32_t*>(scratch + ((size_t)heads * 8 + 255) / 256 * 256);
-    if (a.cap <= SHORT_CAP) {
-        select_kernel<128, true><<<heads, 128, (size_t)a.cap * 8, st>>>(a, budget, recent, slack, row, es, 1, lists, counts);
-        return cudaGetLastError();
-    }
-    if (a.cap <= HELD_CAP)
-        select_kernel<1024, true><<<heads, 1024, (size_t)a.cap * 8, st>>>(a, budget, recent, slack, row, es, 0, lists, counts);
-    else
-        select_kernel<1024, false><<<heads, 1024, 0, st>>>(a, budget, recent, slack, row, es, 0, lists, counts);
-    cudaError_t e = cudaGetLastError();
+    const size_t held = (size_t)a.cap * 8;
+    if (a.cap <= SHORT_CAP)
+        return launch(select_kernel<128, true>, heads, 128, held, st, a, budget, recent, slack, row, es, 1, lists, counts);
+    const cudaError_t e =
+        a.cap <= HELD_CAP
+            ? launch(select_kernel<1024, true>, heads, 1024, held, st, a, budget, recent, slack, row, es, 0, lists, counts)
+            : launch(select_kernel<1024, false>, heads, 1024, 0, st, a, budget, recent, slack, row, es, 0, lists, counts);
     if (e != cudaSuccess) return e;
-    const int parts = (int)std::max<int64_t>(1, (148 * 8 + heads - 1) / heads);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(heads * parts));
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, move_kernel, a, parts, row, es, (const int32_t*)lists, (const int2*)counts);
+    const int parts = std::max(1, (148 * 8 + heads - 1) / heads);
+    return launch(move_kernel, (int64_t)heads * parts, 256, 0, st, a, parts, row, es, lists, counts);
 }
 
 }  // namespace shared

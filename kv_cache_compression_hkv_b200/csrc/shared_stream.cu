@@ -60,9 +60,10 @@ template <int D> constexpr int stream_smem() { return SW * SN * 2 * SK * D * 2; 
 // heads a block, nothing to join) or 4 (steps dealt out in turn, joined in
 // shared memory).  LOW: at most 8 rows, the upper half of the M side is empty.
 template <int D, int WPH, bool LOW>
-__global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_constant__ View a, int dependent) {
+__global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_constant__ View a, int beside) {
     extern __shared__ __align__(1024) unsigned char raw[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (!beside) ptx::grid_dep_wait();
     ptx::grid_dep_trigger();  // the joining kernel waits for this grid's end
     const int item = blockIdx.x * (SW / WPH) + warp / WPH, wi = warp % WPH;
     const int rps = a.rep * a.T;
@@ -274,25 +275,16 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
         }
     }
     // this grid ends after the one it was launched beside (the prefixes')
-    if (dependent) ptx::grid_dep_wait();
+    if (beside) ptx::grid_dep_wait();
 }
 
-cudaError_t launch_stream(const View& a, int d, int warps_per_head, bool dependent, cudaStream_t st) {
+cudaError_t launch_stream(const View& a, int d, int warps_per_head, bool beside, cudaStream_t st) {
     const int rps = a.rep * a.T;
     const int64_t items = (int64_t)a.S * a.Hk * a.no, per = SW / warps_per_head;
     const int64_t blocks = (items + per - 1) / per;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(32 * SW);
-    cfg.dynamicSmemBytes = d == 128 ? stream_smem<128>() : stream_smem<64>();
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = dependent ? 1 : 0;
-    auto run = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, a, (int)dependent); };
+    auto run = [&](auto kernel) {
+        return launch(kernel, blocks, 32 * SW, d == 128 ? stream_smem<128>() : stream_smem<64>(), st, a, (int)beside);
+    };
     const bool low = rps <= 8, one = warps_per_head == 1;
     if (d == 128)
         return one ? (low ? run(stream_attend_kernel<128, 1, true>) : run(stream_attend_kernel<128, 1, false>))

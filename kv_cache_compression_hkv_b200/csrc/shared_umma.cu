@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
     const int rps = a.rep * a.T;
     const int64_t R = (int64_t)a.S * a.H * a.T;
 
+    ptx::grid_dep_wait();
     ptx::grid_dep_trigger();
     // what this block works on
     int hk, s = 0, g, first, rows, piece, p_tiles, t0, t1, p_len, n_own = 0, p_lo = 0;
@@ -558,6 +559,7 @@ __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
     // the first keys, which the most queries see, first
     const int heads = a.S * a.Hk, sh = blockIdx.x % heads, k0 = blockIdx.x / heads * C::KB;
     const int s = sh / a.Hk, hk = sh % a.Hk;
+    ptx::grid_dep_wait();
     const int n = own_len(a, s, hk);
     if (k0 >= n) return;
     // key j is seen by the queries t >= j - (n - T)
@@ -726,9 +728,8 @@ bool make_map(CUtensorMap* m, const void* ptr, int d, int n0, int n1, int n2, co
 template <int D, int NT, int MODE>
 static cudaError_t go(const View& a, const CUtensorMap* m, int64_t blocks, int row_tiles, int splits, cudaStream_t st) {
     using C = Shape<D, NT>;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    attend_umma_kernel<D, NT, MODE><<<(int)blocks, C::THREADS, C::SMEM, st>>>(a, m[0], m[1], m[2], m[3], row_tiles, splits);
-    return cudaGetLastError();
+    return launch(attend_umma_kernel<D, NT, MODE>, blocks, C::THREADS, C::SMEM, st, a, m[0], m[1], m[2], m[3], row_tiles,
+                  splits);
 }
 
 static bool own_maps(const View& a, int d, CUtensorMap* m) {
@@ -771,12 +772,8 @@ cudaError_t launch_column_sums_umma(const View& a, int d, cudaStream_t st) {
     if (!make_map(&km, a.k, d, a.cap, a.Hk, a.S, a.ks, 128) || !make_map(&qm, a.q, d, a.T, a.H, a.S, a.qs, 64))
         return cudaErrorInvalidValue;
     const int64_t blocks = (int64_t)a.S * a.Hk * ((a.cap + 127) / 128);
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    if (d == 128)
-        column_sums_umma_kernel<128><<<(int)blocks, SumShape<128>::THREADS, SumShape<128>::SMEM, st>>>(a, km, qm);
-    else
-        column_sums_umma_kernel<64><<<(int)blocks, SumShape<64>::THREADS, SumShape<64>::SMEM, st>>>(a, km, qm);
-    return cudaGetLastError();
+    if (d == 128) return launch(column_sums_umma_kernel<128>, blocks, SumShape<128>::THREADS, SumShape<128>::SMEM, st, a, km, qm);
+    return launch(column_sums_umma_kernel<64>, blocks, SumShape<64>::THREADS, SumShape<64>::SMEM, st, a, km, qm);
 }
 
 cudaError_t prepare_shared_umma() {
