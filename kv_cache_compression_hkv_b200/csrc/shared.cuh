@@ -50,6 +50,7 @@ struct View {
     float* part_o;    // [np + no][R][d]
     float* logit;     // [S][Hk][rep T][lcap] exp2-domain logits of the own keys (few rows, accumulate)
     int32_t lcap;     // capacity rounded up to 4
+    int32_t fused_sums;  // the attention blocks add the accumulated weights themselves
     float* row_lse;   // [R] log2 of the row sums (tile path, accumulate)
 };
 

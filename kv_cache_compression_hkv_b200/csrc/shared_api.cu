@@ -138,7 +138,8 @@ Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char
         a.part_o = (float*)take(ns * R * d * sizeof(float));
     }
     if (accumulate && stream) a.logit = (float*)take((size_t)heads * rps * a.lcap * 4);
-    if (accumulate && !stream) a.row_lse = (float*)take((size_t)R * 4);
+    a.fused_sums = accumulate && p.umma_rows && a.no == 1 && rps <= 256;
+    if (accumulate && !stream && !a.fused_sums) a.row_lse = (float*)take((size_t)R * 4);
     p.bytes = o;
     return p;
 }

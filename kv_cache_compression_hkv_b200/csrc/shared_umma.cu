@@ -49,8 +49,8 @@ template <int D, int NT> struct Shape {
     static constexpr uint32_t TMEM = NT == 2 ? 512 : 256;
     static constexpr int Q_BYTES = QT * D * 2, KV_BYTES = UK * D * 2;
     enum { B_Q, B_FULL, B_FREE = B_FULL + NS, B_S = B_FREE + NS, B_SF = B_S + NT, B_P = B_SF + NT, B_PV = B_P + 2 * NT,
-           B_COUNT = B_PV + 2 * NT };
-    static constexpr int TAIL = B_COUNT * 8 + 16 + 16 + (QT + 1) * 4 + 12;
+           B_T = B_PV + 2 * NT, B_TF = B_T + NT, B_COUNT = B_TF + NT };
+    static constexpr int TAIL = B_COUNT * 8 + 16 + 16 + (QT + 4) * 4 + ROWS * 4 + 2 * QT * 4;
     static constexpr int SMEM = 1024 + NT * Q_BYTES + NS * 2 * KV_BYTES + TAIL;
 };
 
@@ -58,7 +58,11 @@ template <int D, int NT> struct Shape {
 
 // MODE 0: every key of a row tile of one (sequence, KV head): prefix, then
 //         own, cut in `splits` pieces of the tile list; with one piece the
-//         results are final, else partial (slot = piece).
+//         results are final, else partial (slot = piece).  With a.fused_sums
+//         (one piece, and all rows of the (sequence, KV head) in this block)
+//         the block also adds the own keys' accumulated weights: S once more,
+//         transposed (128 keys on the M side, the rows as N), into the places
+//         of S and P, so that a thread sums 2^(x - lse) of its key.
 // MODE 1: rows of all sequences of a prefix over the prefix's keys, cut in
 //         a.np ranges; partial results (slot = range).
 template <int D, int NT, int MODE>
@@ -70,8 +74,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
     extern __shared__ unsigned char raw[];
     unsigned char* base = reinterpret_cast<unsigned char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     unsigned char* q_s = base;
-    unsigned char* ring = q_s + NT * C::Q_BYTES;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(ring + C::NS * 2 * C::KV_BYTES);  // a pair: V, then K
+    unsigned char* ring = q_s + NT * C::Q_BYTES;  // pairs: V, then K
+    float* nl_s = reinterpret_cast<float*>(ring + C::NS * 2 * C::KV_BYTES);  // [ROWS] -log2 of the rows' sums
+    float* half_s = nl_s + C::ROWS;                                          // [2][QT] column sums of the second row tile
+    uint64_t* bars = reinterpret_cast<uint64_t*>(half_s + 2 * QT);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::B_COUNT);
     int* res = reinterpret_cast<int*>(tmem_slot + 4);
     int* list = res + 4;
@@ -180,7 +186,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
     if (warp == 0) tc::alloc(tmem_slot, C::TMEM);
     if (tid == 0) {
         for (int i = 0; i < C::B_COUNT; ++i)
-            mbar_init(bars + i, i == C::B_Q ? 4 * NT : (i >= C::B_SF && i < C::B_PV) ? 4 : 1);
+            mbar_init(bars + i, i == C::B_Q ? 4 * NT : ((i >= C::B_SF && i < C::B_PV) || i >= C::B_TF) ? 4 : 1);
         ptx::fence_mbar_init();
     }
     tc::fence_before();
@@ -188,6 +194,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
     bool fail = false;
+
+    const int n2 = MODE == 0 && a.fused_sums ? (n_own + QT - 1) / QT : 0;  // blocks of 128 own keys for the sums
 
     // list tile t0 + j: where its keys start, and how many of 64 are keys
     auto tile_at = [&](int j, bool& pre, int& k0, int& valid) {
@@ -219,6 +227,17 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                         tc::tma_load_4d(dst + sub * UK * 128, pre ? &pvm : &vm, bars + C::B_FULL + slot, sub * 64, k0, hk,
                                         pre ? g : s);
                 }
+                issued = i + 1;
+            }
+            for (int kb = 0; kb < n2 && !fail; ++kb) {
+                const int i = n + 1 + kb, slot = i % C::NS, use = i / C::NS;
+                if (use > 0 && !mbar_wait(bars + C::B_FREE + slot, (use - 1) & 1, WAIT_NS)) { fail = true; break; }
+                unsigned char* dst = ring + slot * 2 * C::KV_BYTES;
+                mbar_expect_tx(bars + C::B_FULL + slot, 2 * C::KV_BYTES);
+                for (int sub = 0; sub < NSUB; ++sub)
+                    for (int e = 0; e < 2; ++e)
+                        tc::tma_load_4d(dst + sub * QT * 128 + e * UK * 128, &km, bars + C::B_FULL + slot, sub * 64,
+                                        kb * QT + e * UK, hk, s);
                 issued = i + 1;
             }
             if (fail)  // the block's own copies land before its shared memory goes
@@ -308,6 +327,34 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                     else if (now - since > WAIT_NS) fail = true;
                 }
             }
+            int sums = 0;  // transposed tiles issued
+            if (n2 > 0 && !fail) {
+                constexpr uint32_t IT = tc::idesc_bf16(QT, false);
+                const uint64_t t_desc = tc::sw128_desc(ring_u, 16, 1024);
+                // the places of S and P are free once the last products are done
+#pragma unroll
+                for (int x = 0; x < NT; ++x)
+                    if (pj[x] > 0 && !mbar_wait(bars + C::B_PV + 2 * x + ((pj[x] - 1) & 1), ((pj[x] - 1) >> 1) & 1, WAIT_NS))
+                        fail = true;
+                for (int kb = 0; kb < n2 && !fail; ++kb) {
+                    const int i = nn + 1 + kb;
+                    if (!mbar_wait(bars + C::B_FULL + i % C::NS, (i / C::NS) & 1, WAIT_NS)) { fail = true; break; }
+#pragma unroll
+                    for (int x = 0; x < NT; ++x) {
+                        if (kb > 0 && !mbar_wait(bars + C::B_TF + x, (kb - 1) & 1, WAIT_NS)) { fail = true; continue; }
+                        tc::fence_after();
+                        const uint64_t kd = t_desc + (i % C::NS) * (2 * C::KV_BYTES / 16), qd = q_desc + x * (C::Q_BYTES / 16);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            tc::mma_ss(tm + x * 128, kd + (kk / 4) * (QT * 8) + (kk % 4) * 2, qd + (kk / 4) * (QT * 8) + (kk % 4) * 2,
+                                       IT, kk > 0);
+                        tc::commit(bars + C::B_T + x);
+                    }
+                    tc::commit(bars + C::B_FREE + i % C::NS);
+                    ++freed;
+                    ++sums;
+                }
+            }
             // The tensor cores finish what was issued before TMEM is freed, and
             // the last commits' arrivals land before the shared memory goes.
 #pragma unroll
@@ -315,7 +362,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                 if (sj[x] > pj[x]) mbar_wait(bars + C::B_S + x, (sj[x] - 1) & 1, WAIT_NS);
                 if (pj[x] > 0) mbar_wait(bars + C::B_PV + 2 * x + ((pj[x] - 1) & 1), ((pj[x] - 1) >> 1) & 1, WAIT_NS);
             }
+            // (freed pairs and key blocks are numbered through)
             if (freed > 0) mbar_wait(bars + C::B_FREE + (freed - 1) % C::NS, ((freed - 1) / C::NS) & 1, WAIT_NS);
+            if (sums > 0)
+#pragma unroll
+                for (int x = 0; x < NT; ++x) mbar_wait(bars + C::B_T + x, (sums - 1) & 1, WAIT_NS);
         }
         __syncwarp();
     } else {
@@ -439,6 +490,54 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
         if (!fail && nt > 0) {
             const int jl = nt - 1;
             if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_PV + 2 * x + (jl & 1), (jl >> 1) & 1, WAIT_NS))) fail = true;
+        }
+        if (MODE == 0 && n2 > 0) {
+            // Every row thread comes here and to every barrier below, failed or not.
+            nl_s[tid] = live && !(m == -INFINITY && l == 0.f) ? -(m + log2f(l)) : -INFINITY;
+            asm volatile("bar.sync 1, %0;" ::"n"(C::ROWS) : "memory");
+            const int shift = n_own - a.T;  // key j is seen by the queries t >= j - shift
+            const float* nl = nl_s + x * QT;
+            float* wrow = a.weight + (int64_t)(s * a.Hk + hk) * a.cap;
+            for (int kb = 0; kb < n2; ++kb) {
+                const int key = kb * QT + (tid & 127);
+                const float old = x == 0 && key < n_own ? wrow[key] : 0.f;
+                float total = 0.f;
+                if (!fail && __any_sync(FULL_MASK, !mbar_wait(bars + C::B_T + x, kb & 1, WAIT_NS))) fail = true;
+                if (!fail) {
+                    tc::fence_after();
+                    const int from = (key - shift) * a.rep - x * QT;  // rows before it do not see the key
+                    const bool whole = __shfl_sync(FULL_MASK, from, 31) <= 0;
+#pragma unroll
+                    for (int c0 = 0; c0 < QT; c0 += 32) {
+                        uint32_t o[32];
+                        tc::ld32(t_s + c0, o);
+                        tc::ld_wait();
+                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int u = 0; u < 32; u += 4) {
+                            const float4 e = *reinterpret_cast<const float4*>(nl + c0 + u);
+                            const float ee[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) {
+                                const float p = tc::ex2(fmaf(__uint_as_float(o[u + v]), c, ee[v]));
+                                acc[v] += whole || c0 + u + v >= from ? p : 0.f;
+                            }
+                        }
+                        total += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+                    }
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::arrive(bars + C::B_TF + x);
+                }
+                if constexpr (NT == 2) {
+                    if (x == 1) half_s[(kb & 1) * QT + (tid & 127)] = total;
+                    asm volatile("bar.sync 1, %0;" ::"n"(C::ROWS) : "memory");
+                    if (x == 0) total += half_s[(kb & 1) * QT + tid];
+                }
+                if (x == 0 && key < n_own && !fail) wrow[key] = old + total;
+            }
+            // (Q's place is written next: by now every product that read it is done)
+            if constexpr (NT == 2) asm volatile("bar.sync 1, %0;" ::"n"(C::ROWS) : "memory");
         }
         if (!fail) {
             tc::fence_after();
