@@ -124,7 +124,10 @@ class SharedPrefixCache:
         n = C.c_size_t()
         _check(lib().hkv_shared_evict_bytes(self._ref, C.byref(n)), "hkv_shared_evict_bytes")
         self._evict_bytes = n.value
-        self._attend_bytes = {}  # (T, accumulate) -> scratch bytes
+        self._evict_like = self.lens.new_empty(1).expand(self._evict_bytes // 4)
+        self._plans = {}  # (T, accumulate) -> see _plan
+        L = lib()
+        self._append_fn, self._attend_fn, self._evict_fn = L.hkv_shared_append, L.hkv_shared_attend, L.hkv_shared_evict
 
     # -- argument checks (each a few hundred nanoseconds: a decode step's calls
     #    take the GPU ten to twenty microseconds) ------------------------------
@@ -182,7 +185,7 @@ class SharedPrefixCache:
             raise ValueError("weight_t: expected a contiguous float32 [S, Hkv, T] tensor on the device")
         if T == 0:
             return
-        self._call(lib().hkv_shared_append, "hkv_shared_append", stream,
+        self._call(self._append_fn, "hkv_shared_append", stream,
                    lambda: ((self._ref, k_t.data_ptr(), ks, v_t.data_ptr(), vs,
                              None if weight_t is None else weight_t.data_ptr(), T), None))
 
@@ -193,11 +196,11 @@ class SharedPrefixCache:
         [S, H, T, d], lse float32 [S, H, T]); a query that sees nothing gets
         zeros and -inf.  accumulate adds to `weight` the softmax weights each
         own token received.  scale of the logits: 1 / sqrt(d) by default."""
-        c = self.cfg
-        qs = self._tensor(q, "q", c.num_heads)
-        T = q.shape[2]
-        if T < 1 or T > c.capacity:
-            raise ValueError("q: between 1 token and the capacity")
+        qs = self._tensor(q, "q", self.cfg.num_heads)
+        plan = self._plans.get((q.shape[2], accumulate))
+        if plan is None:
+            plan = self._plan(q.shape[2], accumulate)
+        T, accumulate, need, lse_like, scratch_like = plan
         if not (qs[0] and qs[1] and qs[2]):
             raise ValueError("q: no repeated rows")
         if scale is None:
@@ -205,32 +208,45 @@ class SharedPrefixCache:
         elif not (scale != 0 and abs(scale) < float("inf")):
             raise ValueError("scale: a finite number other than 0")
         if out is not None:
-            self._tensor(out, "out", c.num_heads)
+            self._tensor(out, "out", self.cfg.num_heads)
             if out.shape != q.shape or 0 in out.stride():
                 raise ValueError("out: expected q's shape, no repeated rows")
         if lse is not None and (lse.dtype != torch.float32 or lse.device != self.device or
                                 lse.shape != q.shape[:3] or not lse.is_contiguous()):
             raise ValueError("lse: expected a contiguous float32 [S, H, T] tensor on the device")
-        accumulate = int(bool(accumulate))
-        need = self._attend_bytes.get((T, accumulate))
-        if need is None:
-            n = C.c_size_t()
-            _check(lib().hkv_shared_attend_bytes(self._ref, T, accumulate, C.byref(n)), "hkv_shared_attend_bytes")
-            need = self._attend_bytes[(T, accumulate)] = n.value
 
         def args():
             nonlocal out, lse
+            so = qs
             if out is None:
-                out = q.new_empty(q.shape)
+                if q.is_contiguous():
+                    out = torch.empty_like(q)
+                else:
+                    out = q.new_empty(q.shape)
+                    so = _Strides(*out.stride()[:3])
+            else:
+                so = _Strides(*out.stride()[:3])
             if lse is None:
-                lse = self.weight.new_empty(q.shape[:3])
-            scratch = self.lens.new_empty(need // 4)
-            so = out.stride()
-            return (self._ref, q.data_ptr(), qs, out.data_ptr(), _Strides(so[0], so[1], so[2]), lse.data_ptr(), T,
-                    float(scale), accumulate, scratch.data_ptr(), need), scratch
+                lse = torch.empty_like(lse_like)
+            scratch = torch.empty_like(scratch_like)
+            return (self._ref, q.data_ptr(), qs, out.data_ptr(), so, lse.data_ptr(), T, scale, accumulate,
+                    scratch.data_ptr(), need), scratch
 
-        self._call(lib().hkv_shared_attend, "hkv_shared_attend", stream, args)
+        self._call(self._attend_fn, "hkv_shared_attend", stream, args)
         return out, lse
+
+    def _plan(self, T, accumulate):
+        """What a call of these sizes needs: kept, as it depends on nothing
+        else.  (empty_like of an expanded element is the cheapest allocation.)"""
+        c = self.cfg
+        if T < 1 or T > c.capacity:
+            raise ValueError("q: between 1 token and the capacity")
+        acc, n = int(bool(accumulate)), C.c_size_t()
+        _check(lib().hkv_shared_attend_bytes(self._ref, T, acc, C.byref(n)), "hkv_shared_attend_bytes")
+        plan = (T, acc, n.value, self.weight.new_empty(1).expand(c.num_seqs, c.num_heads, T),
+                self.lens.new_empty(1).expand(n.value // 4))
+        self._plans[(T, accumulate)] = plan
+        return plan
 
     def evict(self, budgets, recent: int = 0, slack: int = 1, stream=None):
         """Brings every head holding at least budget + slack tokens back to
@@ -246,10 +262,10 @@ class SharedPrefixCache:
             raise ValueError("recent at least 0, slack at least 1")
 
         def args():
-            scratch = self.lens.new_empty(self._evict_bytes // 4)
+            scratch = torch.empty_like(self._evict_like)
             return (self._ref, budgets.data_ptr(), recent, slack, scratch.data_ptr(), self._evict_bytes), scratch
 
-        self._call(lib().hkv_shared_evict, "hkv_shared_evict", stream, args)
+        self._call(self._evict_fn, "hkv_shared_evict", stream, args)
 
     def check(self):
         """(code, detail) of the first error latched on the device (waits)."""
