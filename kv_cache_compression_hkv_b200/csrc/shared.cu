@@ -1,6 +1,5 @@
-// shared.cu -- shared-prefix cache: append, attention over prefix and own
-// tokens on the CUDA cores, the joining of partial results, and the
-// accumulated weights.
+// shared.cu -- shared-prefix cache: append, attention in fp32 on the CUDA
+// cores, the joining of partial results, and the accumulated weights.
 //
 // A row (sequence s, query head h, query t) attends over the n_p keys of its
 // prefix and its own keys j < lim:
@@ -12,6 +11,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -19,19 +19,6 @@
 
 namespace hkv {
 namespace shared {
-
-namespace {
-
-template <typename T> __device__ __forceinline__ float4 load4(const T* p);
-template <> __device__ __forceinline__ float4 load4<float>(const float* p) {
-    return *reinterpret_cast<const float4*>(p);
-}
-template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-}
-
-}  // namespace
 
 // ---------------------------------------------------------------------------
 // append
@@ -113,93 +100,117 @@ cudaError_t launch_append(const View& a, int dtype, int d, const void* k_t, cons
 }
 
 // ---------------------------------------------------------------------------
-// attention on the CUDA cores
+// attention in fp32, on the CUDA cores (fp32 products stay fp32)
 // ---------------------------------------------------------------------------
 
 constexpr int RT = 16;   // rows of a block
 constexpr int KT = 32;   // keys a step
 
-template <int D> struct SimtSmem {
+template <int D> struct F32Smem {
     static constexpr int KP = D + 4;  // padded rows: float4 reads of 32 rows spread over the banks
     float q[RT][KP];
-    float k[KT][KP];
-    float v[KT][D];
+    float k[2][KT][KP];
+    float v[2][KT][D];
     float p[KT][RT];
+    float2 ml[RT];
     int list[RT + 1];
     int res[4];
 };
 
-// One block per (tile of 16 rows, key range): prefix tiles first, then the
-// own keys.  Warp w owns rows 4w .. 4w + 3: lane = key for the logits, lanes
-// across d for the weighted sum.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) attend_simt_kernel(View a, int ptiles, int otiles) {
+__device__ __forceinline__ void cp16(void* dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
+                 : "memory");
+}
+
+// One block per (tile of 16 rows, keys): first the prefixes' tiles, whose rows
+// come from all their sequences (np > 0), then tiles of one (sequence, KV
+// head) over a piece of its list of keys.  Steps of 32 keys, the next one's on
+// their way.  Warp w owns rows 4w .. 4w + 3: lane = key for the logits, lanes
+// across d for the weighted sum.  Where a block has all of its rows' keys the
+// result is final, and, with the logits kept (one tile has all the head's
+// rows), so are the accumulated weights.
+template <int D>
+__global__ void __launch_bounds__(128) attend_f32_kernel(const __grid_constant__ View a, int ptiles, int otiles) {
     extern __shared__ __align__(16) unsigned char raw[];
-    SimtSmem<D>& sm = *reinterpret_cast<SimtSmem<D>*>(raw);
-    int* cnt = reinterpret_cast<int*>(raw + sizeof(SimtSmem<D>));
+    F32Smem<D>& sm = *reinterpret_cast<F32Smem<D>*>(raw);
+    int* cnt = reinterpret_cast<int*>(raw + sizeof(F32Smem<D>));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rps = a.rep * a.T;
     const int64_t R = (int64_t)a.S * a.H * a.T;
+    const bool final = a.np + a.no == 1;
     ptx::grid_dep_wait();
     ptx::grid_dep_trigger();
     const int n_prefix = ptiles * a.Hk * a.np;
     const bool is_prefix = (int)blockIdx.x < n_prefix;
-    const T *kb, *vb;
-    int64_t kst, vst;
-    int lo, hi, slot, rows, hk, s = 0, first = 0, n_own = 0;
+    int slot, rows, hk, s = 0, first = 0, n_own = 0, g;
+    Piece pc;
     if (is_prefix) {
         const int b = blockIdx.x;
-        const int j = b % a.np, tile = b / a.np / a.Hk;
+        slot = b % a.np;
         hk = b / a.np % a.Hk;
-        int g;
-        if (!find_prefix_tile(a, tile, RT, g, first, rows, cnt, sm.res, sm.list)) return;
-        split_range(prefix_len(a, g), a.np, j, lo, hi);
-        slot = j;
-        kb = static_cast<const T*>(a.pk) + g * a.pks[0] + hk * a.pks[1];
-        vb = static_cast<const T*>(a.pv) + g * a.pvs[0] + hk * a.pvs[1];
-        kst = a.pks[2];
-        vst = a.pvs[2];
+        if (!find_prefix_tile(a, b / a.np / a.Hk, RT, g, first, rows, cnt, sm.res, sm.list)) return;
+        split_range(prefix_len(a, g), a.np, slot, pc.pa, pc.pb);
+        pc.oa = pc.ob = 0;
     } else {
-        const int b = blockIdx.x - n_prefix;
-        const int j = b % a.no, tile = b / a.no % otiles;
-        const int sh = b / a.no / otiles;
+        // the rows with the most keys (the last queries) first
+        const int b = blockIdx.x - n_prefix, heads = a.S * a.Hk;
+        const int j = b % a.no, sh = b / a.no % heads, tile = otiles - 1 - b / a.no / heads;
         s = sh / a.Hk;
         hk = sh % a.Hk;
         first = tile * RT;
         rows = min(RT, rps - first);
+        g = prefix_of(a, s);
         n_own = own_len(a, s, hk);
-        split_range(n_own, a.no, j, lo, hi);
+        pc = list_piece(a.listed ? prefix_len(a, g) : 0, n_own, a.no, j);
         slot = a.np + j;
-        kb = static_cast<const T*>(a.k) + s * a.ks[0] + hk * a.ks[1];
-        vb = static_cast<const T*>(a.v) + s * a.vs[0] + hk * a.vs[1];
-        kst = a.ks[2];
-        vst = a.vs[2];
     }
-    if (lo >= hi) return;  // the joining kernel knows
+    if (pc.empty() && !final) return;  // the joining kernel knows
     const int o0 = first / rps;
     auto seq_row = [&](int r, int& sq, int& i) {  // row r of the tile -> sequence, row within (sequence, KV head)
         const int f = first + r;
         sq = is_prefix ? sm.list[f / rps - o0] : s;
         i = is_prefix ? f % rps : f;
     };
+    // own keys past the last row's limit are needed only where their logits are kept
+    const bool keep = !is_prefix && a.logit;
+    if (!is_prefix && !keep) pc.ob = min(pc.ob, own_limit(a, n_own, first + rows - 1));
+    const int psteps = (pc.pb - pc.pa + KT - 1) / KT, steps = psteps + max(0, pc.ob - pc.oa + KT - 1) / KT;
+    const float* pkb = static_cast<const float*>(a.pk) + (g < 0 ? 0 : g) * a.pks[0] + hk * a.pks[1];
+    const float* pvb = static_cast<const float*>(a.pv) + (g < 0 ? 0 : g) * a.pvs[0] + hk * a.pvs[1];
+    const float* kb = static_cast<const float*>(a.k) + s * a.ks[0] + hk * a.ks[1];
+    const float* vb = static_cast<const float*>(a.v) + s * a.vs[0] + hk * a.vs[1];
+    auto load = [&](int st) {
+        if (st < steps) {
+            const bool pre = st < psteps;
+            const int k0 = pre ? pc.pa + st * KT : pc.oa + (st - psteps) * KT, hi = pre ? pc.pb : pc.ob;
+            const float *kp = pre ? pkb : kb, *vp = pre ? pvb : vb;
+            const int64_t kst = pre ? a.pks[2] : a.ks[2], vst = pre ? a.pvs[2] : a.vs[2];
+#pragma unroll
+            for (int e = 0; e < KT * (D / 4) / 128; ++e) {
+                const int idx = e * 128 + tid, r = idx / (D / 4), c = idx % (D / 4) * 4;
+                const bool on = k0 + r < hi;
+                const int64_t key = on ? k0 + r : k0;
+                cp16(&sm.k[st & 1][r][c], kp + key * kst + c, on);
+                cp16(&sm.v[st & 1][r][c], vp + key * vst + c, on);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    load(0);
     for (int e = tid; e < RT * (D / 4); e += 128) {
         const int r = e / (D / 4), c = e % (D / 4) * 4;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < rows) {
             int sq, i;
             seq_row(r, sq, i);
-            x = load4(static_cast<const T*>(a.q) + sq * a.qs[0] + (hk * a.rep + i % a.rep) * a.qs[1] +
-                      i / a.rep * a.qs[2] + c);
+            x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + sq * a.qs[0] +
+                                                 (hk * a.rep + i % a.rep) * a.qs[1] + i / a.rep * a.qs[2] + c);
         }
-        sm.q[r][c] = x.x * a.qscale;
-        sm.q[r][c + 1] = x.y * a.qscale;
-        sm.q[r][c + 2] = x.z * a.qscale;
-        sm.q[r][c + 3] = x.w * a.qscale;
+        *reinterpret_cast<float4*>(&sm.q[r][c]) = make_float4(x.x * a.qscale, x.y * a.qscale, x.z * a.qscale, x.w * a.qscale);
     }
     constexpr int V = D / 32;
     float m[4], l[4], o[4][V];
     int lim[4];
-    float* lrow[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const int r = warp * 4 + u;
@@ -207,90 +218,118 @@ __global__ void __launch_bounds__(128) attend_simt_kernel(View a, int ptiles, in
         l[u] = 0.f;
 #pragma unroll
         for (int c = 0; c < V; ++c) o[u][c] = 0.f;
-        lim[u] = r >= rows ? 0 : (is_prefix ? hi : own_limit(a, n_own, first + r));
-        lrow[u] = !is_prefix && a.logit && r < rows
-                      ? a.logit + ((int64_t)(s * a.Hk + hk) * rps + first + r) * a.lcap : nullptr;
+        lim[u] = r >= rows || is_prefix ? 0 : own_limit(a, n_own, first + r);
     }
-    int stop = hi;
-    if (!is_prefix) stop = min(hi, own_limit(a, n_own, first + rows - 1));
-    if (!is_prefix && a.logit) stop = hi;  // every kept logit is written, -inf past a row's limit
-    for (int k0 = lo; k0 < stop; k0 += KT) {
+    float* lrow = keep ? a.logit + ((int64_t)(s * a.Hk + hk) * rps + warp * 4) * a.lcap : nullptr;
+    const bool idle = warp * 4 >= rows;
+    for (int st = 0; st < steps; ++st) {
+        load(st + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();
-        for (int e = tid; e < KT * (D / 4); e += 128) {
-            const int r = e / (D / 4), c = e % (D / 4) * 4;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-            if (k0 + r < hi) {
-                x = load4(kb + (int64_t)(k0 + r) * kst + c);
-                y = load4(vb + (int64_t)(k0 + r) * vst + c);
-            }
-            *reinterpret_cast<float4*>(&sm.k[r][c]) = x;
-            *reinterpret_cast<float4*>(&sm.v[r][c]) = y;
-        }
-        __syncthreads();
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        if (!idle) {
+            const bool pre = st < psteps;
+            const int k0 = pre ? pc.pa + st * KT : pc.oa + (st - psteps) * KT, hi = pre ? pc.pb : pc.ob;
+            float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-        for (int c = 0; c < D; c += 4) {
-            const float4 kk = *reinterpret_cast<const float4*>(&sm.k[lane][c]);
+            for (int c = 0; c < D; c += 4) {
+                const float4 kk = *reinterpret_cast<const float4*>(&sm.k[st & 1][lane][c]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float4 qq = *reinterpret_cast<const float4*>(&sm.q[warp * 4 + u][c]);
+                    x[u] = fmaf(kk.x, qq.x, fmaf(kk.y, qq.y, fmaf(kk.z, qq.z, fmaf(kk.w, qq.w, x[u]))));
+                }
+            }
+            const int key = k0 + lane;
+            float pw[4], mt[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const float4 qq = *reinterpret_cast<const float4*>(&sm.q[warp * 4 + u][c]);
-                x[u] = fmaf(kk.x, qq.x, fmaf(kk.y, qq.y, fmaf(kk.z, qq.z, fmaf(kk.w, qq.w, x[u]))));
+                const bool in = key < hi && (pre ? warp * 4 + u < rows : key < lim[u]);
+                x[u] = in ? x[u] : -INFINITY;
+                if (lrow && !pre && key < hi && warp * 4 + u < rows) lrow[(int64_t)u * a.lcap + key] = x[u];
+                mt[u] = x[u];
+            }
+#pragma unroll
+            for (int off = 16; off; off >>= 1)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) mt[u] = fmaxf(mt[u], __shfl_xor_sync(FULL_MASK, mt[u], off));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float mn = fmaxf(m[u], mt[u]);
+                const float mb = mn == -INFINITY ? 0.f : mn;
+                const float alpha = exp2f(m[u] - mb);
+                pw[u] = exp2f(x[u] - mb);
+                l[u] = l[u] * alpha + pw[u];  // each lane its own keys; summed at the end
+                m[u] = mn;
+#pragma unroll
+                for (int c = 0; c < V; ++c) o[u][c] *= alpha;
+            }
+            *reinterpret_cast<float4*>(&sm.p[lane][warp * 4]) = make_float4(pw[0], pw[1], pw[2], pw[3]);
+            __syncwarp();
+#pragma unroll 8
+            for (int kk = 0; kk < KT; ++kk) {
+                const float4 p4 = *reinterpret_cast<const float4*>(&sm.p[kk][warp * 4]);
+                const float pr[4] = {p4.x, p4.y, p4.z, p4.w};
+                float vv[V];
+                if constexpr (V == 4) {
+                    const float4 y = *reinterpret_cast<const float4*>(&sm.v[st & 1][kk][lane * 4]);
+                    vv[0] = y.x; vv[1] = y.y; vv[2] = y.z; vv[3] = y.w;
+                } else {
+                    const float2 y = *reinterpret_cast<const float2*>(&sm.v[st & 1][kk][lane * 2]);
+                    vv[0] = y.x; vv[1] = y.y;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int c = 0; c < V; ++c) o[u][c] = fmaf(pr[u], vv[c], o[u][c]);
             }
         }
-        const int key = k0 + lane;
-        float pw[4];
+        __syncthreads();  // the stage is loaded again next
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (!idle) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const bool in = key < lim[u] && key < hi;
-            x[u] = in ? x[u] : -INFINITY;
-            if (lrow[u] && key < hi) lrow[u][key] = x[u];
-            float mt = x[u];
+            const int r = warp * 4 + u;
+            float ls = l[u];
 #pragma unroll
-            for (int off = 16; off; off >>= 1) mt = fmaxf(mt, __shfl_xor_sync(FULL_MASK, mt, off));
-            const float mn = fmaxf(m[u], mt);
-            const float mb = mn == -INFINITY ? 0.f : mn;
-            const float alpha = exp2f(m[u] - mb);
-            pw[u] = in ? exp2f(x[u] - mb) : 0.f;
-            l[u] = l[u] * alpha + pw[u];  // each lane its own keys; summed at the end
-            m[u] = mn;
-#pragma unroll
-            for (int c = 0; c < V; ++c) o[u][c] *= alpha;
-        }
-        *reinterpret_cast<float4*>(&sm.p[lane][warp * 4]) = make_float4(pw[0], pw[1], pw[2], pw[3]);
-        __syncwarp();
-#pragma unroll 4
-        for (int kk = 0; kk < KT; ++kk) {
-            const float4 p4 = *reinterpret_cast<const float4*>(&sm.p[kk][warp * 4]);
-            const float pr[4] = {p4.x, p4.y, p4.z, p4.w};
-            float vv[V];
-            if constexpr (V == 4) {
-                const float4 y = *reinterpret_cast<const float4*>(&sm.v[kk][lane * 4]);
-                vv[0] = y.x; vv[1] = y.y; vv[2] = y.z; vv[3] = y.w;
-            } else {
-                const float2 y = *reinterpret_cast<const float2*>(&sm.v[kk][lane * 2]);
-                vv[0] = y.x; vv[1] = y.y;
+            for (int off = 16; off; off >>= 1) ls += __shfl_xor_sync(FULL_MASK, ls, off);
+            if (r >= rows) continue;
+            int sq, i;
+            seq_row(r, sq, i);
+            const int64_t row = row_of(a, sq, hk, i);
+            // (a sum that is NaN, of NaN logits alone, must not pass for an empty row)
+            if (ls != ls && m[u] == -INFINITY) m[u] = 0.f;
+            const bool some = !(m[u] == -INFINITY);
+            const float f = !final ? 1.f : some ? 1.f / ls : 0.f;
+            float* po = final ? static_cast<float*>(a.out) + s * a.os[0] + (hk * a.rep + i % a.rep) * a.os[1] + i / a.rep * a.os[2]
+                              : a.part_o + (slot * R + row) * D;
+            if constexpr (V == 4)
+                *reinterpret_cast<float4*>(po + lane * 4) = make_float4(o[u][0] * f, o[u][1] * f, o[u][2] * f, o[u][3] * f);
+            else
+                *reinterpret_cast<float2*>(po + lane * 2) = make_float2(o[u][0] * f, o[u][1] * f);
+            if (lane == 0) {
+                if (final) {
+                    const float l2 = some ? m[u] + log2f(ls) : -INFINITY;
+                    if (a.lse) a.lse[row] = l2 * 0.6931471805599453f;
+                    if (a.row_lse) a.row_lse[row] = l2;
+                    sm.ml[r] = make_float2(m[u], f);
+                } else {
+                    a.part_ml[ml_index(a, row, slot)] = make_float2(m[u], ls);
+                }
             }
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int c = 0; c < V; ++c) o[u][c] = fmaf(pr[u], vv[c], o[u][c]);
         }
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int r = warp * 4 + u;
-        float ls = l[u];
-#pragma unroll
-        for (int off = 16; off; off >>= 1) ls += __shfl_xor_sync(FULL_MASK, ls, off);
-        if (r >= rows) continue;
-        int sq, i;
-        seq_row(r, sq, i);
-        const int64_t row = row_of(a, sq, hk, i);
-        // (a sum that is NaN, of NaN logits alone, must not pass for an empty row)
-        if (lane == 0) a.part_ml[ml_index(a, row, slot)] = make_float2(ls != ls && m[u] == -INFINITY ? 0.f : m[u], ls);
-        float* po = a.part_o + (slot * R + row) * D + lane * V;
-#pragma unroll
-        for (int c = 0; c < V; ++c) po[c] = o[u][c];
+    if (!final || !keep) return;
+    __syncthreads();
+    const float* lg = a.logit + (int64_t)(s * a.Hk + hk) * rps * a.lcap;
+    float* w = a.weight + (int64_t)(s * a.Hk + hk) * a.cap;
+    for (int j = tid; j < n_own; j += 128) {
+        float sum = 0.f;
+        for (int i = 0; i < rps; ++i) {
+            const float2 y = sm.ml[i];
+            if (y.x != -INFINITY) sum += exp2f(lg[(int64_t)i * a.lcap + j] - y.x) * y.y;
+        }
+        w[j] += sum;
     }
 }
 
@@ -455,10 +494,16 @@ __global__ void __launch_bounds__(128, 8) combine_kernel(const __grid_constant__
 // One block per (sequence, KV head, 32 keys): lane = key, warp w takes rows
 // 4w .. 4w + 3 of every tile of 16; a key's weight 2^(x - lse) over the rows
 // that see it, per tile, then over the tiles, then over the warps.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) column_sums_simt_kernel(View a) {
+template <int D> struct SumSmem {
+    float q[RT][D + 4];
+    float k[KT][D + 4];
+    float p[4][KT];
+};
+
+template <int D>
+__global__ void __launch_bounds__(128) column_sums_f32_kernel(const __grid_constant__ View a) {
     extern __shared__ __align__(16) unsigned char raw[];
-    SimtSmem<D>& sm = *reinterpret_cast<SimtSmem<D>*>(raw);
+    SumSmem<D>& sm = *reinterpret_cast<SumSmem<D>*>(raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int chunks = (a.cap + KT - 1) / KT;
     const int sh = blockIdx.x / chunks, k0 = blockIdx.x % chunks * KT;
@@ -466,11 +511,11 @@ __global__ void __launch_bounds__(128) column_sums_simt_kernel(View a) {
     ptx::grid_dep_wait();
     const int n = own_len(a, s, hk);
     if (k0 >= n) return;
-    const T* kb = static_cast<const T*>(a.k) + s * a.ks[0] + hk * a.ks[1];
+    const float* kb = static_cast<const float*>(a.k) + s * a.ks[0] + hk * a.ks[1];
     for (int e = tid; e < KT * (D / 4); e += 128) {
         const int r = e / (D / 4), c = e % (D / 4) * 4;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k0 + r < n) x = load4(kb + (int64_t)(k0 + r) * a.ks[2] + c);
+        if (k0 + r < n) x = *reinterpret_cast<const float4*>(kb + (int64_t)(k0 + r) * a.ks[2] + c);
         *reinterpret_cast<float4*>(&sm.k[r][c]) = x;
     }
     // the first row that sees key k0: n - T + t + 1 > k0
@@ -485,8 +530,8 @@ __global__ void __launch_bounds__(128) column_sums_simt_kernel(View a) {
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows) {
                 const int i = f + r;
-                x = load4(static_cast<const T*>(a.q) + s * a.qs[0] + (hk * a.rep + i % a.rep) * a.qs[1] +
-                          i / a.rep * a.qs[2] + c);
+                x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + s * a.qs[0] +
+                                                     (hk * a.rep + i % a.rep) * a.qs[1] + i / a.rep * a.qs[2] + c);
             }
             sm.q[r][c] = x.x * a.qscale;
             sm.q[r][c + 1] = x.y * a.qscale;
@@ -537,16 +582,24 @@ template <typename F> cudaError_t by_type(int dtype, int d, F&& f) {
 
 }  // namespace
 
-cudaError_t launch_attend_simt(const View& a, int dtype, int d, cudaStream_t st) {
+cudaError_t launch_attend_f32(const View& a, int d, cudaStream_t st) {
     const int rps = a.rep * a.T, otiles = (rps + RT - 1) / RT;
     const int64_t ptiles = a.np ? max_prefix_tiles(a.S, a.G, rps, RT) : 0;
     const int64_t blocks = ptiles * a.Hk * a.np + (int64_t)a.S * a.Hk * otiles * a.no;
-    return by_type(dtype, d, [&](auto tag, auto dim) {
-        using E = decltype(tag);
+    auto go = [&](auto dim) {
         constexpr int D = decltype(dim)::value;
-        const size_t sm = sizeof(SimtSmem<D>) + (size_t)a.G * 4;
-        return launch(attend_simt_kernel<E, D>, blocks, 128, sm, st, a, (int)ptiles, otiles);
-    });
+        return launch(attend_f32_kernel<D>, blocks, 128, sizeof(F32Smem<D>) + (size_t)a.G * 4, st, a, (int)ptiles, otiles);
+    };
+    return d == 64 ? go(std::integral_constant<int, 64>()) : go(std::integral_constant<int, 128>());
+}
+
+cudaError_t prepare_shared_f32() {
+    cudaError_t e = cudaFuncSetAttribute(attend_f32_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(F32Smem<64>) + MAX_PREFIXES * 4);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(attend_f32_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)sizeof(F32Smem<128>) + MAX_PREFIXES * 4);
+    return e;
 }
 
 cudaError_t launch_combine(const View& a, int dtype, int d, cudaStream_t st) {
@@ -562,13 +615,10 @@ cudaError_t launch_combine(const View& a, int dtype, int d, cudaStream_t st) {
     });
 }
 
-cudaError_t launch_column_sums_simt(const View& a, int dtype, int d, cudaStream_t st) {
+cudaError_t launch_column_sums_f32(const View& a, int d, cudaStream_t st) {
     const int64_t blocks = (int64_t)a.S * a.Hk * ((a.cap + KT - 1) / KT);
-    return by_type(dtype, d, [&](auto tag, auto dim) {
-        using E = decltype(tag);
-        constexpr int D = decltype(dim)::value;
-        return launch(column_sums_simt_kernel<E, D>, blocks, 128, sizeof(SimtSmem<D>), st, a);
-    });
+    if (d == 64) return launch(column_sums_f32_kernel<64>, blocks, 128, sizeof(SumSmem<64>), st, a);
+    return launch(column_sums_f32_kernel<128>, blocks, 128, sizeof(SumSmem<128>), st, a);
 }
 
 }  // namespace shared

@@ -44,7 +44,7 @@ struct View {
     int32_t accumulate;
     // partial results of a row: slots [0, np) the prefix's splits, [np, np + no) its own keys'
     int32_t np, no;
-    // 1: the slots are no pieces of one list of 64-key tiles, the prefix's and then the own ones (np is 0)
+    // 1 (np is 0): the slots are no pieces of one list of 64-key tiles, the prefix's and then the own ones
     int32_t listed;
     float2* part_ml;  // [R][np + no] (max, sum)
     float* part_o;    // [np + no][R][d]
@@ -77,16 +77,29 @@ __device__ __forceinline__ void split_range(int n, int ns, int j, int& lo, int& 
     lo = (int)min((int64_t)n, c * j);
     hi = (int)min((int64_t)n, c * (j + 1));
 }
+// Piece j of `no` of a list of 64-key tiles, those of pl prefix keys and then
+// those of n own keys: prefix keys [pa, pb), own keys [oa, ob).
+struct Piece {
+    int pa, pb, oa, ob;
+    __device__ bool empty() const { return pa >= pb && oa >= ob; }
+};
+__device__ __forceinline__ Piece list_piece(int pl, int n, int no, int j) {
+    const int pt = (pl + KEY_STEP - 1) / KEY_STEP, all = pt + (n + KEY_STEP - 1) / KEY_STEP;
+    const int64_t per = (all + no - 1) / no;
+    const int t0 = (int)min((int64_t)all, per * j), t1 = (int)min((int64_t)all, per * j + per);
+    Piece p;
+    p.pa = min(pl, t0 * KEY_STEP);
+    p.pb = min(pl, t1 * KEY_STEP);
+    p.oa = min(n, max(0, t0 - pt) * KEY_STEP);
+    p.ob = min(n, max(0, t1 - pt) * KEY_STEP);
+    return p;
+}
 // Whether slot j of the partial results of a row with pk prefix keys and ok own keys was written.
 __device__ __forceinline__ bool slot_valid(const View& a, int j, int pk, int ok) {
+    if (a.listed) return !list_piece(pk, ok, a.no, j).empty();
+    if (j >= a.np) return !list_piece(0, ok, a.no, j - a.np).empty();
     int lo, hi;
-    if (a.listed) {
-        const int all = (pk + KEY_STEP - 1) / KEY_STEP + (ok + KEY_STEP - 1) / KEY_STEP;
-        const int64_t per = (all + a.no - 1) / a.no;
-        return per * j < all;
-    }
-    if (j < a.np) split_range(pk, a.np, j, lo, hi);
-    else split_range(ok, a.no, j - a.np, lo, hi);
+    split_range(pk, a.np, j, lo, hi);
     return lo < hi;
 }
 // Row of (sequence, query head, query) in lse and the partial arrays.
@@ -208,12 +221,13 @@ cudaError_t launch_column_sums_umma(const View& a, int d, cudaStream_t st);
 cudaError_t launch_prefix_umma(const View& a, int d, cudaStream_t st);
 cudaError_t launch_append(const View& a, int dtype, int d, const void* k_t, const int64_t* kts, const void* v_t,
                           const int64_t* vts, const float* w_t, cudaStream_t st);
-cudaError_t launch_attend_simt(const View& a, int dtype, int d, cudaStream_t st);
+cudaError_t launch_attend_f32(const View& a, int d, cudaStream_t st);
 cudaError_t prepare_shared_stream();
 // beside: launched right behind the prefixes' kernel, whose end this launch's end includes
 cudaError_t launch_stream(const View& a, int d, int warps_per_head, bool beside, cudaStream_t st);
 cudaError_t launch_combine(const View& a, int dtype, int d, cudaStream_t st);
-cudaError_t launch_column_sums_simt(const View& a, int dtype, int d, cudaStream_t st);
+cudaError_t launch_column_sums_f32(const View& a, int d, cudaStream_t st);
+cudaError_t prepare_shared_f32();
 cudaError_t prepare_shared_evict();
 size_t evict_bytes(int heads, int cap);
 cudaError_t launch_evict(const View& a, int dtype, int d, const int32_t* budget, int recent, int slack,

@@ -74,57 +74,61 @@ View view_of(const hkv_shared_cache* c) {
     return a;
 }
 
-// The kernels of an attention call, and how its keys are split over blocks:
-//   fp32       CUDA cores, whatever the rows;
-//   bf16       rows of one (sequence, KV head) up to STREAM_ROWS: own keys by
-//              the streaming kernel, the prefixes' for all their sequences'
-//              rows on the tensor cores; more rows: tensor cores, prefix and own keys
-//              in one pass, cut only where there are too few row tiles.
+// The kernels of an attention call, and how its keys are split over blocks.
+// Few rows a (sequence, KV head) (STREAM_ROWS): the own keys are streamed; the
+// prefix's either with them (folded: each sequence reads it again, from L2) or
+// once for the rows of all its sequences, by tiles that leave partial results
+// for the joining kernel.  Folding saves that kernel and the joining, and costs
+// the re-reads: see FOLD_BYTES.  More rows: prefix and own keys in one pass, cut
+// only where there are too few row tiles.
 struct Plan {
     bool umma_prefix, umma_rows, stream;
     int warps_per_head;  // of the stream kernel
     size_t bytes;
 };
 
+// Prefix rows read by all sequences together up to which they are folded.
+constexpr int64_t FOLD_BYTES = 48 << 20;
+
 Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char* base) {
     a.T = T;
     a.accumulate = accumulate;
     const int64_t rps = (int64_t)a.rep * T, R = (int64_t)a.S * a.H * T, heads = (int64_t)a.S * a.Hk;
-    const bool stream = rps <= hkv::shared::STREAM_ROWS;
+    const bool few = rps <= hkv::shared::STREAM_ROWS, bf16 = dtype == HKV_DTYPE_BF16;
+    const bool fold = a.G == 0 || !few || heads * a.pcap * d * (bf16 ? 4 : 8) <= FOLD_BYTES;
+    const int64_t keys = (int64_t)a.cap + (fold && a.G ? a.pcap : 0);  // of a list of keys, at most
     Plan p;
-    p.stream = dtype == HKV_DTYPE_BF16 && stream;
+    p.stream = bf16 && few;
+    p.umma_rows = bf16 && !few;
+    p.umma_prefix = bf16 && !fold;
     p.warps_per_head = 1;
-    p.umma_rows = dtype == HKV_DTYPE_BF16 && !stream;
-    p.umma_prefix = dtype == HKV_DTYPE_BF16 && stream && a.G > 0;
     // `want` blocks over `tiles`, at least `least` keys a split
-    auto splits = [&](int64_t want, int64_t tiles, int64_t keys, int64_t least) {
-        int64_t n = (want + tiles - 1) / tiles, most = (keys + least - 1) / least;
+    auto splits = [&](int64_t want, int64_t tiles, int64_t n_keys, int64_t least) {
+        int64_t n = (want + tiles - 1) / tiles, most = (n_keys + least - 1) / least;
         n = n < most ? n : most;
         return (int)(n < 1 ? 1 : n > hkv::shared::MAX_SPLITS ? hkv::shared::MAX_SPLITS : n);
     };
-    a.np = 0;
-    a.listed = 0;
+    a.listed = fold;
     a.lcap = (a.cap + 3) & ~3;
     if (p.umma_rows) {
         const int nt = hkv::shared::umma_row_tiles(rps);
         const int64_t items = heads * ((rps + 128 * nt - 1) / (128 * nt));
-        a.listed = 1;
-        a.no = items >= 148 ? 1 : splits(nt == 2 ? 148 : 296, items, (int64_t)a.cap + (a.G ? a.pcap : 0), 256);
+        a.no = items >= 148 ? 1 : splits(nt == 2 ? 148 : 296, items, keys, 256);
     } else if (p.stream) {
         // eight warps fit an SM: a head goes to as many as fill the GPU, one or several blocks of four
-        const int64_t warps = (148 * 8 + heads / 2) / heads, most = ((int64_t)a.cap + 31) / 32;
+        const int64_t warps = (148 * 8 + heads / 2) / heads, most = (keys + 31) / 32;
         const int64_t n = warps < most ? warps : most;
-        p.warps_per_head = n > 2 ? 4 : 1;
-        a.no = splits(n > 2 ? (n + 2) / 4 : n, 1, a.cap, 64);
+        p.warps_per_head = n > 1 ? 4 : 1;
+        a.no = splits((n + 2) / 4, 1, keys, 64);
     } else {
-        a.no = splits(148 * 6, heads * ((rps + 15) / 16), a.cap, 128);
+        const int64_t items = heads * ((rps + 15) / 16);
+        a.no = items >= 148 * 2 ? 1 : splits(148 * 4, items, keys, 128);
     }
-    if (!p.umma_rows) {
-        if (a.G) {
-            const int64_t tiles = (a.S * rps + 127) / 128, groups = a.G < a.S ? a.G : a.S;
-            a.np = p.umma_prefix ? splits(296, a.Hk * (tiles > groups ? tiles : groups), a.pcap, 128)
-                                 : splits(148 * 6, a.Hk * (a.S * rps / 16 + 1), a.pcap, 128);
-        }
+    a.np = 0;
+    if (!fold) {
+        const int64_t tiles = (a.S * rps + 127) / 128, groups = a.G < a.S ? a.G : a.S;
+        a.np = bf16 ? splits(296, a.Hk * (tiles > groups ? tiles : groups), a.pcap, 128)
+                    : splits(148 * 6, a.Hk * (a.S * rps / 16 + 1), a.pcap, 128);
     }
     size_t o = 0;
     auto take = [&](size_t bytes) {
@@ -133,13 +137,13 @@ Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char
         return q;
     };
     const size_t ns = a.np + a.no;
-    if (!p.umma_rows || ns > 1) {
+    if (ns > 1) {
         a.part_ml = (float2*)take(ns * R * sizeof(float2));
         a.part_o = (float*)take(ns * R * d * sizeof(float));
     }
-    if (accumulate && stream) a.logit = (float*)take((size_t)heads * rps * a.lcap * 4);
     a.fused_sums = accumulate && p.umma_rows && a.no == 1 && rps <= 256;
-    if (accumulate && !stream && !a.fused_sums) a.row_lse = (float*)take((size_t)R * 4);
+    if (accumulate && few) a.logit = (float*)take((size_t)heads * rps * a.lcap * 4);
+    if (accumulate && !few && !a.fused_sums) a.row_lse = (float*)take((size_t)R * 4);
     p.bytes = o;
     return p;
 }
@@ -155,6 +159,7 @@ cudaError_t prepare() {
     e = hkv::shared::prepare_shared_umma();
     if (e == cudaSuccess) e = hkv::shared::prepare_shared_stream();
     if (e == cudaSuccess) e = hkv::shared::prepare_shared_evict();
+    if (e == cudaSuccess) e = hkv::shared::prepare_shared_f32();
     if (e == cudaSuccess && dev < 64) ready.fetch_or(bit);
     return e;
 }
@@ -222,11 +227,11 @@ hkv_status hkv_shared_attend(const hkv_shared_cache* c, const void* q, const int
     if (e == cudaSuccess && p.umma_rows) e = hkv::shared::launch_attend_umma(a, d, st);
     if (e == cudaSuccess && p.umma_prefix) e = hkv::shared::launch_prefix_umma(a, d, st);
     if (e == cudaSuccess && p.stream) e = hkv::shared::launch_stream(a, d, p.warps_per_head, p.umma_prefix, st);
-    if (e == cudaSuccess && !p.umma_rows && !p.stream) e = hkv::shared::launch_attend_simt(a, c->dtype, d, st);
+    if (e == cudaSuccess && c->dtype == HKV_DTYPE_F32) e = hkv::shared::launch_attend_f32(a, d, st);
     if (e == cudaSuccess && a.part_ml) e = hkv::shared::launch_combine(a, c->dtype, d, st);
     if (e == cudaSuccess && a.row_lse)
         e = p.umma_rows ? hkv::shared::launch_column_sums_umma(a, d, st)
-                        : hkv::shared::launch_column_sums_simt(a, c->dtype, d, st);
+                        : hkv::shared::launch_column_sums_f32(a, d, st);
     return cuda_status(e);
 }
 

@@ -59,6 +59,8 @@ template <int D> constexpr int stream_smem() { return SW * SN * 2 * SK * D * 2; 
 // WPH warps of a block work on one (sequence, KV head, key range): 1 (four
 // heads a block, nothing to join) or 4 (steps dealt out in turn, joined in
 // shared memory).  LOW: at most 8 rows, the upper half of the M side is empty.
+// Where the item has all of the rows' keys (no splits, the prefix listed with
+// the own keys) the results are final, the accumulated weights too.
 template <int D, int WPH, bool LOW>
 __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_constant__ View a, int beside) {
     extern __shared__ __align__(1024) unsigned char raw[];
@@ -72,9 +74,12 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
     const int j = on ? item % a.no : 0, sh = on ? item / a.no : 0;
     const int s = sh / a.Hk, hk = sh % a.Hk;
     const int n = own_len(a, s, hk);
-    int lo, hi;
-    split_range(n, a.no, j, lo, hi);
-    const bool work = on && lo < hi;
+    // this item's keys: a piece of the prefix's (where they are listed with the
+    // own ones, see the caller) and of the own
+    const int pg = a.listed ? prefix_of(a, s) : -1;
+    const Piece pc = list_piece(prefix_len(a, pg), n, a.no, j);
+    const bool final = a.np + a.no == 1;
+    const bool work = on && !pc.empty();
     constexpr int CH = D / 8;  // 16-byte pieces of a row
     constexpr int NT = LOW ? 1 : 2;
 
@@ -91,20 +96,26 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
         const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(a.k) + s * a.ks[0] + hk * a.ks[1];
         const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(a.v) + s * a.vs[0] + hk * a.vs[1];
         const uint32_t stage0 = ptx::smem_u32(raw) + warp * SN * 2 * SK * D * 2;
-        const int steps = (hi - lo + SK - 1) / SK;
+        const __nv_bfloat16* pkb = static_cast<const __nv_bfloat16*>(a.pk) + (pg < 0 ? 0 : pg) * a.pks[0] + hk * a.pks[1];
+        const __nv_bfloat16* pvb = static_cast<const __nv_bfloat16*>(a.pv) + (pg < 0 ? 0 : pg) * a.pvs[0] + hk * a.pvs[1];
+        const int psteps = (pc.pb - pc.pa + SK - 1) / SK, steps = psteps + (pc.ob - pc.oa + SK - 1) / SK;
         const int mine = wi < steps ? (steps - wi + WPH - 1) / WPH : 0;
         auto load = [&](int i) {  // this warp's i-th step
             if (i < mine) {
-                const int k0 = lo + (i * WPH + wi) * SK;
+                const int st = i * WPH + wi;
+                const bool pre = st < psteps;
+                const int k0 = pre ? pc.pa + st * SK : pc.oa + (st - psteps) * SK, hi = pre ? pc.pb : pc.ob;
+                const __nv_bfloat16 *kp = pre ? pkb : kb, *vp = pre ? pvb : vb;
+                const int64_t kst = pre ? a.pks[2] : a.ks[2], vst = pre ? a.pvs[2] : a.vs[2];
                 const uint32_t kd = stage0 + (i % SN) * 2 * SK * D * 2, vd = kd + SK * D * 2;
 #pragma unroll
                 for (int e = 0; e < SK * CH / 32; ++e) {
                     const int idx = e * 32 + lane, r = idx / CH, c = idx % CH;
                     const bool in = k0 + r < hi;
-                    const int64_t key = in ? k0 + r : lo;
+                    const int64_t key = in ? k0 + r : k0;
                     const uint32_t off = r * (D * 2) + ((c ^ (r & 7)) << 4);
-                    cp16(kd + off, kb + key * a.ks[2] + c * 8, in);
-                    cp16(vd + off, vb + key * a.vs[2] + c * 8, in);
+                    cp16(kd + off, kp + key * kst + c * 8, in);
+                    cp16(vd + off, vp + key * vst + c * 8, in);
                 }
             }
             cp_commit();
@@ -118,7 +129,7 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
         for (int u = 0; u < 2; ++u) {
             const int i = g + 8 * u;
             const bool live = i < rps && u < NT;
-            lim[u] = live ? min(hi, own_limit(a, n, i)) : 0;
+            lim[u] = live ? min(pc.ob, own_limit(a, n, i)) : 0;
             const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + s * a.qs[0] +
                                       (hk * a.rep + i % a.rep) * a.qs[1] + i / a.rep * a.qs[2];
 #pragma unroll
@@ -135,7 +146,9 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
             cp_wait<SN - 2>();
             __syncwarp();
             load(i + SN - 1);  // into the stage of step i - 1, which every lane has left
-            const int k0 = lo + (i * WPH + wi) * SK;
+            const int st = i * WPH + wi;
+            const bool pre = st < psteps;
+            const int k0 = pre ? pc.pa + st * SK : pc.oa + (st - psteps) * SK, hi = pre ? pc.pb : pc.ob;
             const uint32_t ks = stage0 + (i % SN) * 2 * SK * D * 2, vs = ks + SK * D * 2;
             float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
             {
@@ -159,10 +172,10 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float& y = x[h][2 * u + e];
-                        y = key + e < lim[u] ? y * a.qscale : -INFINITY;
+                        y = key + e < (pre ? hi : lim[u]) ? y * a.qscale : -INFINITY;
                         mt[u] = fmaxf(mt[u], y);
                     }
-                    if (lrow[u] && key < hi)
+                    if (lrow[u] && !pre && key < hi)
                         *reinterpret_cast<float2*>(lrow[u] + key) = make_float2(x[h][2 * u], x[h][2 * u + 1]);
                 }
             }
@@ -217,8 +230,42 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
         }
     }
     const int slot = a.np + j;
+    const float* lg = a.logit + (int64_t)sh * rps * a.lcap;
+    float* w = a.weight + (int64_t)sh * a.cap;
     if constexpr (WPH == 1) {
-        if (work) {
+        if (final) {
+            // the warp has all of its rows' keys
+            float inv[2] = {0.f, 0.f};
+            if (on) {
+#pragma unroll
+                for (int u = 0; u < NT; ++u) {
+                    const int i = g + 8 * u;
+                    if (i >= rps) continue;
+                    const bool some = !(m[u] == -INFINITY);
+                    inv[u] = some ? 1.f / l[u] : 0.f;
+                    const int h = hk * a.rep + i % a.rep, t = i / a.rep;
+                    __nv_bfloat16* po = static_cast<__nv_bfloat16*>(a.out) + s * a.os[0] + h * a.os[1] + t * a.os[2] + q2;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c)
+                        *reinterpret_cast<uint32_t*>(po + c * 8) = pack(o[c][2 * u] * inv[u], o[c][2 * u + 1] * inv[u]);
+                    if ((lane & 3) == 0 && a.lse)
+                        a.lse[row_index(a, s, h, t)] = some ? (m[u] + log2f(l[u])) * 0.6931471805599453f : -INFINITY;
+                }
+                if (a.logit) {
+                    __syncwarp();  // the logits that other lanes kept
+                    for (int k0 = 0; k0 < n; k0 += 32) {
+                        const int key = k0 + lane;
+                        float sum = 0.f;
+                        for (int i = 0; i < rps; ++i) {
+                            const float M = __shfl_sync(FULL_MASK, i < 8 ? m[0] : m[1], (i & 7) * 4);
+                            const float f = __shfl_sync(FULL_MASK, i < 8 ? inv[0] : inv[1], (i & 7) * 4);
+                            if (key < n && M != -INFINITY) sum += exp2f(lg[(int64_t)i * a.lcap + key] - M) * f;
+                        }
+                        if (key < n) w[key] += sum;
+                    }
+                }
+            }
+        } else if (work) {
 #pragma unroll
             for (int u = 0; u < NT; ++u) {
                 const int i = g + 8 * u;
@@ -235,7 +282,7 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
         // the four warps' states of the rows, joined by the block
         constexpr int ROWS = LOW ? 8 : 16, PITCH = D + 8;
         static_assert(SW * ROWS * PITCH * 4 <= stream_smem<D>(), "the states fit the stages");
-        __shared__ float2 ml[SW][ROWS];
+        __shared__ float2 ml[SW][ROWS], joined[ROWS];
         float* st = reinterpret_cast<float*>(raw);
         __syncthreads();  // every warp has left its stages
 #pragma unroll
@@ -248,7 +295,7 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
                     make_float2(o[c][2 * u], o[c][2 * u + 1]);
         }
         __syncthreads();
-        if (work) {
+        if (work || (final && on)) {
             for (int e = tid; e < min(ROWS, rps) * (D / 4); e += 32 * SW) {
                 const int i = e / (D / 4), c = e % (D / 4) * 4;
                 float M = -INFINITY, L = 0.f;
@@ -269,9 +316,33 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
                     }
                 }
                 const int64_t row = row_of(a, s, hk, i);
-                *reinterpret_cast<float4*>(a.part_o + (slot * R + row) * D + c) = acc;
-                if (c == 0) a.part_ml[ml_index(a, row, slot)] = make_float2(M, L);
+                if (final) {
+                    const bool some = !(M == -INFINITY);
+                    const float inv = some ? 1.f / L : 0.f;
+                    __nv_bfloat16* po = static_cast<__nv_bfloat16*>(a.out) + s * a.os[0] + (hk * a.rep + i % a.rep) * a.os[1] +
+                                        i / a.rep * a.os[2] + c;
+                    *reinterpret_cast<uint2*>(po) = make_uint2(pack(acc.x * inv, acc.y * inv), pack(acc.z * inv, acc.w * inv));
+                    if (c == 0) {
+                        if (a.lse) a.lse[row] = some ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+                        joined[i] = make_float2(M, inv);
+                    }
+                } else {
+                    *reinterpret_cast<float4*>(a.part_o + (slot * R + row) * D + c) = acc;
+                    if (c == 0) a.part_ml[ml_index(a, row, slot)] = make_float2(M, L);
+                }
             }
+        }
+        if (final && a.logit) {  // (the same for the whole block)
+            __syncthreads();
+            if (on)
+                for (int key = tid; key < n; key += 32 * SW) {
+                    float sum = 0.f;
+                    for (int i = 0; i < rps; ++i) {
+                        const float2 y = joined[i];
+                        if (y.x != -INFINITY) sum += exp2f(lg[(int64_t)i * a.lcap + key] - y.x) * y.y;
+                    }
+                    w[key] += sum;
+                }
         }
     }
     // this grid ends after the one it was launched beside (the prefixes')

@@ -201,7 +201,7 @@ class SharedPrefixCache:
         if plan is None:
             plan = self._plan(q.shape[2], accumulate)
         T, accumulate, need, lse_like, scratch_like = plan
-        if not (qs[0] and qs[1] and qs[2]):
+        if not (qs[0] and qs[1] and qs[2]) and any(n > 1 and st == 0 for n, st in zip(q.shape, q.stride())):
             raise ValueError("q: no repeated rows")
         if scale is None:
             scale = 0.0

@@ -94,7 +94,7 @@ def test_scratch_sizes():
     c = cache()
     assert L.hkv_shared_attend_bytes(C.byref(c), 1, 1, C.byref(n)) == 0
     assert L.hkv_shared_attend_bytes(C.byref(c), 1, 0, C.byref(m)) == 0
-    assert 0 < m.value <= n.value < 64 << 20
+    assert 0 <= m.value <= n.value < 64 << 20
     assert L.hkv_shared_evict_bytes(C.byref(c), C.byref(n)) == 0
     assert n.value <= 4 * 2 * 96 * 8 + 4096
     # no prefixes: their pointers are not looked at
