@@ -103,37 +103,74 @@ cudaError_t launch_append(const View& a, int dtype, int d, const void* k_t, cons
 // attention in fp32, on the CUDA cores (fp32 products stay fp32)
 // ---------------------------------------------------------------------------
 
-constexpr int RT = 16;   // rows of a block
-constexpr int KT = 32;   // keys a step
-
-template <int D> struct F32Smem {
+// A block's shape: four warps of RW rows each, steps of 32 KPL keys in ST
+// stages.  Few rows (up to 16 of a head): 4 x 4 rows, two stages.  More: 4 x 8
+// rows, and two keys a lane where d = 64 leaves the shared memory for it: a
+// warp then reads 10 times from shared memory for 64 fused multiply-adds
+// instead of 5 for 16; one stage, so that four blocks share an SM and hide each
+// other's loads.
+template <int D, int RW_, int KPL_, int ST_> struct F32Shape {
+    static constexpr int WARPS = 4, RW = RW_, KPL = KPL_, ST = ST_, THREADS = 32 * WARPS;
+    static constexpr int RT = WARPS * RW, KT = 32 * KPL;
     static constexpr int KP = D + 4;  // padded rows: float4 reads of 32 rows spread over the banks
-    float q[RT][KP];
-    float k[2][KT][KP];
-    float v[2][KT][D];
-    float p[KT][RT];
-    float2 ml[RT];
-    int list[RT + 1];
-    int res[4];
+    struct Smem {
+        float q[RT][KP];
+        float k[ST][KT][KP];
+        float v[ST][KT][D];
+        float p[KT][RT];
+        float2 ml[RT];
+        int list[RT + 1];
+        int res[4];
+    };
+    struct SumSmem {
+        float q[RT][KP];
+        float k[KT][KP];
+        float part[WARPS][KT];
+    };
 };
+template <int D> using FewF32 = F32Shape<D, 4, 1, 2>;
+template <int D> using ManyF32 = F32Shape<D, 8, D == 64 ? 2 : 1, 1>;
+
+// x[u][p] = q row u . k row lane + 32 p, for a warp's rows and p < N (0 beyond).
+template <int D, int N, int RW, int KPL, int KP>
+__device__ __forceinline__ void dots(float (&x)[RW][KPL], const float (*q)[KP], const float (*k)[KP], int lane) {
+#pragma unroll
+    for (int u = 0; u < RW; ++u)
+#pragma unroll
+        for (int p = 0; p < KPL; ++p) x[u][p] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+        float4 kk[N];
+#pragma unroll
+        for (int p = 0; p < N; ++p) kk[p] = *reinterpret_cast<const float4*>(&k[lane + 32 * p][c]);
+#pragma unroll
+        for (int u = 0; u < RW; ++u) {
+            const float4 qq = *reinterpret_cast<const float4*>(&q[u][c]);
+#pragma unroll
+            for (int p = 0; p < N; ++p)
+                x[u][p] = fmaf(kk[p].x, qq.x, fmaf(kk[p].y, qq.y, fmaf(kk[p].z, qq.z, fmaf(kk[p].w, qq.w, x[u][p]))));
+        }
+    }
+}
 
 __device__ __forceinline__ void cp16(void* dst, const void* src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
                  : "memory");
 }
 
-// One block per (tile of 16 rows, keys): first the prefixes' tiles, whose rows
+// One block per (tile of RT rows, keys): first the prefixes' tiles, whose rows
 // come from all their sequences (np > 0), then tiles of one (sequence, KV
-// head) over a piece of its list of keys.  Steps of 32 keys, the next one's on
-// their way.  Warp w owns rows 4w .. 4w + 3: lane = key for the logits, lanes
-// across d for the weighted sum.  Where a block has all of its rows' keys the
+// head) over a piece of its list of keys.  The next step's keys are on their
+// way.  A warp owns RW rows: lane = key for the logits, lanes across d for the
+// weighted sum.  Where a block has all of its rows' keys the
 // result is final, and, with the logits kept (one tile has all the head's
 // rows), so are the accumulated weights.
-template <int D>
-__global__ void __launch_bounds__(128) attend_f32_kernel(const __grid_constant__ View a, int ptiles, int otiles) {
+template <int D, typename C>
+__global__ void __launch_bounds__(C::THREADS, 4) attend_f32_kernel(const __grid_constant__ View a, int ptiles, int otiles) {
     extern __shared__ __align__(16) unsigned char raw[];
-    F32Smem<D>& sm = *reinterpret_cast<F32Smem<D>*>(raw);
-    int* cnt = reinterpret_cast<int*>(raw + sizeof(F32Smem<D>));
+    constexpr int RT = C::RT, KT = C::KT, RW = C::RW, KPL = C::KPL, THREADS = C::THREADS;
+    typename C::Smem& sm = *reinterpret_cast<typename C::Smem*>(raw);
+    int* cnt = reinterpret_cast<int*>(raw + sizeof(typename C::Smem));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rps = a.rep * a.T;
     const int64_t R = (int64_t)a.S * a.H * a.T;
@@ -179,6 +216,7 @@ __global__ void __launch_bounds__(128) attend_f32_kernel(const __grid_constant__
     const float* pvb = static_cast<const float*>(a.pv) + (g < 0 ? 0 : g) * a.pvs[0] + hk * a.pvs[1];
     const float* kb = static_cast<const float*>(a.k) + s * a.ks[0] + hk * a.ks[1];
     const float* vb = static_cast<const float*>(a.v) + s * a.vs[0] + hk * a.vs[1];
+    constexpr int ST = C::ST;
     auto load = [&](int st) {
         if (st < steps) {
             const bool pre = st < psteps;
@@ -186,122 +224,143 @@ __global__ void __launch_bounds__(128) attend_f32_kernel(const __grid_constant__
             const float *kp = pre ? pkb : kb, *vp = pre ? pvb : vb;
             const int64_t kst = pre ? a.pks[2] : a.ks[2], vst = pre ? a.pvs[2] : a.vs[2];
 #pragma unroll
-            for (int e = 0; e < KT * (D / 4) / 128; ++e) {
-                const int idx = e * 128 + tid, r = idx / (D / 4), c = idx % (D / 4) * 4;
+            for (int e = 0; e < KT * (D / 4) / THREADS; ++e) {
+                const int idx = e * THREADS + tid, r = idx / (D / 4), c = idx % (D / 4) * 4;
                 const bool on = k0 + r < hi;
                 const int64_t key = on ? k0 + r : k0;
-                cp16(&sm.k[st & 1][r][c], kp + key * kst + c, on);
-                cp16(&sm.v[st & 1][r][c], vp + key * vst + c, on);
+                cp16(&sm.k[st % ST][r][c], kp + key * kst + c, on);
+                cp16(&sm.v[st % ST][r][c], vp + key * vst + c, on);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     load(0);
-    for (int e = tid; e < RT * (D / 4); e += 128) {
+    for (int e = tid; e < RT * (D / 4); e += THREADS) {
         const int r = e / (D / 4), c = e % (D / 4) * 4;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < rows) {
             int sq, i;
             seq_row(r, sq, i);
+            const int t = query_of(a, i);
             x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + sq * a.qs[0] +
-                                                 (hk * a.rep + i % a.rep) * a.qs[1] + i / a.rep * a.qs[2] + c);
+                                                 (hk * a.rep + i - t * a.rep) * a.qs[1] + t * a.qs[2] + c);
         }
         *reinterpret_cast<float4*>(&sm.q[r][c]) = make_float4(x.x * a.qscale, x.y * a.qscale, x.z * a.qscale, x.w * a.qscale);
     }
     constexpr int V = D / 32;
-    float m[4], l[4], o[4][V];
-    int lim[4];
+    float m[RW], l[RW], o[RW][V];
+    int lim[RW];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int r = warp * 4 + u;
+    for (int u = 0; u < RW; ++u) {
+        const int r = warp * RW + u;
         m[u] = -INFINITY;
         l[u] = 0.f;
 #pragma unroll
         for (int c = 0; c < V; ++c) o[u][c] = 0.f;
         lim[u] = r >= rows || is_prefix ? 0 : own_limit(a, n_own, first + r);
     }
-    float* lrow = keep ? a.logit + ((int64_t)(s * a.Hk + hk) * rps + warp * 4) * a.lcap : nullptr;
-    const bool idle = warp * 4 >= rows;
+    float* lrow = keep ? a.logit + ((int64_t)(s * a.Hk + hk) * rps + warp * RW) * a.lcap : nullptr;
+    const bool idle = warp * RW >= rows;
+    int lim_last = 0;
+#pragma unroll
+    for (int u = 0; u < RW; ++u) lim_last = max(lim_last, lim[u]);
     for (int st = 0; st < steps; ++st) {
-        load(st + 1);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        if constexpr (ST == 2) {
+            load(st + 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
         __syncthreads();
-        if (!idle) {
-            const bool pre = st < psteps;
-            const int k0 = pre ? pc.pa + st * KT : pc.oa + (st - psteps) * KT, hi = pre ? pc.pb : pc.ob;
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-            for (int c = 0; c < D; c += 4) {
-                const float4 kk = *reinterpret_cast<const float4*>(&sm.k[st & 1][lane][c]);
+        const bool pre = st < psteps;
+        const int k0 = pre ? pc.pa + st * KT : pc.oa + (st - psteps) * KT, hi = pre ? pc.pb : pc.ob;
+        // keys that some row of the warp sees (the last row sees the most)
+        const int need = (pre || keep ? hi : min(hi, lim_last)) - k0;
+        if (!idle && need > 0) {
+            float x[RW][KPL], mt[RW];
+            const int groups = KPL == 1 || need <= 32 ? 1 : KPL;  // of 32 keys
+            if (groups == KPL) dots<D, KPL>(x, &sm.q[warp * RW], sm.k[st % ST], lane);
+            else dots<D, 1>(x, &sm.q[warp * RW], sm.k[st % ST], lane);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const float4 qq = *reinterpret_cast<const float4*>(&sm.q[warp * 4 + u][c]);
-                    x[u] = fmaf(kk.x, qq.x, fmaf(kk.y, qq.y, fmaf(kk.z, qq.z, fmaf(kk.w, qq.w, x[u]))));
+            for (int u = 0; u < RW; ++u) {
+                mt[u] = -INFINITY;
+#pragma unroll
+                for (int p = 0; p < KPL; ++p) {
+                    const int key = k0 + lane + 32 * p;
+                    const bool in = key < hi && (pre ? warp * RW + u < rows : key < lim[u]);
+                    x[u][p] = in ? x[u][p] : -INFINITY;
+                    if (lrow && !pre && key < hi && warp * RW + u < rows) lrow[(int64_t)u * a.lcap + key] = x[u][p];
+                    mt[u] = fmaxf(mt[u], x[u][p]);
                 }
-            }
-            const int key = k0 + lane;
-            float pw[4], mt[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const bool in = key < hi && (pre ? warp * 4 + u < rows : key < lim[u]);
-                x[u] = in ? x[u] : -INFINITY;
-                if (lrow && !pre && key < hi && warp * 4 + u < rows) lrow[(int64_t)u * a.lcap + key] = x[u];
-                mt[u] = x[u];
             }
 #pragma unroll
             for (int off = 16; off; off >>= 1)
 #pragma unroll
-                for (int u = 0; u < 4; ++u) mt[u] = fmaxf(mt[u], __shfl_xor_sync(FULL_MASK, mt[u], off));
+                for (int u = 0; u < RW; ++u) mt[u] = fmaxf(mt[u], __shfl_xor_sync(FULL_MASK, mt[u], off));
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < RW; ++u) {
                 const float mn = fmaxf(m[u], mt[u]);
                 const float mb = mn == -INFINITY ? 0.f : mn;
                 const float alpha = exp2f(m[u] - mb);
-                pw[u] = exp2f(x[u] - mb);
-                l[u] = l[u] * alpha + pw[u];  // each lane its own keys; summed at the end
+                l[u] *= alpha;  // each lane its own keys; summed at the end
+#pragma unroll
+                for (int p = 0; p < KPL; ++p) {
+                    x[u][p] = exp2f(x[u][p] - mb);
+                    l[u] += x[u][p];
+                }
                 m[u] = mn;
 #pragma unroll
                 for (int c = 0; c < V; ++c) o[u][c] *= alpha;
             }
-            *reinterpret_cast<float4*>(&sm.p[lane][warp * 4]) = make_float4(pw[0], pw[1], pw[2], pw[3]);
+#pragma unroll
+            for (int p = 0; p < KPL; ++p)
+#pragma unroll
+                for (int u = 0; u < RW; u += 4)
+                    *reinterpret_cast<float4*>(&sm.p[lane + 32 * p][warp * RW + u]) =
+                        make_float4(x[u][p], x[u + 1][p], x[u + 2][p], x[u + 3][p]);
             __syncwarp();
-#pragma unroll 8
-            for (int kk = 0; kk < KT; ++kk) {
-                const float4 p4 = *reinterpret_cast<const float4*>(&sm.p[kk][warp * 4]);
-                const float pr[4] = {p4.x, p4.y, p4.z, p4.w};
-                float vv[V];
+#pragma unroll 4
+            for (int kk = 0; kk < 32 * groups; ++kk) {
+                float pr[RW], vv[V];
+#pragma unroll
+                for (int u = 0; u < RW; u += 4) {
+                    const float4 p4 = *reinterpret_cast<const float4*>(&sm.p[kk][warp * RW + u]);
+                    pr[u] = p4.x; pr[u + 1] = p4.y; pr[u + 2] = p4.z; pr[u + 3] = p4.w;
+                }
                 if constexpr (V == 4) {
-                    const float4 y = *reinterpret_cast<const float4*>(&sm.v[st & 1][kk][lane * 4]);
+                    const float4 y = *reinterpret_cast<const float4*>(&sm.v[st % ST][kk][lane * 4]);
                     vv[0] = y.x; vv[1] = y.y; vv[2] = y.z; vv[3] = y.w;
                 } else {
-                    const float2 y = *reinterpret_cast<const float2*>(&sm.v[st & 1][kk][lane * 2]);
+                    const float2 y = *reinterpret_cast<const float2*>(&sm.v[st % ST][kk][lane * 2]);
                     vv[0] = y.x; vv[1] = y.y;
                 }
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
+                for (int u = 0; u < RW; ++u)
 #pragma unroll
                     for (int c = 0; c < V; ++c) o[u][c] = fmaf(pr[u], vv[c], o[u][c]);
             }
         }
         __syncthreads();  // the stage is loaded again next
+        if constexpr (ST == 1) load(st + 1);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!idle) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int r = warp * 4 + u;
+        for (int u = 0; u < RW; ++u) {
+            const int r = warp * RW + u;
             float ls = l[u];
 #pragma unroll
             for (int off = 16; off; off >>= 1) ls += __shfl_xor_sync(FULL_MASK, ls, off);
             if (r >= rows) continue;
             int sq, i;
             seq_row(r, sq, i);
-            const int64_t row = row_of(a, sq, hk, i);
+            const int t = query_of(a, i), h = hk * a.rep + i - t * a.rep;
+            const int64_t row = row_index(a, sq, h, t);
             // (a sum that is NaN, of NaN logits alone, must not pass for an empty row)
             if (ls != ls && m[u] == -INFINITY) m[u] = 0.f;
             const bool some = !(m[u] == -INFINITY);
             const float f = !final ? 1.f : some ? 1.f / ls : 0.f;
-            float* po = final ? static_cast<float*>(a.out) + s * a.os[0] + (hk * a.rep + i % a.rep) * a.os[1] + i / a.rep * a.os[2]
+            float* po = final ? static_cast<float*>(a.out) + s * a.os[0] + h * a.os[1] + t * a.os[2]
                               : a.part_o + (slot * R + row) * D;
             if constexpr (V == 4)
                 *reinterpret_cast<float4*>(po + lane * 4) = make_float4(o[u][0] * f, o[u][1] * f, o[u][2] * f, o[u][3] * f);
@@ -323,7 +382,7 @@ __global__ void __launch_bounds__(128) attend_f32_kernel(const __grid_constant__
     __syncthreads();
     const float* lg = a.logit + (int64_t)(s * a.Hk + hk) * rps * a.lcap;
     float* w = a.weight + (int64_t)(s * a.Hk + hk) * a.cap;
-    for (int j = tid; j < n_own; j += 128) {
+    for (int j = tid; j < n_own; j += THREADS) {
         float sum = 0.f;
         for (int i = 0; i < rps; ++i) {
             const float2 y = sm.ml[i];
@@ -491,80 +550,88 @@ __global__ void __launch_bounds__(128, 8) combine_kernel(const __grid_constant__
 // accumulated weights of many rows: the logits once more, summed by key
 // ---------------------------------------------------------------------------
 
-// One block per (sequence, KV head, 32 keys): lane = key, warp w takes rows
-// 4w .. 4w + 3 of every tile of 16; a key's weight 2^(x - lse) over the rows
-// that see it, per tile, then over the tiles, then over the warps.
-template <int D> struct SumSmem {
-    float q[RT][D + 4];
-    float k[KT][D + 4];
-    float p[4][KT];
-};
-
-template <int D>
-__global__ void __launch_bounds__(128) column_sums_f32_kernel(const __grid_constant__ View a) {
+// One block per (sequence, KV head, KT keys): lane = key, the warps share the
+// rows of each tile; a key's weight 2^(x - lse) over the rows that see it, per
+// tile, then over the tiles, then over the warps.  The next rows are on their
+// way.
+template <int D, typename C>
+__global__ void __launch_bounds__(C::THREADS, 4) column_sums_f32_kernel(const __grid_constant__ View a) {
     extern __shared__ __align__(16) unsigned char raw[];
-    SumSmem<D>& sm = *reinterpret_cast<SumSmem<D>*>(raw);
+    constexpr int RT = C::RT, KT = C::KT, RW = C::RW, KPL = C::KPL, THREADS = C::THREADS;
+    typename C::SumSmem& sm = *reinterpret_cast<typename C::SumSmem*>(raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int chunks = (a.cap + KT - 1) / KT;
-    const int sh = blockIdx.x / chunks, k0 = blockIdx.x % chunks * KT;
+    // the first keys, which the most queries see, first
+    const int heads = a.S * a.Hk, sh = blockIdx.x % heads, k0 = blockIdx.x / heads * KT;
     const int s = sh / a.Hk, hk = sh % a.Hk, rps = a.rep * a.T;
     ptx::grid_dep_wait();
     const int n = own_len(a, s, hk);
     if (k0 >= n) return;
     const float* kb = static_cast<const float*>(a.k) + s * a.ks[0] + hk * a.ks[1];
-    for (int e = tid; e < KT * (D / 4); e += 128) {
+    for (int e = tid; e < KT * (D / 4); e += THREADS) {
         const int r = e / (D / 4), c = e % (D / 4) * 4;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k0 + r < n) x = *reinterpret_cast<const float4*>(kb + (int64_t)(k0 + r) * a.ks[2] + c);
-        *reinterpret_cast<float4*>(&sm.k[r][c]) = x;
+        cp16(&sm.k[r][c], kb + (int64_t)(k0 + r < n ? k0 + r : k0) * a.ks[2] + c, k0 + r < n);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
     // the first row that sees key k0: n - T + t + 1 > k0
     const int t0 = max(0, k0 - (n - a.T));
-    const int key = k0 + lane;
-    float total = 0.f;
-    for (int f = t0 * a.rep / RT * RT; f < rps; f += RT) {
-        __syncthreads();
-        const int rows = min(RT, rps - f);
-        for (int e = tid; e < RT * (D / 4); e += 128) {
-            const int r = e / (D / 4), c = e % (D / 4) * 4;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < rows) {
-                const int i = f + r;
-                x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + s * a.qs[0] +
-                                                     (hk * a.rep + i % a.rep) * a.qs[1] + i / a.rep * a.qs[2] + c);
-            }
-            sm.q[r][c] = x.x * a.qscale;
-            sm.q[r][c + 1] = x.y * a.qscale;
-            sm.q[r][c + 2] = x.z * a.qscale;
-            sm.q[r][c + 3] = x.w * a.qscale;
-        }
-        __syncthreads();
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-        for (int c = 0; c < D; c += 4) {
-            const float4 kk = *reinterpret_cast<const float4*>(&sm.k[lane][c]);
+    constexpr int Q4 = RT * (D / 4) / THREADS;
+    float4 next[Q4];
+    auto fetch = [&](int f) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float4 qq = *reinterpret_cast<const float4*>(&sm.q[warp * 4 + u][c]);
-                x[u] = fmaf(kk.x, qq.x, fmaf(kk.y, qq.y, fmaf(kk.z, qq.z, fmaf(kk.w, qq.w, x[u]))));
-            }
+        for (int e = 0; e < Q4; ++e) {
+            const int idx = e * THREADS + tid, i = f + idx / (D / 4), c = idx % (D / 4) * 4;
+            const int t = query_of(a, i);
+            next[e] = i < rps ? *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + s * a.qs[0] +
+                                                                 (hk * a.rep + i - t * a.rep) * a.qs[1] + t * a.qs[2] + c)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        float tile = 0.f;
+    };
+    const int f0 = t0 * a.rep / RT * RT;
+    fetch(f0);
+    float total[KPL];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int r = warp * 4 + u;
-            if (r >= rows) continue;
-            const float e = a.row_lse[row_of(a, s, hk, f + r)];
-            if (key < n && key < own_limit(a, n, f + r) && e != -INFINITY) tile += exp2f(x[u] - e);
+    for (int p = 0; p < KPL; ++p) total[p] = 0.f;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    for (int f = f0; f < rps; f += RT) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < Q4; ++e) {
+            const int idx = e * THREADS + tid;
+            const float4 y = next[e];
+            *reinterpret_cast<float4*>(&sm.q[idx / (D / 4)][idx % (D / 4) * 4]) =
+                make_float4(y.x * a.qscale, y.y * a.qscale, y.z * a.qscale, y.w * a.qscale);
         }
-        total += tile;
+        __syncthreads();
+        if (f + RT < rps) fetch(f + RT);
+        float lse[RW];
+#pragma unroll
+        for (int u = 0; u < RW; ++u) {
+            const int i = f + warp * RW + u;
+            lse[u] = i < rps ? a.row_lse[row_of(a, s, hk, i)] : -INFINITY;
+        }
+        if (f + warp * RW >= rps) continue;
+        float x[RW][KPL], tile[KPL];
+        dots<D, KPL>(x, &sm.q[warp * RW], sm.k, lane);
+#pragma unroll
+        for (int p = 0; p < KPL; ++p) tile[p] = 0.f;
+#pragma unroll
+        for (int u = 0; u < RW; ++u)
+#pragma unroll
+            for (int p = 0; p < KPL; ++p)
+                if (lse[u] != -INFINITY && k0 + lane + 32 * p < own_limit(a, n, f + warp * RW + u))
+                    tile[p] += exp2f(x[u][p] - lse[u]);
+#pragma unroll
+        for (int p = 0; p < KPL; ++p) total[p] += tile[p];
     }
+#pragma unroll
+    for (int p = 0; p < KPL; ++p) sm.part[warp][lane + 32 * p] = total[p];
     __syncthreads();
-    float* red = &sm.p[0][0];
-    red[warp * 32 + lane] = total;
-    __syncthreads();
-    if (warp == 0 && key < n)
-        a.weight[(int64_t)sh * a.cap + key] += (red[lane] + red[32 + lane]) + (red[64 + lane] + red[96 + lane]);
+    if (tid < KT && k0 + tid < n) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) sum += sm.part[w][tid];
+        a.weight[(int64_t)sh * a.cap + k0 + tid] += sum;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -582,23 +649,46 @@ template <typename F> cudaError_t by_type(int dtype, int d, F&& f) {
 
 }  // namespace
 
-cudaError_t launch_attend_f32(const View& a, int d, cudaStream_t st) {
-    const int rps = a.rep * a.T, otiles = (rps + RT - 1) / RT;
-    const int64_t ptiles = a.np ? max_prefix_tiles(a.S, a.G, rps, RT) : 0;
+namespace {
+
+template <int D, typename C> cudaError_t attend_f32(const View& a, cudaStream_t st) {
+    const int rps = a.rep * a.T, otiles = (rps + C::RT - 1) / C::RT;
+    const int64_t ptiles = a.np ? max_prefix_tiles(a.S, a.G, rps, C::RT) : 0;
     const int64_t blocks = ptiles * a.Hk * a.np + (int64_t)a.S * a.Hk * otiles * a.no;
-    auto go = [&](auto dim) {
-        constexpr int D = decltype(dim)::value;
-        return launch(attend_f32_kernel<D>, blocks, 128, sizeof(F32Smem<D>) + (size_t)a.G * 4, st, a, (int)ptiles, otiles);
-    };
-    return d == 64 ? go(std::integral_constant<int, 64>()) : go(std::integral_constant<int, 128>());
+    return launch(attend_f32_kernel<D, C>, blocks, C::THREADS, sizeof(typename C::Smem) + (size_t)a.G * 4, st, a,
+                  (int)ptiles, otiles);
+}
+template <int D, typename C> cudaError_t prepare_f32() {
+    cudaError_t e = cudaFuncSetAttribute(attend_f32_kernel<D, C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(typename C::Smem) + MAX_PREFIXES * 4);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(column_sums_f32_kernel<D, ManyF32<D>>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)sizeof(typename ManyF32<D>::SumSmem));
+    return e;
+}
+template <int D> cudaError_t sums_f32(const View& a, cudaStream_t st) {
+    using C = ManyF32<D>;
+    return launch(column_sums_f32_kernel<D, C>, (int64_t)a.S * a.Hk * ((a.cap + C::KT - 1) / C::KT), C::THREADS,
+                  sizeof(typename C::SumSmem), st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_f32(const View& a, int d, cudaStream_t st) {
+    if (a.rep * a.T <= STREAM_ROWS)
+        return d == 64 ? attend_f32<64, FewF32<64>>(a, st) : attend_f32<128, FewF32<128>>(a, st);
+    return d == 64 ? attend_f32<64, ManyF32<64>>(a, st) : attend_f32<128, ManyF32<128>>(a, st);
+}
+
+cudaError_t launch_column_sums_f32(const View& a, int d, cudaStream_t st) {
+    return d == 64 ? sums_f32<64>(a, st) : sums_f32<128>(a, st);
 }
 
 cudaError_t prepare_shared_f32() {
-    cudaError_t e = cudaFuncSetAttribute(attend_f32_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(F32Smem<64>) + MAX_PREFIXES * 4);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(attend_f32_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)sizeof(F32Smem<128>) + MAX_PREFIXES * 4);
+    cudaError_t e = prepare_f32<64, FewF32<64>>();
+    if (e == cudaSuccess) e = prepare_f32<128, FewF32<128>>();
+    if (e == cudaSuccess) e = prepare_f32<64, ManyF32<64>>();
+    if (e == cudaSuccess) e = prepare_f32<128, ManyF32<128>>();
     return e;
 }
 
@@ -613,12 +703,6 @@ cudaError_t launch_combine(const View& a, int dtype, int d, cudaStream_t st) {
         if (rps <= 8) return launch(combine_kernel<E, D, 8>, blocks, 128, 0, st, a, (int)rb);
         return launch(combine_kernel<E, D, STREAM_ROWS>, blocks, 128, 0, st, a, (int)rb);
     });
-}
-
-cudaError_t launch_column_sums_f32(const View& a, int d, cudaStream_t st) {
-    const int64_t blocks = (int64_t)a.S * a.Hk * ((a.cap + KT - 1) / KT);
-    if (d == 64) return launch(column_sums_f32_kernel<64>, blocks, 128, sizeof(SumSmem<64>), st, a);
-    return launch(column_sums_f32_kernel<128>, blocks, 128, sizeof(SumSmem<128>), st, a);
 }
 
 }  // namespace shared

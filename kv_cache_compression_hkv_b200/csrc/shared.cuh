@@ -25,6 +25,7 @@ constexpr int STREAM_ROWS = 16;
 // The cache and one call's tensors, by value.
 struct View {
     int32_t S, H, Hk, rep, cap, G, pcap, T;
+    uint64_t rep_inv;  // ceil(2^40 / rep), see query_of
     void *k, *v;
     int64_t ks[3], vs[3];
     int32_t* pos;
@@ -107,13 +108,18 @@ __device__ __forceinline__ int64_t row_index(const View& a, int s, int h, int t)
     return ((int64_t)s * a.H + h) * a.T + t;
 }
 __device__ __forceinline__ int64_t ml_index(const View& a, int64_t row, int slot) { return row * (a.np + a.no) + slot; }
-// Rows of one (sequence, KV head) are numbered i = t * rep + (query head within the KV head).
+// Rows of one (sequence, KV head) are numbered i = t * rep + (query head within
+// the KV head).  i / rep by multiplication (exact for i < 2^24 and rep < 2^16:
+// the product is too large by less than i rep / 2^40 < 1 / rep); kernels that
+// divided spent more on their rows' places than on reading them.
+__device__ __forceinline__ int query_of(const View& a, int i) { return (int)((uint64_t)i * a.rep_inv >> 40); }
 __device__ __forceinline__ int64_t row_of(const View& a, int s, int hk, int i) {
-    return row_index(a, s, hk * a.rep + i % a.rep, i / a.rep);
+    const int t = query_of(a, i);
+    return row_index(a, s, hk * a.rep + i - t * a.rep, t);
 }
 // Own slots row i sees: those before len - T + t + 1.
 __device__ __forceinline__ int own_limit(const View& a, int n, int i) {
-    const int lim = n - a.T + i / a.rep + 1;
+    const int lim = n - a.T + query_of(a, i) + 1;
     return lim < 0 ? 0 : lim;
 }
 

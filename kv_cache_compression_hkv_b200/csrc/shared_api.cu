@@ -37,7 +37,7 @@ bool cache_ok(const hkv_shared_cache* c) {
     if (c->dtype != HKV_DTYPE_F32 && c->dtype != HKV_DTYPE_BF16) return false;
     if (c->head_dim != 64 && c->head_dim != 128) return false;
     if (c->num_seqs < 1 || c->num_heads < 1 || c->num_kv_heads < 1 || c->num_heads % c->num_kv_heads) return false;
-    if ((int64_t)c->num_seqs * c->num_heads > kMaxRows) return false;
+    if ((int64_t)c->num_seqs * c->num_heads > kMaxRows || c->num_heads / c->num_kv_heads > 0xffff) return false;
     if (c->capacity < 1 || c->capacity > kMaxSlots) return false;
     if (c->num_prefixes < 0 || c->num_prefixes > hkv::shared::MAX_PREFIXES) return false;
     const int64_t es = c->dtype == HKV_DTYPE_F32 ? 4 : 2;
@@ -62,6 +62,7 @@ View view_of(const hkv_shared_cache* c) {
     View a;
     memset(&a, 0, sizeof(a));
     a.S = c->num_seqs; a.H = c->num_heads; a.Hk = c->num_kv_heads; a.rep = c->num_heads / c->num_kv_heads;
+    a.rep_inv = (((uint64_t)1 << 40) + a.rep - 1) / a.rep;
     a.cap = c->capacity; a.G = c->num_prefixes; a.pcap = c->prefix_capacity;
     a.k = c->k; a.v = c->v;
     a.pos = c->pos; a.weight = c->weight; a.len = c->len; a.next_pos = c->next_pos;
@@ -121,8 +122,8 @@ Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char
         p.warps_per_head = n > 1 ? 4 : 1;
         a.no = splits((n + 2) / 4, 1, keys, 64);
     } else {
-        const int64_t items = heads * ((rps + 15) / 16);
-        a.no = items >= 148 * 2 ? 1 : splits(148 * 4, items, keys, 128);
+        const int64_t items = heads * (few ? 1 : (rps + 31) / 32);
+        a.no = items >= 148 ? 1 : splits(148 * (few ? 4 : 2), items, keys, 128);
     }
     a.np = 0;
     if (!fold) {
@@ -165,7 +166,7 @@ cudaError_t prepare() {
 }
 
 bool queries_ok(const hkv_shared_cache* c, int T) {
-    return T >= 1 && T <= c->capacity && (int64_t)T * (c->num_heads / c->num_kv_heads) <= kMaxRows &&
+    return T >= 1 && T <= c->capacity && (int64_t)T * (c->num_heads / c->num_kv_heads) < kMaxRows &&
            (int64_t)c->num_seqs * c->num_heads * T <= (int64_t)1 << 30;
 }
 

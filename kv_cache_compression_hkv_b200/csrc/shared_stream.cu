@@ -130,8 +130,9 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
             const int i = g + 8 * u;
             const bool live = i < rps && u < NT;
             lim[u] = live ? min(pc.ob, own_limit(a, n, i)) : 0;
+            const int t = query_of(a, i);
             const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + s * a.qs[0] +
-                                      (hk * a.rep + i % a.rep) * a.qs[1] + i / a.rep * a.qs[2];
+                                      (hk * a.rep + i - t * a.rep) * a.qs[1] + t * a.qs[2];
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 qa[kk][u] = live ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + q2) : 0u;
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
                     if (i >= rps) continue;
                     const bool some = !(m[u] == -INFINITY);
                     inv[u] = some ? 1.f / l[u] : 0.f;
-                    const int h = hk * a.rep + i % a.rep, t = i / a.rep;
+                    const int t = query_of(a, i), h = hk * a.rep + i - t * a.rep;
                     __nv_bfloat16* po = static_cast<__nv_bfloat16*>(a.out) + s * a.os[0] + h * a.os[1] + t * a.os[2] + q2;
 #pragma unroll
                     for (int c = 0; c < D / 8; ++c)
@@ -319,8 +320,9 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
                 if (final) {
                     const bool some = !(M == -INFINITY);
                     const float inv = some ? 1.f / L : 0.f;
-                    __nv_bfloat16* po = static_cast<__nv_bfloat16*>(a.out) + s * a.os[0] + (hk * a.rep + i % a.rep) * a.os[1] +
-                                        i / a.rep * a.os[2] + c;
+                    const int t = query_of(a, i);
+                    __nv_bfloat16* po = static_cast<__nv_bfloat16*>(a.out) + s * a.os[0] +
+                                        (hk * a.rep + i - t * a.rep) * a.os[1] + t * a.os[2] + c;
                     *reinterpret_cast<uint2*>(po) = make_uint2(pack(acc.x * inv, acc.y * inv), pack(acc.z * inv, acc.w * inv));
                     if (c == 0) {
                         if (a.lse) a.lse[row] = some ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;

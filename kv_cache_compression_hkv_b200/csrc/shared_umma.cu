@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                 ri = f % rps;
             }
         }
-        h = hk * a.rep + ri % a.rep;
-        t = ri / a.rep;
+        t = query_of(a, ri);
+        h = hk * a.rep + ri - t * a.rep;
         const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
         const int64_t at = live ? sq * a.qs[0] + h * a.qs[1] + t * a.qs[2] : -1;
         const uint32_t tile = smem_u32(q_s + (warp >> 2) * C::Q_BYTES);
