@@ -12,6 +12,8 @@
 // rate is a third of what HBM leaves time for.)
 #include <math.h>
 
+#include <type_traits>
+
 #include "kernels.h"
 #include "ptx.cuh"
 #include "shared.cuh"
@@ -23,7 +25,7 @@ namespace shared {
 namespace {
 
 constexpr int SK = 16;   // keys of a step
-constexpr int SN = 3;    // stages of a warp
+constexpr int SN = 2;    // stages of a warp
 constexpr int SW = 4;    // warps of a block
 constexpr float RAISE = 16.f;
 
@@ -57,12 +59,12 @@ __device__ __forceinline__ uint32_t pack(float x, float y) {
 template <int D> constexpr int stream_smem() { return SW * SN * 2 * SK * D * 2; }
 
 // WPH warps of a block work on one (sequence, KV head, key range): 1 (four
-// heads a block, nothing to join) or 4 (steps dealt out in turn, joined in
+// heads a block, nothing to join), 2 or 4 (steps dealt out in turn, joined in
 // shared memory).  LOW: at most 8 rows, the upper half of the M side is empty.
 // Where the item has all of the rows' keys (no splits, the prefix listed with
 // the own keys) the results are final, the accumulated weights too.
 template <int D, int WPH, bool LOW>
-__global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_constant__ View a, int beside) {
+__global__ void __launch_bounds__(32 * SW, 3) stream_attend_kernel(const __grid_constant__ View a, int beside) {
     extern __shared__ __align__(1024) unsigned char raw[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (!beside) ptx::grid_dep_wait();
@@ -73,6 +75,23 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
     const bool on = item < a.S * a.Hk * a.no;
     const int j = on ? item % a.no : 0, sh = on ? item / a.no : 0;
     const int s = sh / a.Hk, hk = sh % a.Hk;
+    constexpr int NT = LOW ? 1 : 2;
+    const int g = lane >> 2, q2 = (lane & 3) * 2;  // this thread's rows g, g + 8; columns q2, q2 + 1
+    // Q fragments (on their way while the lengths are looked up)
+    uint32_t qa[D / 16][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int i = g + 8 * u;
+        const bool live = on && i < rps && u < NT;
+        const int t = query_of(a, i);
+        const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + s * a.qs[0] + (hk * a.rep + i - t * a.rep) * a.qs[1] +
+                                  t * a.qs[2];
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            qa[kk][u] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + kk * 16 + q2)) : 0u;
+            qa[kk][2 + u] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + kk * 16 + q2 + 8)) : 0u;
+        }
+    }
     const int n = own_len(a, s, hk);
     // this item's keys: a piece of the prefix's (where they are listed with the
     // own ones, see the caller) and of the own
@@ -81,7 +100,6 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
     const bool final = a.np + a.no == 1;
     const bool work = on && !pc.empty();
     constexpr int CH = D / 8;  // 16-byte pieces of a row
-    constexpr int NT = LOW ? 1 : 2;
 
     // accumulators: 16 rows x D, fragments of 8 columns
     float o[D / 8][4];
@@ -90,7 +108,6 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
     for (int c = 0; c < D / 8; ++c)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
-    const int g = lane >> 2, q2 = (lane & 3) * 2;  // this thread's rows g, g + 8; columns q2, q2 + 1
 
     if (work) {
         const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(a.k) + s * a.ks[0] + hk * a.ks[1];
@@ -100,45 +117,53 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
         const __nv_bfloat16* pvb = static_cast<const __nv_bfloat16*>(a.pv) + (pg < 0 ? 0 : pg) * a.pvs[0] + hk * a.pvs[1];
         const int psteps = (pc.pb - pc.pa + SK - 1) / SK, steps = psteps + (pc.ob - pc.oa + SK - 1) / SK;
         const int mine = wi < steps ? (steps - wi + WPH - 1) / WPH : 0;
+        // A lane's pieces of a step: piece c0 of rows r0, r0 + RPI, ...; in shared
+        // memory piece c of row r lies at r (2 D) + ((c ^ (r & 7)) << 4).  Rows are
+        // a power of two apart, so both come from one place by adding and xoring
+        // constants (with a multiplication for each piece the step took 500
+        // instructions instead of <INSTR>).
+        constexpr int RPI = 32 / CH, ITER = SK / RPI;
+        const int r0 = lane / CH, c0 = lane % CH;
+        const uint32_t dst0 = stage0 + r0 * (D * 2) + ((c0 ^ r0) << 4);
         auto load = [&](int i) {  // this warp's i-th step
             if (i < mine) {
                 const int st = i * WPH + wi;
                 const bool pre = st < psteps;
                 const int k0 = pre ? pc.pa + st * SK : pc.oa + (st - psteps) * SK, hi = pre ? pc.pb : pc.ob;
-                const __nv_bfloat16 *kp = pre ? pkb : kb, *vp = pre ? pvb : vb;
                 const int64_t kst = pre ? a.pks[2] : a.ks[2], vst = pre ? a.pvs[2] : a.vs[2];
-                const uint32_t kd = stage0 + (i % SN) * 2 * SK * D * 2, vd = kd + SK * D * 2;
+                const __nv_bfloat16* kp = (pre ? pkb : kb) + (k0 + r0) * kst + c0 * 8;
+                const __nv_bfloat16* vp = (pre ? pvb : vb) + (k0 + r0) * vst + c0 * 8;
+                const uint32_t kd = dst0 + (i % SN) * 2 * SK * D * 2;
+                if (k0 + SK <= hi) {
 #pragma unroll
-                for (int e = 0; e < SK * CH / 32; ++e) {
-                    const int idx = e * 32 + lane, r = idx / CH, c = idx % CH;
-                    const bool in = k0 + r < hi;
-                    const int64_t key = in ? k0 + r : k0;
-                    const uint32_t off = r * (D * 2) + ((c ^ (r & 7)) << 4);
-                    cp16(kd + off, kp + key * kst + c * 8, in);
-                    cp16(vd + off, vp + key * vst + c * 8, in);
+                    for (int e = 0; e < ITER; ++e) {
+                        const uint32_t d = (kd ^ ((e * RPI & 7) << 4)) + e * RPI * (D * 2);
+                        cp16(d, kp, true);
+                        cp16(d + SK * D * 2, vp, true);
+                        kp += RPI * kst;
+                        vp += RPI * vst;
+                    }
+                } else {  // rows past the last key: zeros
+#pragma unroll
+                    for (int e = 0; e < ITER; ++e) {
+                        const uint32_t d = (kd ^ ((e * RPI & 7) << 4)) + e * RPI * (D * 2);
+                        const bool in = k0 + r0 + e * RPI < hi;
+                        cp16(d, in ? kp + e * RPI * kst : kb, in);
+                        cp16(d + SK * D * 2, in ? vp + e * RPI * vst : vb, in);
+                    }
                 }
             }
             cp_commit();
         };
 #pragma unroll
         for (int i = 0; i < SN - 1; ++i) load(i);
-        // Q fragments
-        uint32_t qa[D / 16][4];
         int lim[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int i = g + 8 * u;
-            const bool live = i < rps && u < NT;
-            lim[u] = live ? min(pc.ob, own_limit(a, n, i)) : 0;
-            const int t = query_of(a, i);
-            const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + s * a.qs[0] +
-                                      (hk * a.rep + i - t * a.rep) * a.qs[1] + t * a.qs[2];
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                qa[kk][u] = live ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + q2) : 0u;
-                qa[kk][2 + u] = live ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + q2 + 8) : 0u;
-            }
-        }
+        for (int u = 0; u < 2; ++u) lim[u] = g + 8 * u < rps && u < NT ? min(pc.ob, own_limit(a, n, g + 8 * u)) : 0;
+        // where a lane's row addresses of K's and V's fragments start: pieces 2 kk + cb of row r
+        const int kr = ((lane >> 4) << 3) + (lane & 7), vr = ((lane >> 3) & 1) * 8 + (lane & 7);
+        const uint32_t k_frag = kr * (D * 2) + ((((lane >> 3) & 1) ^ (kr & 7)) << 4);
+        const uint32_t v_frag = vr * (D * 2) + (((lane >> 4) ^ (vr & 7)) << 4);
         float* lrow[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -153,11 +178,11 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
             const uint32_t ks = stage0 + (i % SN) * 2 * SK * D * 2, vs = ks + SK * D * 2;
             float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
             {
-                const int r = ((lane >> 4) << 3) + (lane & 7), cb = (lane >> 3) & 1;
+                const uint32_t k_at = ks + k_frag;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     uint32_t b[4];
-                    ldsm4(ks + r * (D * 2) + (((kk * 2 + cb) ^ (r & 7)) << 4), b);
+                    ldsm4(k_at ^ (kk << 5), b);
                     mma16816(x[0], qa[kk], b[0], b[1]);
                     mma16816(x[1], qa[kk], b[2], b[3]);
                 }
@@ -211,11 +236,11 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
                 }
             }
             {
-                const int r = ((lane >> 3) & 1) * 8 + (lane & 7), cb = lane >> 4;
+                const uint32_t v_at = vs + v_frag;
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c) {
                     uint32_t b[4];
-                    ldsm4t(vs + r * (D * 2) + (((c * 2 + cb) ^ (r & 7)) << 4), b);
+                    ldsm4t(v_at ^ (c << 5), b);
                     mma16816(o[2 * c], pa, b[0], b[1]);
                     mma16816(o[2 * c + 1], pa, b[2], b[3]);
                 }
@@ -254,15 +279,25 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
                 }
                 if (a.logit) {
                     __syncwarp();  // the logits that other lanes kept
-                    for (int k0 = 0; k0 < n; k0 += 32) {
-                        const int key = k0 + lane;
-                        float sum = 0.f;
+                    for (int k0 = lane; k0 - lane < n; k0 += 128) {
+                        float sum[4], old[4];
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            sum[v] = 0.f;
+                            old[v] = k0 + 32 * v < n ? w[k0 + 32 * v] : 0.f;
+                        }
                         for (int i = 0; i < rps; ++i) {
                             const float M = __shfl_sync(FULL_MASK, i < 8 ? m[0] : m[1], (i & 7) * 4);
                             const float f = __shfl_sync(FULL_MASK, i < 8 ? inv[0] : inv[1], (i & 7) * 4);
-                            if (key < n && M != -INFINITY) sum += exp2f(lg[(int64_t)i * a.lcap + key] - M) * f;
+                            if (M == -INFINITY) continue;
+                            const float* x = lg + (int64_t)i * a.lcap + k0;
+#pragma unroll
+                            for (int v = 0; v < 4; ++v)
+                                if (k0 + 32 * v < n) sum[v] += exp2f(x[32 * v] - M) * f;
                         }
-                        if (key < n) w[key] += sum;
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            if (k0 + 32 * v < n) w[k0 + 32 * v] = old[v] + sum[v];
                     }
                 }
             }
@@ -280,10 +315,10 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
             }
         }
     } else {
-        // the four warps' states of the rows, joined by the block
+        // the warps' states of the rows, joined by the warps of the head
         constexpr int ROWS = LOW ? 8 : 16, PITCH = D + 8;
         static_assert(SW * ROWS * PITCH * 4 <= stream_smem<D>(), "the states fit the stages");
-        __shared__ float2 ml[SW][ROWS], joined[ROWS];
+        __shared__ float2 ml[SW][ROWS], joined[SW / WPH][ROWS];
         float* st = reinterpret_cast<float*>(raw);
         __syncthreads();  // every warp has left its stages
 #pragma unroll
@@ -297,17 +332,18 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
         }
         __syncthreads();
         if (work || (final && on)) {
-            for (int e = tid; e < min(ROWS, rps) * (D / 4); e += 32 * SW) {
+            const int w0 = warp / WPH * WPH;  // the head's first warp
+            for (int e = wi * 32 + lane; e < min(ROWS, rps) * (D / 4); e += 32 * WPH) {
                 const int i = e / (D / 4), c = e % (D / 4) * 4;
                 float M = -INFINITY, L = 0.f;
 #pragma unroll
-                for (int w = 0; w < SW; ++w) M = fmaxf(M, ml[w][i].x);
+                for (int v = 0; v < WPH; ++v) M = fmaxf(M, ml[w0 + v][i].x);
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int w = 0; w < SW; ++w) {
-                    const float2 y = ml[w][i];
+                for (int v = 0; v < WPH; ++v) {
+                    const float2 y = ml[w0 + v][i];
                     const float f = y.x == -INFINITY ? 0.f : exp2f(y.x - M);
-                    const float4 z = *reinterpret_cast<const float4*>(st + (w * ROWS + i) * PITCH + c);
+                    const float4 z = *reinterpret_cast<const float4*>(st + ((w0 + v) * ROWS + i) * PITCH + c);
                     if (f != 0.f) {
                         L = fmaf(y.y, f, L);
                         acc.x = fmaf(z.x, f, acc.x);
@@ -326,7 +362,7 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
                     *reinterpret_cast<uint2*>(po) = make_uint2(pack(acc.x * inv, acc.y * inv), pack(acc.z * inv, acc.w * inv));
                     if (c == 0) {
                         if (a.lse) a.lse[row] = some ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
-                        joined[i] = make_float2(M, inv);
+                        joined[warp / WPH][i] = make_float2(M, inv);
                     }
                 } else {
                     *reinterpret_cast<float4*>(a.part_o + (slot * R + row) * D + c) = acc;
@@ -337,13 +373,25 @@ __global__ void __launch_bounds__(32 * SW) stream_attend_kernel(const __grid_con
         if (final && a.logit) {  // (the same for the whole block)
             __syncthreads();
             if (on)
-                for (int key = tid; key < n; key += 32 * SW) {
-                    float sum = 0.f;
-                    for (int i = 0; i < rps; ++i) {
-                        const float2 y = joined[i];
-                        if (y.x != -INFINITY) sum += exp2f(lg[(int64_t)i * a.lcap + key] - y.x) * y.y;
+                for (int k0 = wi * 32 + lane; k0 < n; k0 += 4 * 32 * WPH) {
+                    float sum[4], old[4];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const int key = k0 + 32 * WPH * v;
+                        sum[v] = 0.f;
+                        old[v] = key < n ? w[key] : 0.f;
                     }
-                    w[key] += sum;
+                    for (int i = 0; i < rps; ++i) {
+                        const float2 y = joined[warp / WPH][i];
+                        if (y.x == -INFINITY) continue;
+                        const float* x = lg + (int64_t)i * a.lcap + k0;
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            if (k0 + 32 * WPH * v < n) sum[v] += exp2f(x[32 * WPH * v] - y.x) * y.y;
+                    }
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        if (k0 + 32 * WPH * v < n) w[k0 + 32 * WPH * v] = old[v] + sum[v];
                 }
         }
     }
@@ -358,12 +406,14 @@ cudaError_t launch_stream(const View& a, int d, int warps_per_head, bool beside,
     auto run = [&](auto kernel) {
         return launch(kernel, blocks, 32 * SW, d == 128 ? stream_smem<128>() : stream_smem<64>(), st, a, (int)beside);
     };
-    const bool low = rps <= 8, one = warps_per_head == 1;
-    if (d == 128)
-        return one ? (low ? run(stream_attend_kernel<128, 1, true>) : run(stream_attend_kernel<128, 1, false>))
-                   : (low ? run(stream_attend_kernel<128, 4, true>) : run(stream_attend_kernel<128, 4, false>));
-    return one ? (low ? run(stream_attend_kernel<64, 1, true>) : run(stream_attend_kernel<64, 1, false>))
-               : (low ? run(stream_attend_kernel<64, 4, true>) : run(stream_attend_kernel<64, 4, false>));
+    const bool low = rps <= 8;
+    auto by_warps = [&](auto dim) {
+        constexpr int D = decltype(dim)::value;
+        if (warps_per_head == 1) return low ? run(stream_attend_kernel<D, 1, true>) : run(stream_attend_kernel<D, 1, false>);
+        if (warps_per_head == 2) return low ? run(stream_attend_kernel<D, 2, true>) : run(stream_attend_kernel<D, 2, false>);
+        return low ? run(stream_attend_kernel<D, 4, true>) : run(stream_attend_kernel<D, 4, false>);
+    };
+    return d == 128 ? by_warps(std::integral_constant<int, 128>()) : by_warps(std::integral_constant<int, 64>());
 }
 
 cudaError_t prepare_shared_stream() {
@@ -371,14 +421,17 @@ cudaError_t prepare_shared_stream() {
     auto set = [&](auto kernel, int smem) {
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     };
-    set(stream_attend_kernel<128, 1, true>, stream_smem<128>());
-    set(stream_attend_kernel<128, 1, false>, stream_smem<128>());
-    set(stream_attend_kernel<128, 4, true>, stream_smem<128>());
-    set(stream_attend_kernel<128, 4, false>, stream_smem<128>());
-    set(stream_attend_kernel<64, 1, true>, stream_smem<64>());
-    set(stream_attend_kernel<64, 1, false>, stream_smem<64>());
-    set(stream_attend_kernel<64, 4, true>, stream_smem<64>());
-    set(stream_attend_kernel<64, 4, false>, stream_smem<64>());
+    auto all = [&](auto dim) {
+        constexpr int D = decltype(dim)::value;
+        set(stream_attend_kernel<D, 1, true>, stream_smem<D>());
+        set(stream_attend_kernel<D, 1, false>, stream_smem<D>());
+        set(stream_attend_kernel<D, 2, true>, stream_smem<D>());
+        set(stream_attend_kernel<D, 2, false>, stream_smem<D>());
+        set(stream_attend_kernel<D, 4, true>, stream_smem<D>());
+        set(stream_attend_kernel<D, 4, false>, stream_smem<D>());
+    };
+    all(std::integral_constant<int, 64>());
+    all(std::integral_constant<int, 128>());
     return e;
 }
 
