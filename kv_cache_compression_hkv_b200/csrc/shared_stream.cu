@@ -25,7 +25,7 @@ namespace shared {
 namespace {
 
 constexpr int SK = 16;   // keys of a step
-constexpr int SN = 2;    // stages of a warp
+constexpr int SN = 3;    // stages of a warp
 constexpr int SW = 4;    // warps of a block
 constexpr float RAISE = 16.f;
 
@@ -64,7 +64,7 @@ template <int D> constexpr int stream_smem() { return SW * SN * 2 * SK * D * 2; 
 // Where the item has all of the rows' keys (no splits, the prefix listed with
 // the own keys) the results are final, the accumulated weights too.
 template <int D, int WPH, bool LOW>
-__global__ void __launch_bounds__(32 * SW, 3) stream_attend_kernel(const __grid_constant__ View a, int beside) {
+__global__ void __launch_bounds__(32 * SW, 2) stream_attend_kernel(const __grid_constant__ View a, int beside) {
     extern __shared__ __align__(1024) unsigned char raw[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (!beside) ptx::grid_dep_wait();
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(32 * SW, 3) stream_attend_kernel(const __grid_
         // memory piece c of row r lies at r (2 D) + ((c ^ (r & 7)) << 4).  Rows are
         // a power of two apart, so both come from one place by adding and xoring
         // constants (with a multiplication for each piece the step took 500
-        // instructions instead of <INSTR>).
+        // instructions instead of 370).
         constexpr int RPI = 32 / CH, ITER = SK / RPI;
         const int r0 = lane / CH, c0 = lane % CH;
         const uint32_t dst0 = stage0 + r0 * (D * 2) + ((c0 ^ r0) << 4);

@@ -623,13 +623,14 @@ namespace {
 
 template <int D> struct SumShape {
     static constexpr int KB = 128;      // keys of a block (MMA M)
-    static constexpr int QN = 64;       // queries of a tile (MMA N)
-    static constexpr int NS = 4;        // query tiles in flight: shared memory and S slots in TMEM alike
+    static constexpr int QN = 128;      // queries of a tile (MMA N)
+    static constexpr int NS = 2;        // query tiles in shared memory, and S slots in TMEM
+    static constexpr int NL = 4;        // places of the rows' sums
     static constexpr int THREADS = 256 + 64, COPY_WARP = 8, MMA_WARP = 9;
     static constexpr uint32_t TMEM = NS * QN;
     static constexpr int K_BYTES = KB * D * 2, Q_BYTES = QN * D * 2;
-    enum { B_K, B_FULL, B_FREE = B_FULL + NS, B_S = B_FREE + NS, B_COUNT = B_S + NS };
-    static constexpr int SMEM = 1024 + K_BYTES + NS * Q_BYTES + NS * QN * 4 + KB * 4 + B_COUNT * 8 + 16;
+    enum { B_K, B_FULL, B_FREE = B_FULL + NS, B_S = B_FREE + NS, B_SF = B_S + NS, B_COUNT = B_SF + NS };
+    static constexpr int SMEM = 1024 + K_BYTES + NS * Q_BYTES + NL * QN * 4 + KB * 4 + B_COUNT * 8 + 16;
 };
 
 }  // namespace
@@ -637,10 +638,11 @@ template <int D> struct SumShape {
 // weight[key] += sum over rows of 2^(c q.k - lse2[row]), the log2 of the row
 // sums being known: the logits once more, keys on the M side, so that a
 // thread owns a key (TMEM lane) and sums along its own columns.  One block
-// per (sequence, KV head, 128 keys) walks 64-query tiles of each query head
+// per (sequence, KV head, 128 keys) walks 128-query tiles of each query head
 // in turn, from the first query that sees its first key on; two groups of
-// four warps take every other tile.  A row that is not to be counted has
-// -lse2 = -inf there.
+// four warps take every other tile.  (With 64 queries a tile an MMA waits for
+// shared memory, which gives it the 128 keys again for every 64 queries: 408
+// cycles instead of 256.)  A row that is not to be counted has -lse2 = -inf.
 template <int D>
 __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
     column_sums_umma_kernel(const __grid_constant__ View a, const __grid_constant__ CUtensorMap km,
@@ -649,8 +651,8 @@ __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
     extern __shared__ unsigned char raw[];
     unsigned char* k_s = reinterpret_cast<unsigned char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     unsigned char* q_s = k_s + C::K_BYTES;
-    float* nl_s = reinterpret_cast<float*>(q_s + C::NS * C::Q_BYTES);  // [NS][QN]
-    float* half = nl_s + C::NS * C::QN;                                // [KB]
+    float* nl_s = reinterpret_cast<float*>(q_s + C::NS * C::Q_BYTES);  // [NL][QN]
+    float* half = nl_s + C::NL * C::QN;                                // [KB]
     uint64_t* bars = reinterpret_cast<uint64_t*>(half + C::KB);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::B_COUNT);
     constexpr int NSUB = D / 64;
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
 
     if (warp == 0) tc::alloc(tmem_slot, C::TMEM);
     if (tid == 0) {
-        for (int i = 0; i < C::B_COUNT; ++i) mbar_init(bars + i, i >= C::B_FREE && i < C::B_S ? 5 : 1);
+        for (int i = 0; i < C::B_COUNT; ++i) mbar_init(bars + i, i >= C::B_SF ? 4 : 1);
         ptx::fence_mbar_init();
     }
     tc::fence_before();
@@ -684,17 +686,26 @@ __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
             for (int sub = 0; sub < NSUB; ++sub) tc::tma_load_4d(k_s + sub * C::KB * 128, &km, bars + C::B_K, sub * 64, k0, hk, s);
         }
         int issued = 0;
+        // The sums of the next tile's rows are read a tile ahead.  Their places
+        // are free: Q's place is given back once S of tile j - 2 is done, and that
+        // S was issued after the rows had finished with tile j - 4.
+        float nl[C::QN / 32];
+        auto fetch = [&](int j) {
+            const float* src = a.row_lse + row_index(a, s, hk * a.rep + j / per_head, 0);
+#pragma unroll
+            for (int u = 0; u < C::QN / 32; ++u) {
+                const int t = (tile0 + j % per_head) * C::QN + u * 32 + lane;
+                const float e = j < tiles && t < a.T ? src[t] : -INFINITY;
+                nl[u] = e == -INFINITY ? -INFINITY : -e;
+            }
+        };
+        if (tiles > 0) fetch(0);
         for (int j = 0; j < tiles; ++j) {
             const int slot = j % C::NS, use = j / C::NS;
             if (use > 0 && __any_sync(FULL_MASK, !mbar_wait(bars + C::B_FREE + slot, (use - 1) & 1, WAIT_NS))) { fail = true; break; }
             const int h = hk * a.rep + j / per_head, t0 = (tile0 + j % per_head) * C::QN;
-            const float* src = a.row_lse + row_index(a, s, h, 0);
 #pragma unroll
-            for (int u = 0; u < C::QN; u += 32) {
-                const int t = t0 + u + lane;
-                const float e = t < a.T ? src[t] : -INFINITY;
-                nl_s[slot * C::QN + u + lane] = e == -INFINITY ? -INFINITY : -e;
-            }
+            for (int u = 0; u < C::QN / 32; ++u) nl_s[j % C::NL * C::QN + u * 32 + lane] = nl[u];
             __syncwarp();
             if (lane == 0) {
                 mbar_expect_tx(bars + C::B_FULL + slot, C::Q_BYTES);
@@ -702,6 +713,7 @@ __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
                     tc::tma_load_4d(q_s + slot * C::Q_BYTES + sub * C::QN * 128, &qm, bars + C::B_FULL + slot, sub * 64, t0, h, s);
             }
             issued = j + 1;
+            fetch(j + 1 < tiles ? j + 1 : j);
         }
         if (fail && lane == 0) {
             mbar_wait(bars + C::B_K, 0, WAIT_NS);
@@ -710,19 +722,21 @@ __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
         }
     } else if (warp == C::MMA_WARP) {
         constexpr uint32_t IS = tc::idesc_bf16(C::QN, false);
-        const bool leader = tc::elect();
         const uint32_t tm = tc::uniform(tmem);
         const uint64_t k_desc = tc::sw128_desc(tc::uniform(smem_u32(k_s)), 16, 1024),
                        q_desc = tc::sw128_desc(tc::uniform(smem_u32(q_s)), 16, 1024);
-        auto ok = [&](bool w) { return !__any_sync(FULL_MASK, !w); };
         const int nt = tc::uniform(tiles);
-        int done = -1;
-        if (!ok(mbar_wait(bars + C::B_K, 0, WAIT_NS))) fail = true;
-        for (int j = 0; j < nt && !fail; ++j) {
-            const int slot = j % C::NS;
-            if (!ok(mbar_wait(bars + C::B_FULL + slot, (j / C::NS) & 1, WAIT_NS))) { fail = true; break; }
-            tc::fence_after();
-            if (leader) {
+        if (tc::elect()) {
+            int done = -1;
+            if (!mbar_wait(bars + C::B_K, 0, WAIT_NS)) fail = true;
+            for (int j = 0; j < nt && !fail; ++j) {
+                const int slot = j % C::NS;
+                if (!mbar_wait(bars + C::B_FULL + slot, (j / C::NS) & 1, WAIT_NS) ||
+                    (j >= C::NS && !mbar_wait(bars + C::B_SF + slot, (j / C::NS - 1) & 1, WAIT_NS))) {
+                    fail = true;
+                    break;
+                }
+                tc::fence_after();
                 const uint64_t qd = q_desc + slot * (C::Q_BYTES / 16);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
@@ -730,15 +744,14 @@ __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
                                qd + (kk / 4) * (C::QN * 8) + (kk % 4) * 2, IS, kk > 0);
                 tc::commit(bars + C::B_S + slot);
                 tc::commit(bars + C::B_FREE + slot);
+                done = j;
             }
-            __syncwarp();
-            done = j;
+            if (done >= 0) {
+                mbar_wait(bars + C::B_S + done % C::NS, (done / C::NS) & 1, WAIT_NS);
+                mbar_wait(bars + C::B_FREE + done % C::NS, (done / C::NS) & 1, WAIT_NS);
+            }
         }
-        if (done >= 0) {
-            mbar_wait(bars + C::B_S + done % C::NS, (done / C::NS) & 1, WAIT_NS);
-            // (the row warps' arrivals complete the other barrier's phase)
-            if (!fail) mbar_wait(bars + C::B_FREE + done % C::NS, (done / C::NS) & 1, WAIT_NS);
-        }
+        __syncwarp();
     } else {
         const int grp = warp >> 2, key = k0 + (tid & 127);
         const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -748,33 +761,30 @@ __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
             const int slot = j % C::NS, t0 = (tile0 + j % per_head) * C::QN;
             if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_S + slot, (j / C::NS) & 1, WAIT_NS))) { fail = true; break; }
             tc::fence_after();
-            uint32_t sr[2][32];
-            tc::ld32(t_lane + slot * C::QN, sr[0]);
-            tc::ld32(t_lane + slot * C::QN + 32, sr[1]);
-            const float* nl = nl_s + slot * C::QN;
-            tc::ld_wait();
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            if (t0 >= last) {
+            const float* nl = nl_s + j % C::NL * C::QN;
+            const int from = key - shift - t0;  // columns before it do not see the key
+            const bool whole = t0 >= last;
 #pragma unroll
-                for (int u = 0; u < C::QN; u += 4) {
-                    const float4 e = *reinterpret_cast<const float4*>(nl + u);
-                    acc[0] += tc::ex2(fmaf(__uint_as_float(sr[u >> 5][u & 31]), c, e.x));
-                    acc[1] += tc::ex2(fmaf(__uint_as_float(sr[u >> 5][(u & 31) + 1]), c, e.y));
-                    acc[2] += tc::ex2(fmaf(__uint_as_float(sr[u >> 5][(u & 31) + 2]), c, e.z));
-                    acc[3] += tc::ex2(fmaf(__uint_as_float(sr[u >> 5][(u & 31) + 3]), c, e.w));
-                }
-            } else {
-                const int from = key - shift - t0;  // columns before it do not see the key
+            for (int c0 = 0; c0 < C::QN; c0 += 32) {
+                uint32_t o[32];
+                tc::ld32(t_lane + slot * C::QN + c0, o);
+                tc::ld_wait();
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int u = 0; u < C::QN; ++u) {
-                    const float p = tc::ex2(fmaf(__uint_as_float(sr[u >> 5][u & 31]), c, nl[u]));
-                    acc[u & 3] += u >= from ? p : 0.f;
+                for (int u = 0; u < 32; u += 4) {
+                    const float4 e = *reinterpret_cast<const float4*>(nl + c0 + u);
+                    const float ee[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const float p = tc::ex2(fmaf(__uint_as_float(o[u + v]), c, ee[v]));
+                        acc[v] += whole || c0 + u + v >= from ? p : 0.f;
+                    }
                 }
+                total += (acc[0] + acc[1]) + (acc[2] + acc[3]);
             }
-            total += (acc[0] + acc[1]) + (acc[2] + acc[3]);
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) tc::arrive(bars + C::B_FREE + slot);
+            if (lane == 0) tc::arrive(bars + C::B_SF + slot);
         }
         if (grp == 1) half[tid & 127] = total;
     }
@@ -868,7 +878,7 @@ cudaError_t launch_prefix_umma(const View& a, int d, cudaStream_t st) {
 
 cudaError_t launch_column_sums_umma(const View& a, int d, cudaStream_t st) {
     CUtensorMap km, qm;
-    if (!make_map(&km, a.k, d, a.cap, a.Hk, a.S, a.ks, 128) || !make_map(&qm, a.q, d, a.T, a.H, a.S, a.qs, 64))
+    if (!make_map(&km, a.k, d, a.cap, a.Hk, a.S, a.ks, 128) || !make_map(&qm, a.q, d, a.T, a.H, a.S, a.qs, 128))
         return cudaErrorInvalidValue;
     const int64_t blocks = (int64_t)a.S * a.Hk * ((a.cap + 127) / 128);
     if (d == 128) return launch(column_sums_umma_kernel<128>, blocks, SumShape<128>::THREADS, SumShape<128>::SMEM, st, a, km, qm);
