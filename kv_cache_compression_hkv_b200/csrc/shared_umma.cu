@@ -12,13 +12,15 @@
 // 16, so weights stay below 2^16 and bf16's relative rounding is unaffected;
 // the sum l is of the unrounded weights in fp32.
 // Roles: 4 NT softmax warps; a copy warp (TMA into a ring of pairs K0, V0 K1,
-// V1 K2, ... as they are used together); an MMA warp, one lane of which waits
-// and issues.
+// V1 K2, ... as they are used together); an MMA warp a row tile, one lane of
+// which waits and issues.
 // S of tile j + 1 is issued as soon as the rows hold S of tile j in registers,
 // so a softmax warp finds its next logits ready.  (With P over S's own place
 // and two such places, S of tile j + 2 had to wait for the product of tile j
 // behind the other row tile's: 2150 cycles a tile.)
 #include <math.h>
+
+#include <type_traits>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -43,8 +45,8 @@ constexpr uint64_t WAIT_NS = 2000000000ull;
 template <int D, int NT> struct Shape {
     static constexpr int NS = NT == 2 ? (D == 128 ? 4 : 6) : (D == 128 ? 2 : 3);  // (V, K) pairs in the ring
     static constexpr int ROWS = 128 * NT;
-    static constexpr int THREADS = ROWS + 64;
-    static constexpr int COPY_WARP = 4 * NT, MMA_WARP = 4 * NT + 1;
+    static constexpr int THREADS = ROWS + 32 + 32 * NT;
+    static constexpr int COPY_WARP = 4 * NT, MMA_WARP = 4 * NT + 1;  // MMA_WARP + x issues for row tile x
     static constexpr uint32_t O_COL = 128 * NT;  // before it, a row tile: 64 columns of S, two times 32 of P
     static constexpr uint32_t TMEM = NT == 2 ? 512 : 256;
     static constexpr int Q_BYTES = QT * D * 2, KV_BYTES = UK * D * 2;
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
     if (warp == 0) tc::alloc(tmem_slot, C::TMEM);
     if (tid == 0) {
         for (int i = 0; i < C::B_COUNT; ++i)
-            mbar_init(bars + i, i == C::B_Q ? 4 * NT : ((i >= C::B_SF && i < C::B_PV) || i >= C::B_TF) ? 4 : 1);
+            mbar_init(bars + i, i == C::B_Q ? 4 * NT : i >= C::B_FREE && i < C::B_S ? NT : ((i >= C::B_SF && i < C::B_PV) || i >= C::B_TF) ? 4 : 1);
         ptx::fence_mbar_init();
     }
     tc::fence_before();
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                 for (int i = max(0, issued - C::NS); i < issued; ++i)
                     mbar_wait(bars + C::B_FULL + i % C::NS, (i / C::NS) & 1, WAIT_NS);
         }
-    } else if (warp == C::MMA_WARP) {
+    } else if (warp >= C::MMA_WARP) {
         // All that an MMA's operands come from is made uniform first (with
         // addresses in per-thread registers an issue took 84 cycles, up to
         // three times the product), and one lane does the waiting too (votes
@@ -253,120 +255,75 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
         constexpr uint32_t IS = tc::idesc_bf16(UK, false), IO = tc::idesc_bf16(D, true);
         const uint32_t tm = tc::uniform(tmem);
         const int nn = tc::uniform(n);
-        int nu[NT];
-#pragma unroll
-        for (int x = 0; x < NT; ++x) nu[x] = tc::uniform(nx[x]);
+        const int x = NT == 1 ? 0 : warp - C::MMA_WARP;
+        const int nu = tc::uniform(NT == 1 || x == 0 ? nx[0] : nx[NT - 1]);
         const uint32_t ring_u = tc::uniform(smem_u32(ring)), q_u = tc::uniform(smem_u32(q_s));
-        const uint64_t q_desc = tc::sw128_desc(q_u, 16, 1024), k_desc = tc::sw128_desc(ring_u + C::KV_BYTES, 16, 1024),
+        const uint64_t q_desc = tc::sw128_desc(q_u + x * C::Q_BYTES, 16, 1024), k_desc = tc::sw128_desc(ring_u + C::KV_BYTES, 16, 1024),
                        v_desc = tc::sw128_desc(ring_u, UK * 128, 1024);
         if (tc::elect()) {
-            // What is ready goes: P V(x, j) once pair j + 1 is there and the
-            // weights are written; S(x, j) once pair j is there, the rows have
-            // read S(x, j - 1) and P V(x, j - 2) was issued (the commit behind S
-            // then covers it, which tells the rows that P's slot is free).  (In
-            // a fixed order S of one row tile waited for the weights of the
-            // other.)
-            int sj[NT], pj[NT];  // next tile of each
-#pragma unroll
-            for (int x = 0; x < NT; ++x) sj[x] = pj[x] = 0;
-            int there = 0, freed = 0;  // pairs known to have landed; pairs given back
-            auto landed = [&](int i) {
-                if (i < there) return true;
-                if (!ptx::mbar_test(bars + C::B_FULL + there % C::NS, (there / C::NS) & 1)) return false;
-                ++there;
-                return i < there;
-            };
-            // pair i is done with S of tile i and P V of tile i - 1
-            auto used = [&](int i) {
-                bool done = i <= nn;
-#pragma unroll
-                for (int x = 0; x < NT; ++x) done = done && sj[x] > min(i, nu[x] - 1) && pj[x] >= min(i, nu[x]);
-                return done;
+            // Pair i: S of tile i once it has landed and the rows have read S of
+            // tile i - 1, then P V of tile i - 1 once its weights are written.
+            // (One warp for both row tiles kept S of one waiting for the weights
+            // of the other.)  The commit behind S of tile i also covers P V of
+            // tile i - 2, which tells the rows that P's place is free.
+            const uint32_t t_s = tm + x * 128, t_o = tm + C::O_COL + x * D;
+            int s_done = -1, pv_done = -1, freed = 0, sums = 0;
+            auto full = [&](int i) { return mbar_wait(bars + C::B_FULL + i % C::NS, (i / C::NS) & 1, WAIT_NS); };
+            auto give_back = [&](int i) {
+                tc::commit(bars + C::B_FREE + i % C::NS);
+                ++freed;
             };
             if (!mbar_wait(bars + C::B_Q, 0, WAIT_NS)) fail = true;
-            uint32_t idle = 0;
-            uint64_t since = 0;
-            while (!fail && freed <= nn && nn > 0) {
-                bool went = false;
+            for (int i = 0; i <= nn && nn > 0 && !fail; ++i) {
+                if (!full(i)) { fail = true; break; }
+                const uint32_t pair = (i % C::NS) * (2 * C::KV_BYTES / 16);
+                if (i < nu) {
+                    if (i > 0 && !mbar_wait(bars + C::B_SF + x, (i - 1) & 1, WAIT_NS)) { fail = true; break; }
+                    tc::fence_after();
 #pragma unroll
-                for (int x = 0; x < NT; ++x) {
-                    if (pj[x] < sj[x] && landed(pj[x] + 1) &&
-                        ptx::mbar_test(bars + C::B_P + 2 * x + (pj[x] & 1), (pj[x] >> 1) & 1)) {
-                        tc::fence_after();
-                        const uint64_t vd = v_desc + ((pj[x] + 1) % C::NS) * (2 * C::KV_BYTES / 16);
-#pragma unroll
-                        for (int kk = 0; kk < UK / 16; ++kk)
-                            tc::mma_ts(tm + C::O_COL + x * D, tm + x * 128 + UK + (pj[x] & 1) * 32 + kk * 8, vd + kk * 128, IO,
-                                       (pj[x] > 0 || kk > 0));
-                        tc::commit(bars + C::B_PV + 2 * x + (pj[x] & 1));
-                        ++pj[x];
-                        went = true;
-                    }
-                    if (sj[x] < nu[x] && sj[x] <= pj[x] + 1 && landed(sj[x]) &&
-                        (sj[x] == 0 || ptx::mbar_test(bars + C::B_SF + x, (sj[x] - 1) & 1))) {
-                        tc::fence_after();
-                        const uint64_t qd = q_desc + x * (C::Q_BYTES / 16), kd = k_desc + (sj[x] % C::NS) * (2 * C::KV_BYTES / 16);
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)  // descriptors count 16-byte units
-                            tc::mma_ss(tm + x * 128, qd + (kk / 4) * (QT * 8) + (kk % 4) * 2,
-                                       kd + (kk / 4) * (UK * 8) + (kk % 4) * 2, IS, kk > 0);
-                        tc::commit(bars + C::B_S + x);
-                        ++sj[x];
-                        went = true;
-                    }
+                    for (int kk = 0; kk < D / 16; ++kk)  // descriptors count 16-byte units
+                        tc::mma_ss(t_s, q_desc + (kk / 4) * (QT * 8) + (kk % 4) * 2,
+                                   k_desc + pair + (kk / 4) * (UK * 8) + (kk % 4) * 2, IS, kk > 0);
+                    tc::commit(bars + C::B_S + x);
+                    s_done = i;
                 }
-                if (went) {
-                    while (used(freed)) {
-                        tc::commit(bars + C::B_FREE + freed % C::NS);
-                        ++freed;
-                    }
-                    idle = 0;
-                } else if ((++idle & 1023) == 0) {
-                    const uint64_t now = ptx::globaltimer();
-                    if (idle == 1024) since = now;
-                    else if (now - since > WAIT_NS) fail = true;
+                if (i > 0 && i <= nu) {
+                    const int j = i - 1;
+                    if (!mbar_wait(bars + C::B_P + 2 * x + (j & 1), (j >> 1) & 1, WAIT_NS)) { fail = true; break; }
+                    tc::fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < UK / 16; ++kk)
+                        tc::mma_ts(t_o, t_s + UK + (j & 1) * 32 + kk * 8, v_desc + pair + kk * 128, IO, (j > 0 || kk > 0));
+                    tc::commit(bars + C::B_PV + 2 * x + (j & 1));
+                    pv_done = j;
                 }
+                give_back(i);
             }
-            int sums = 0;  // transposed tiles issued
             if (n2 > 0 && !fail) {
                 constexpr uint32_t IT = tc::idesc_bf16(QT, false);
                 const uint64_t t_desc = tc::sw128_desc(ring_u, 16, 1024);
-                // the places of S and P are free once the last products are done
-#pragma unroll
-                for (int x = 0; x < NT; ++x)
-                    if (pj[x] > 0 && !mbar_wait(bars + C::B_PV + 2 * x + ((pj[x] - 1) & 1), ((pj[x] - 1) >> 1) & 1, WAIT_NS))
-                        fail = true;
+                // the places of S and P are free once the last product is done
+                if (pv_done >= 0 && !mbar_wait(bars + C::B_PV + 2 * x + (pv_done & 1), (pv_done >> 1) & 1, WAIT_NS)) fail = true;
                 for (int kb = 0; kb < n2 && !fail; ++kb) {
                     const int i = nn + 1 + kb;
-                    if (!mbar_wait(bars + C::B_FULL + i % C::NS, (i / C::NS) & 1, WAIT_NS)) { fail = true; break; }
+                    if (!full(i) || (kb > 0 && !mbar_wait(bars + C::B_TF + x, (kb - 1) & 1, WAIT_NS))) { fail = true; break; }
+                    tc::fence_after();
+                    const uint32_t pair = (i % C::NS) * (2 * C::KV_BYTES / 16);
 #pragma unroll
-                    for (int x = 0; x < NT; ++x) {
-                        if (kb > 0 && !mbar_wait(bars + C::B_TF + x, (kb - 1) & 1, WAIT_NS)) { fail = true; continue; }
-                        tc::fence_after();
-                        const uint64_t kd = t_desc + (i % C::NS) * (2 * C::KV_BYTES / 16), qd = q_desc + x * (C::Q_BYTES / 16);
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            tc::mma_ss(tm + x * 128, kd + (kk / 4) * (QT * 8) + (kk % 4) * 2, qd + (kk / 4) * (QT * 8) + (kk % 4) * 2,
-                                       IT, kk > 0);
-                        tc::commit(bars + C::B_T + x);
-                    }
-                    tc::commit(bars + C::B_FREE + i % C::NS);
-                    ++freed;
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        tc::mma_ss(t_s, t_desc + pair + (kk / 4) * (QT * 8) + (kk % 4) * 2, q_desc + (kk / 4) * (QT * 8) + (kk % 4) * 2,
+                                   IT, kk > 0);
+                    tc::commit(bars + C::B_T + x);
+                    give_back(i);
                     ++sums;
                 }
             }
             // The tensor cores finish what was issued before TMEM is freed, and
             // the last commits' arrivals land before the shared memory goes.
-#pragma unroll
-            for (int x = 0; x < NT; ++x) {
-                if (sj[x] > pj[x]) mbar_wait(bars + C::B_S + x, (sj[x] - 1) & 1, WAIT_NS);
-                if (pj[x] > 0) mbar_wait(bars + C::B_PV + 2 * x + ((pj[x] - 1) & 1), ((pj[x] - 1) >> 1) & 1, WAIT_NS);
-            }
-            // (freed pairs and key blocks are numbered through)
+            if (s_done > pv_done) mbar_wait(bars + C::B_S + x, s_done & 1, WAIT_NS);
+            if (pv_done >= 0) mbar_wait(bars + C::B_PV + 2 * x + (pv_done & 1), (pv_done >> 1) & 1, WAIT_NS);
+            if (sums > 0) mbar_wait(bars + C::B_T + x, (sums - 1) & 1, WAIT_NS);
             if (freed > 0) mbar_wait(bars + C::B_FREE + (freed - 1) % C::NS, ((freed - 1) / C::NS) & 1, WAIT_NS);
-            if (sums > 0)
-#pragma unroll
-                for (int x = 0; x < NT; ++x) mbar_wait(bars + C::B_T + x, (sums - 1) & 1, WAIT_NS);
         }
         __syncwarp();
     } else {
@@ -763,25 +720,28 @@ __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
             tc::fence_after();
             const float* nl = nl_s + j % C::NL * C::QN;
             const int from = key - shift - t0;  // columns before it do not see the key
-            const bool whole = t0 >= last;
+            auto sum = [&](auto all) {
 #pragma unroll
-            for (int c0 = 0; c0 < C::QN; c0 += 32) {
-                uint32_t o[32];
-                tc::ld32(t_lane + slot * C::QN + c0, o);
-                tc::ld_wait();
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int c0 = 0; c0 < C::QN; c0 += 32) {
+                    uint32_t o[32];
+                    tc::ld32(t_lane + slot * C::QN + c0, o);
+                    tc::ld_wait();
+                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int u = 0; u < 32; u += 4) {
-                    const float4 e = *reinterpret_cast<const float4*>(nl + c0 + u);
-                    const float ee[4] = {e.x, e.y, e.z, e.w};
+                    for (int u = 0; u < 32; u += 4) {
+                        const float4 e = *reinterpret_cast<const float4*>(nl + c0 + u);
+                        const float ee[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        const float p = tc::ex2(fmaf(__uint_as_float(o[u + v]), c, ee[v]));
-                        acc[v] += whole || c0 + u + v >= from ? p : 0.f;
+                        for (int v = 0; v < 4; ++v) {
+                            const float p = tc::ex2(fmaf(__uint_as_float(o[u + v]), c, ee[v]));
+                            acc[v] += decltype(all)::value || c0 + u + v >= from ? p : 0.f;
+                        }
                     }
+                    total += (acc[0] + acc[1]) + (acc[2] + acc[3]);
                 }
-                total += (acc[0] + acc[1]) + (acc[2] + acc[3]);
-            }
+            };
+            if (t0 >= last) sum(std::true_type());
+            else sum(std::false_type());
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::arrive(bars + C::B_SF + slot);
