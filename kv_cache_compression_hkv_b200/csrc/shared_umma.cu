@@ -58,13 +58,14 @@ template <int D, int NT> struct Shape {
 
 }  // namespace
 
-// MODE 0: every key of a row tile of one (sequence, KV head): prefix, then
-//         own, cut in `splits` pieces of the tile list; with one piece the
-//         results are final, else partial (slot = piece).  With a.fused_sums
-//         (one piece, and all rows of the (sequence, KV head) in this block)
-//         the block also adds the own keys' accumulated weights: S once more,
-//         transposed (128 keys on the M side, the rows as N), into the places
-//         of S and P, so that a thread sums 2^(x - lse) of its key.
+// MODE 0: every key of a row tile of one (sequence, KV head), prefix, then own;
+//         final results.  With a.fused_sums (all rows of the (sequence, KV
+//         head) are in this block) the block also adds the own keys'
+//         accumulated weights: S once more, transposed (128 keys on the M side,
+//         the rows as N), into the places of S and P, so that a thread sums
+//         2^(x - lse) of its key.
+// MODE 2: the same keys cut in `splits` pieces of the tile list; partial
+//         results (slot = piece).
 // MODE 1: rows of all sequences of a prefix over the prefix's keys, cut in
 //         a.np ranges; partial results (slot = range).
 template <int D, int NT, int MODE>
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
         if (warp >= 4 * NT) return;
         live = tid < rows;
         if (live) {
-            if constexpr (MODE == 0) {
+            if constexpr (MODE != 1) {
                 sq = s;
                 ri = first + tid;
             } else {
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    if constexpr (MODE == 0) {
+    if constexpr (MODE != 1) {
         // longest row tiles (the last queries) first
         const int b = blockIdx.x, per = a.S * a.Hk * splits;
         const int tile = row_tiles - 1 - b / per;
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
         const int per_piece = (all + splits - 1) / splits;
         t0 = min(all, piece * per_piece);
         t1 = min(all, t0 + per_piece);
-        if (splits > 1 && t0 >= t1) {  // the joining kernel knows
+        if (MODE == 2 && t0 >= t1) {  // the joining kernel knows
             asm volatile("cp.async.wait_group 0;" ::: "memory");
             return;
         }
@@ -179,18 +180,18 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
         const int last = min(rows, (x + 1) * QT) - 1;
         nx[x] = 0;
         if (last >= x * QT) {
-            const int vis = MODE == 0 ? p_tiles + (own_limit(a, n_own, first + last) + UK - 1) / UK : t1;
+            const int vis = MODE != 1 ? p_tiles + (own_limit(a, n_own, first + last) + UK - 1) / UK : t1;
             nx[x] = max(0, min(vis, t1) - t0);
         }
         n = max(n, nx[x]);
     }
 
-    if (warp == 0) tc::alloc(tmem_slot, C::TMEM);
     if (tid == 0) {
         for (int i = 0; i < C::B_COUNT; ++i)
             mbar_init(bars + i, i == C::B_Q ? 4 * NT : i >= C::B_FREE && i < C::B_S ? NT : ((i >= C::B_SF && i < C::B_PV) || i >= C::B_TF) ? 4 : 1);
         ptx::fence_mbar_init();
     }
+    if (warp == 0) tc::alloc(tmem_slot, C::TMEM);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
         const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t t_s = t_lane + x * 128, t_o = t_lane + C::O_COL + x * D;
         // own keys this row sees; rows past the last one compute on zeros
-        const int lim = MODE == 0 ? (live ? own_limit(a, n_own, ri) : 0x7fffffff) : 0;
+        const int lim = MODE != 1 ? (live ? own_limit(a, n_own, ri) : 0x7fffffff) : 0;
         const int lim_warp = __shfl_sync(FULL_MASK, lim, 0);  // the least of the warp's
         const int nt = NT == 2 ? (x == 0 ? nx[0] : nx[NT - 1]) : nx[0];
         float m = -INFINITY, l = 0.f;  // reference maximum (times c) and sum
@@ -500,21 +501,20 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
             tc::fence_after();
             const int64_t row = live ? row_index(a, sq, h, t) : 0;
             const bool some = nt > 0 && !(m == -INFINITY && l == 0.f);
-            const bool final = MODE == 0 && splits == 1;
+            constexpr bool final = MODE == 0;
             const float f = !final ? 1.f : some ? 1.f / l : 0.f;
             // The rows go out through Q's place (every product that read it is
             // done), 2 D bytes of a row at a time, so that a warp stores whole
             // rows and not 16 bytes of 32 of them.
             const int64_t dst = !live ? -1 : final ? sq * a.os[0] + h * a.os[1] + t * a.os[2] : (piece * R + row) * D;
             unsigned char* tile = q_s + x * C::Q_BYTES;
-            constexpr int FW = D / 2;  // fp32 values of a pass
+            constexpr int PASSES = final ? 1 : 2, FW = D / PASSES;  // values of a pass
 #pragma unroll
-            for (int pass = 0; pass < 2; ++pass) {
-                if ((final && pass == 1) || idle) break;
+            for (int pass = 0; pass < PASSES; ++pass) {
+                if (idle) break;
                 __syncwarp();
 #pragma unroll
-                for (int c0 = 0; c0 < D; c0 += 32) {
-                    if (!final && c0 / FW != pass) continue;
+                for (int c0 = pass * FW; c0 < (pass + 1) * FW; c0 += 32) {
                     uint32_t o[32];
                     if (nt > 0) {
                         tc::ld32(t_o + c0, o);
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = some ? __float_as_uint(__uint_as_float(o[e]) * f) : 0u;
                     const int r = (warp & 3) * 32 + lane;
-                    if (final) {
+                    if constexpr (final) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             uint32_t w[4];
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                     const int64_t o = __shfl_sync(FULL_MASK, dst, r);
                     const uint4 w = *reinterpret_cast<const uint4*>(tile + q_off((warp & 3) * 32 + r, c));
                     if (o >= 0) {
-                        if (final) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + o + c * 8) = w;
+                        if constexpr (final) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + o + c * 8) = w;
                         else *reinterpret_cast<uint4*>(a.part_o + o + pass * FW + c * 4) = w;
                     }
                 }
@@ -820,9 +820,18 @@ cudaError_t launch_attend_umma(const View& a, int d, cudaStream_t st) {
     const int rps = a.rep * a.T, nt = umma_row_tiles(rps), splits = a.no;
     const int tiles = (rps + QT * nt - 1) / (QT * nt);
     const int64_t blocks = (int64_t)tiles * a.S * a.Hk * splits;
-    if (d == 128)
-        return nt == 2 ? go<128, 2, 0>(a, m, blocks, tiles, splits, st) : go<128, 1, 0>(a, m, blocks, tiles, splits, st);
-    return nt == 2 ? go<64, 2, 0>(a, m, blocks, tiles, splits, st) : go<64, 1, 0>(a, m, blocks, tiles, splits, st);
+    auto run = [&](auto dim, auto mode) {
+        constexpr int D = decltype(dim)::value, MODE = decltype(mode)::value;
+        return nt == 2 ? go<D, 2, MODE>(a, m, blocks, tiles, splits, st) : go<D, 1, MODE>(a, m, blocks, tiles, splits, st);
+    };
+    using Final = std::integral_constant<int, 0>;
+    using Pieces = std::integral_constant<int, 2>;
+    if (d == 128) {
+        using Dim = std::integral_constant<int, 128>;
+        return splits == 1 ? run(Dim(), Final()) : run(Dim(), Pieces());
+    }
+    using Dim = std::integral_constant<int, 64>;
+    return splits == 1 ? run(Dim(), Final()) : run(Dim(), Pieces());
 }
 
 cudaError_t launch_prefix_umma(const View& a, int d, cudaStream_t st) {
@@ -850,12 +859,16 @@ cudaError_t prepare_shared_umma() {
     auto set = [&](auto kernel, int smem) {
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     };
-    set(attend_umma_kernel<128, 2, 0>, Shape<128, 2>::SMEM);
-    set(attend_umma_kernel<128, 1, 0>, Shape<128, 1>::SMEM);
-    set(attend_umma_kernel<128, 1, 1>, Shape<128, 1>::SMEM);
-    set(attend_umma_kernel<64, 2, 0>, Shape<64, 2>::SMEM);
-    set(attend_umma_kernel<64, 1, 0>, Shape<64, 1>::SMEM);
-    set(attend_umma_kernel<64, 1, 1>, Shape<64, 1>::SMEM);
+    auto all = [&](auto dim) {
+        constexpr int D = decltype(dim)::value;
+        set(attend_umma_kernel<D, 1, 0>, Shape<D, 1>::SMEM);
+        set(attend_umma_kernel<D, 2, 0>, Shape<D, 2>::SMEM);
+        set(attend_umma_kernel<D, 1, 1>, Shape<D, 1>::SMEM);
+        set(attend_umma_kernel<D, 1, 2>, Shape<D, 1>::SMEM);
+        set(attend_umma_kernel<D, 2, 2>, Shape<D, 2>::SMEM);
+    };
+    all(std::integral_constant<int, 64>());
+    all(std::integral_constant<int, 128>());
     set(column_sums_umma_kernel<128>, SumShape<128>::SMEM);
     set(column_sums_umma_kernel<64>, SumShape<64>::SMEM);
     return e;
