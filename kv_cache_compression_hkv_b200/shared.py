@@ -163,7 +163,10 @@ class SharedPrefixCache:
                     _check(fn(*a, torch._C._cuda_getCurrentRawStream(index)), what)
             return
         if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device) if int(stream) else \
+                torch.cuda.default_stream(self.device)
+        if stream.device != self.device:
+            raise ValueError(f"stream: of {stream.device}, the cache is on {self.device}")
         with torch.cuda.stream(stream):
             a, _scratch = args()
             _check(fn(*a, stream.cuda_stream), what)

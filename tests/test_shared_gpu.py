@@ -77,7 +77,7 @@ def check(c, q, **kw):
     return out, lse
 
 
-HEADS = [(4, 4), (4, 2), (4, 1), (7, 1), (8, 1), (16, 1), (20, 20)]
+HEADS = [(4, 4), (4, 2), (4, 1), (7, 1), (8, 1), (16, 1), (17, 1), (40, 1), (20, 20)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -95,6 +95,29 @@ def test_one_token(dtype, d, H, Hk):
                                       (129, 2, 2, 128)])
 def test_many_tokens(dtype, T, H, Hk, d):
     c, q = make(dtype, S=3, H=H, Hk=Hk, d=d, T=T, cap=T + 90, P=37, seed=T)
+    check(c, q)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,H,Hk,d,P", [(1, 4, 4, 128, 2100), (1, 8, 2, 128, 4100), (4, 4, 2, 64, 4100),
+                                        (2, 14, 2, 128, 3001)])
+def test_long_prefixes_read_once(dtype, T, H, Hk, d, P):
+    """Prefixes too long to be read again by every sequence: their rows of all
+    sequences together, sequences in any order, some without a prefix."""
+    S = 17
+    of = [1, 0, 2, 1, 1, -1, 0, 2, 1, 0, 1, 5, 1, 0, 0, 1, 2]
+    lens = torch.arange(S * Hk).view(S, Hk) * 7 % 60
+    c, q = make(dtype, S=S, H=H, Hk=Hk, d=d, T=T, cap=61, G=3, P=P, plens=[P, P - 77, 0], of=of, lens=lens, seed=T)
+    check(c, q)
+    check(c, q, accumulate=False)
+
+
+@pytest.mark.parametrize("dtype,S,H,Hk,T", [("bf16", 10, 16, 16, 20), ("bf16", 37, 4, 2, 130), ("bf16", 1, 2, 1, 300),
+                                            ("f32", 10, 16, 16, 20), ("f32", 1, 3, 1, 150)])
+def test_many_rows_one_pass(dtype, S, H, Hk, T):
+    """Enough row tiles for whole key lists, and more rows of a head than one
+    block holds: outputs final, weights by the blocks or in a pass of their own."""
+    c, q = make(dtype, S=S, H=H, Hk=Hk, d=64, T=T, cap=T + 33, G=2, P=30, seed=S)
     check(c, q)
 
 
@@ -279,6 +302,16 @@ def test_evict(dtype, cap, budget, recent, slack):
         evict_both(c, b, recent, slack)
 
 
+def test_evict_very_long():
+    """A head whose weights and positions do not fit shared memory."""
+    g = torch.Generator().manual_seed(1)
+    cap = 30001
+    c, _ = make("bf16", S=1, H=2, Hk=2, d=64, cap=cap, G=0, lens=cap)
+    c.pos.copy_(torch.argsort(torch.rand(1, 2, cap, generator=g), -1))
+    c.weight[0, 1] = c.weight[0, 1].round(decimals=3)  # ties
+    evict_both(c, [[20000, 29000]], 500, 1)
+
+
 @pytest.mark.parametrize("cap", [48, 700, 3000])
 def test_evict_ties_and_odd_values(cap):
     """Equal weights, signed zeros, infinities, NaN, negative weights;
@@ -378,6 +411,23 @@ def test_two_streams_at_once():
         outs.append(c.attend(q, accumulate=False, stream=streams[i % 3] if i % 2 else streams[i % 3].cuda_stream)[0])
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
+
+
+def test_default_stream_by_handle_and_from_another_thread():
+    import threading
+    c, q = make("bf16", S=4, H=8, Hk=2, d=128, cap=200, P=90, lens=200)
+    want, _ = c.attend(q, accumulate=False)
+    got = [None] * 8
+
+    def work(i):
+        for _ in range(20):
+            got[i] = c.attend(q, accumulate=False, stream=0 if i % 2 else None)[0]
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in got)
 
 
 def test_python_refusals():
