@@ -51,7 +51,8 @@ struct View {
     float* part_o;    // [np + no][R][d]
     float* logit;     // [S][Hk][rep T][lcap] exp2-domain logits of the own keys (few rows, accumulate)
     int32_t lcap;     // capacity rounded up to 4
-    int32_t fused_sums;  // the attention blocks add the accumulated weights themselves
+    int32_t sum_tiles;  // row tiles of a (sequence, KV head) whose blocks sum the weights themselves (0: they do not)
+    float* part_sum;    // [sum_tiles][S][Hk][cap] their sums, where there are several
     float* row_lse;   // [R] log2 of the row sums (tile path, accumulate)
 };
 
@@ -191,8 +192,13 @@ inline int64_t max_prefix_tiles(int S, int G, int rows_per_seq, int rt) {
     return full + (G < S ? G : S);
 }
 
-// Row tiles of 128 that a tensor-core block takes: two as soon as one (sequence, KV head) has them.
-inline int umma_row_tiles(int64_t rows_per_seq) { return rows_per_seq > 128 ? 2 : 1; }
+// Row tiles of 128 that a tensor-core block takes.  With one, two blocks share
+// an SM and hide each other's beginnings and ends, and the block can sum its
+// keys' weights; with two, the row tiles share the copies of K and V.  (256 rows
+// over 384 keys, 512 heads: 58 us with one, 65 with two; 16004 rows over
+// 5001 keys: 398 with two.)
+constexpr int ONE_TILE_ROWS = 512;
+inline int umma_row_tiles(int64_t rows_per_seq) { return rows_per_seq > ONE_TILE_ROWS ? 2 : 1; }
 
 // Launches a kernel as a programmatic dependent: its blocks may be set up while
 // the kernel in front of it in the stream drains, so it executes
@@ -224,6 +230,7 @@ bool make_map(CUtensorMap* m, const void* ptr, int d, int n0, int n1, int n2, co
 cudaError_t prepare_shared_umma();
 cudaError_t launch_attend_umma(const View& a, int d, cudaStream_t st);
 cudaError_t launch_column_sums_umma(const View& a, int d, cudaStream_t st);
+cudaError_t launch_add_sums(const View& a, cudaStream_t st);
 cudaError_t launch_prefix_umma(const View& a, int d, cudaStream_t st);
 cudaError_t launch_append(const View& a, int dtype, int d, const void* k_t, const int64_t* kts, const void* v_t,
                           const int64_t* vts, const float* w_t, cudaStream_t st);

@@ -146,9 +146,10 @@ Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char
         a.part_ml = (float2*)take(ns * R * sizeof(float2));
         a.part_o = (float*)take(ns * R * d * sizeof(float));
     }
-    a.fused_sums = accumulate && p.umma_rows && a.no == 1 && rps <= 256;
+    a.sum_tiles = accumulate && p.umma_rows && a.no == 1 && rps <= hkv::shared::ONE_TILE_ROWS ? (int)((rps + 127) / 128) : 0;
     if (accumulate && few) a.logit = (float*)take((size_t)heads * rps * a.lcap * 4);
-    if (accumulate && !few && !a.fused_sums) a.row_lse = (float*)take((size_t)R * 4);
+    if (a.sum_tiles > 1) a.part_sum = (float*)take((size_t)a.sum_tiles * heads * a.cap * 4);
+    if (accumulate && !few && !a.sum_tiles) a.row_lse = (float*)take((size_t)R * 4);
     p.bytes = o;
     return p;
 }
@@ -234,6 +235,7 @@ hkv_status hkv_shared_attend(const hkv_shared_cache* c, const void* q, const int
     if (e == cudaSuccess && p.stream) e = hkv::shared::launch_stream(a, d, p.warps_per_head, p.umma_prefix, st);
     if (e == cudaSuccess && c->dtype == HKV_DTYPE_F32) e = hkv::shared::launch_attend_f32(a, d, st);
     if (e == cudaSuccess && a.part_ml) e = hkv::shared::launch_combine(a, c->dtype, d, st);
+    if (e == cudaSuccess && a.part_sum) e = hkv::shared::launch_add_sums(a, st);
     if (e == cudaSuccess && a.row_lse)
         e = p.umma_rows ? hkv::shared::launch_column_sums_umma(a, d, st)
                         : hkv::shared::launch_column_sums_f32(a, d, st);

@@ -52,18 +52,20 @@ template <int D, int NT> struct Shape {
     static constexpr int Q_BYTES = QT * D * 2, KV_BYTES = UK * D * 2;
     enum { B_Q, B_FULL, B_FREE = B_FULL + NS, B_S = B_FREE + NS, B_SF = B_S + NT, B_P = B_SF + NT, B_PV = B_P + 2 * NT,
            B_T = B_PV + 2 * NT, B_TF = B_T + NT, B_COUNT = B_TF + NT };
-    static constexpr int TAIL = B_COUNT * 8 + 16 + 16 + (QT + 4) * 4 + ROWS * 4 + 2 * QT * 4;
+    static constexpr int TAIL = B_COUNT * 8 + 16 + 16 + (QT + 4) * 4 + ROWS * 4;
     static constexpr int SMEM = 1024 + NT * Q_BYTES + NS * 2 * KV_BYTES + TAIL;
 };
 
 }  // namespace
 
 // MODE 0: every key of a row tile of one (sequence, KV head), prefix, then own;
-//         final results.  With a.fused_sums (all rows of the (sequence, KV
-//         head) are in this block) the block also adds the own keys'
-//         accumulated weights: S once more, transposed (128 keys on the M side,
-//         the rows as N), into the places of S and P, so that a thread sums
-//         2^(x - lse) of its key.
+//         final results.  With a.sum_tiles (and one row tile a block) the block
+//         also sums the weights its own keys get from its rows: S once more,
+//         transposed (128 keys on the M side, the rows as N), into the places of
+//         S and P, so that a thread sums 2^(x - lse) of its key.  A block with
+//         all rows of its (sequence, KV head) adds them to the accumulated
+//         weights; several leave theirs for add_sums_kernel, which adds them in
+//         their order.
 // MODE 2: the same keys cut in `splits` pieces of the tile list; partial
 //         results (slot = piece).
 // MODE 1: rows of all sequences of a prefix over the prefix's keys, cut in
@@ -79,8 +81,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
     unsigned char* q_s = base;
     unsigned char* ring = q_s + NT * C::Q_BYTES;  // pairs: V, then K
     float* nl_s = reinterpret_cast<float*>(ring + C::NS * 2 * C::KV_BYTES);  // [ROWS] -log2 of the rows' sums
-    float* half_s = nl_s + C::ROWS;                                          // [2][QT] column sums of the second row tile
-    uint64_t* bars = reinterpret_cast<uint64_t*>(half_s + 2 * QT);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(nl_s + C::ROWS);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::B_COUNT);
     int* res = reinterpret_cast<int*>(tmem_slot + 4);
     int* list = res + 4;
@@ -198,7 +199,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
     const uint32_t tmem = *tmem_slot;
     bool fail = false;
 
-    const int n2 = MODE == 0 && a.fused_sums ? (n_own + QT - 1) / QT : 0;  // blocks of 128 own keys for the sums
+    // own keys that some row sees, and their blocks of 128, for the sums
+    const int seen = MODE == 0 && NT == 1 && a.sum_tiles ? min(n_own, own_limit(a, n_own, first + rows - 1)) : 0;
+    const int n2 = (seen + QT - 1) / QT;
 
     // list tile t0 + j: where its keys start, and how many of 64 are keys
     auto tile_at = [&](int j, bool& pre, int& k0, int& valid) {
@@ -449,53 +452,48 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
             const int jl = nt - 1;
             if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_PV + 2 * x + (jl & 1), (jl >> 1) & 1, WAIT_NS))) fail = true;
         }
-        if (MODE == 0 && n2 > 0) {
-            // Every row thread comes here and to every barrier below, failed or not.
+        if (MODE == 0 && NT == 1 && n2 > 0) {
+            // every row thread comes here, failed or not
             nl_s[tid] = live && !(m == -INFINITY && l == 0.f) ? -(m + log2f(l)) : -INFINITY;
             asm volatile("bar.sync 1, %0;" ::"n"(C::ROWS) : "memory");
             const int shift = n_own - a.T;  // key j is seen by the queries t >= j - shift
-            const float* nl = nl_s + x * QT;
-            float* wrow = a.weight + (int64_t)(s * a.Hk + hk) * a.cap;
-            for (int kb = 0; kb < n2; ++kb) {
-                const int key = kb * QT + (tid & 127);
-                const float old = x == 0 && key < n_own ? wrow[key] : 0.f;
+            const int sh = s * a.Hk + hk;
+            float* wrow = a.weight + (int64_t)sh * a.cap;
+            float* prow = a.part_sum + ((int64_t)(first / QT) * a.S * a.Hk + sh) * a.cap;
+            for (int kb = 0; kb < n2 && !fail; ++kb) {
+                const int key = kb * QT + tid;
+                const float old = a.sum_tiles == 1 && key < seen ? wrow[key] : 0.f;
+                if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_T, kb & 1, WAIT_NS))) { fail = true; break; }
+                tc::fence_after();
+                const int from = (key - shift) * a.rep - first;  // rows of the block before it do not see the key
+                const bool whole = __shfl_sync(FULL_MASK, from, 31) <= 0;
                 float total = 0.f;
-                if (!fail && __any_sync(FULL_MASK, !mbar_wait(bars + C::B_T + x, kb & 1, WAIT_NS))) fail = true;
-                if (!fail) {
-                    tc::fence_after();
-                    const int from = (key - shift) * a.rep - x * QT;  // rows before it do not see the key
-                    const bool whole = __shfl_sync(FULL_MASK, from, 31) <= 0;
 #pragma unroll
-                    for (int c0 = 0; c0 < QT; c0 += 32) {
-                        uint32_t o[32];
-                        tc::ld32(t_s + c0, o);
-                        tc::ld_wait();
-                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int c0 = 0; c0 < QT; c0 += 32) {
+                    uint32_t o[32];
+                    tc::ld32(t_s + c0, o);
+                    tc::ld_wait();
+                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int u = 0; u < 32; u += 4) {
-                            const float4 e = *reinterpret_cast<const float4*>(nl + c0 + u);
-                            const float ee[4] = {e.x, e.y, e.z, e.w};
+                    for (int u = 0; u < 32; u += 4) {
+                        const float4 e = *reinterpret_cast<const float4*>(nl_s + c0 + u);
+                        const float ee[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
-                            for (int v = 0; v < 4; ++v) {
-                                const float p = tc::ex2(fmaf(__uint_as_float(o[u + v]), c, ee[v]));
-                                acc[v] += whole || c0 + u + v >= from ? p : 0.f;
-                            }
+                        for (int v = 0; v < 4; ++v) {
+                            const float p = tc::ex2(fmaf(__uint_as_float(o[u + v]), c, ee[v]));
+                            acc[v] += whole || c0 + u + v >= from ? p : 0.f;
                         }
-                        total += (acc[0] + acc[1]) + (acc[2] + acc[3]);
                     }
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) tc::arrive(bars + C::B_TF + x);
+                    total += (acc[0] + acc[1]) + (acc[2] + acc[3]);
                 }
-                if constexpr (NT == 2) {
-                    if (x == 1) half_s[(kb & 1) * QT + (tid & 127)] = total;
-                    asm volatile("bar.sync 1, %0;" ::"n"(C::ROWS) : "memory");
-                    if (x == 0) total += half_s[(kb & 1) * QT + tid];
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::arrive(bars + C::B_TF);
+                if (key < seen) {
+                    if (a.sum_tiles == 1) wrow[key] = old + total;
+                    else prow[key] = total;
                 }
-                if (x == 0 && key < n_own && !fail) wrow[key] = old + total;
             }
-            // (Q's place is written next: by now every product that read it is done)
-            if constexpr (NT == 2) asm volatile("bar.sync 1, %0;" ::"n"(C::ROWS) : "memory");
         }
         if (!fail) {
             tc::fence_after();
@@ -570,6 +568,20 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
     }
     tc::fence_after();
     if (warp == 0) tc::dealloc(tmem, C::TMEM);
+}
+
+// weight += the sums that the row tiles' blocks left, in their order: those of
+// the tiles whose last row sees the slot.  One thread a slot.
+__global__ void __launch_bounds__(256) add_sums_kernel(const __grid_constant__ View a) {
+    const int chunks = (a.cap + 255) / 256, sh = blockIdx.x / chunks, key = blockIdx.x % chunks * 256 + threadIdx.x;
+    const int n = own_len(a, sh / a.Hk, sh % a.Hk), rps = a.rep * a.T;
+    ptx::grid_dep_wait();
+    if (key >= n) return;
+    float* w = a.weight + (int64_t)sh * a.cap + key;
+    float sum = 0.f;
+    for (int t = 0; t < a.sum_tiles; ++t)
+        if (key < own_limit(a, n, min(rps, (t + 1) * QT) - 1)) sum += a.part_sum[((int64_t)t * a.S * a.Hk + sh) * a.cap + key];
+    *w += sum;
 }
 
 // ---------------------------------------------------------------------------
@@ -832,6 +844,10 @@ cudaError_t launch_attend_umma(const View& a, int d, cudaStream_t st) {
     }
     using Dim = std::integral_constant<int, 64>;
     return splits == 1 ? run(Dim(), Final()) : run(Dim(), Pieces());
+}
+
+cudaError_t launch_add_sums(const View& a, cudaStream_t st) {
+    return launch(add_sums_kernel, (int64_t)a.S * a.Hk * ((a.cap + 255) / 256), 256, 0, st, a);
 }
 
 cudaError_t launch_prefix_umma(const View& a, int d, cudaStream_t st) {
