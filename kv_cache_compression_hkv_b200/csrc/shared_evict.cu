@@ -29,7 +29,7 @@ constexpr int BINS = 2048;
 constexpr int CAND = 64;        // candidates ranked against each other (256 cost short heads four times the rest)
 constexpr int LIST = 512;       // moves whose slots stay in shared memory
 constexpr int SHORT_CAP = 2048; // capacities up to this: blocks of 128 threads that also move the rows
-constexpr int HELD_CAP = 24576; // capacities up to this: weights and positions in shared memory (192 KB)
+constexpr int HELD_CAP = 24576; // capacities up to this: weights and positions in shared memory (195 KB)
 
 // Bits that order as (recent, weight): recent tokens highest, then NaN, then
 // the numbers (-0 as +0).
@@ -118,8 +118,11 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
         sm.newest = INT32_MIN;
         sm.n_cand = 0;
     }
+    // what is held: positions, and weights until the first look at the keys
+    // turns them into their class bits; then a bit a slot: evicted
     int32_t* hpos = reinterpret_cast<int32_t*>(held_raw);
-    float* hw = reinterpret_cast<float*>(held_raw) + a.cap;
+    uint32_t* hclass = reinterpret_cast<uint32_t*>(held_raw) + a.cap;
+    uint32_t* hgone = hclass + a.cap;
     int nw = INT32_MIN;
     for (int i0 = tid; i0 < n; i0 += 4 * THREADS) {
         int32_t p[4];
@@ -136,7 +139,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
             nw = max(nw, p[u]);
             if (HELD && i < n) {
                 hpos[i] = p[u];
-                hw[i] = w[u];
+                hclass[i] = __float_as_uint(w[u]);
             }
         }
     }
@@ -145,9 +148,14 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
     if (lane == 0) atomicMax(&sm.newest, nw);
     __syncthreads();
     const int64_t newest = sm.newest;
+    if (HELD) {
+        for (int i = tid; i < n; i += THREADS) hclass[i] = class_bits(__uint_as_float(hclass[i]), newest - hpos[i] < recent);
+        __syncthreads();
+    }
     auto key = [&](int i) {
         const int p = HELD ? hpos[i] : pos[i];
-        return ((uint64_t)class_bits(HELD ? hw[i] : weight[i], newest - p < recent) << 32) | ((uint32_t)p ^ 0x80000000u);
+        const uint32_t c = HELD ? hclass[i] : class_bits(weight[i], newest - p < recent);
+        return ((uint64_t)c << 32) | ((uint32_t)p ^ 0x80000000u);
     };
 
     // the threshold: (thr_key, thr_slot), the last to go
@@ -270,10 +278,15 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
     int nh = 0, nm = 0;
     for (int i0 = lo; i0 < hi; i0 += 32) {
         const int i = i0 + lane;
-        const bool g = i < hi && gone(i);
-        nh += __popc(__ballot_sync(FULL_MASK, g && i < B));
-        nm += __popc(__ballot_sync(FULL_MASK, i < hi && !g && i >= B));
+        const unsigned g = __ballot_sync(FULL_MASK, i < hi && gone(i));
+        // (bit masks of the 32 slots from i0: those below B, those below the end)
+        const unsigned below = B >= i0 + 32 ? FULL_MASK : B <= i0 ? 0u : (1u << (B - i0)) - 1;
+        const unsigned in = hi >= i0 + 32 ? FULL_MASK : (1u << (hi - i0)) - 1;
+        nh += __popc(g & below);
+        nm += __popc(in & ~g & ~below);
+        if (HELD && lane == 0) hgone[i0 >> 5] = g;
     }
+    __syncwarp();
     if (lane == 0) {
         sm.warp_a[warp] = nh;
         sm.warp_b[warp] = nm;
@@ -292,11 +305,12 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
     int* ml = move && moves <= LIST ? sm.list + LIST : hl + B;
     for (int i0 = lo; i0 < hi; i0 += 32) {
         const int i = i0 + lane;
-        const bool g = i < hi && gone(i), hole = g && i < B, mover = i < hi && !g && i >= B;
-        const unsigned b = __ballot_sync(FULL_MASK, hole), m = __ballot_sync(FULL_MASK, mover);
-        const unsigned lt = (1u << lane) - 1;
-        if (hole) hl[bh + __popc(b & lt)] = i;
-        if (mover) ml[bm + __popc(m & lt)] = i;
+        const unsigned g = HELD ? hgone[i0 >> 5] : __ballot_sync(FULL_MASK, i < hi && gone(i));
+        const unsigned below = B >= i0 + 32 ? FULL_MASK : B <= i0 ? 0u : (1u << (B - i0)) - 1;
+        const unsigned in = hi >= i0 + 32 ? FULL_MASK : (1u << (hi - i0)) - 1;
+        const unsigned b = g & below, m = in & ~g & ~below, lt = (1u << lane) - 1;
+        if (b >> lane & 1) hl[bh + __popc(b & lt)] = i;
+        if (m >> lane & 1) ml[bm + __popc(m & lt)] = i;
         bh += __popc(b);
         bm += __popc(m);
     }
@@ -319,8 +333,11 @@ __global__ void __launch_bounds__(256) move_kernel(const __grid_constant__ View 
     move_rows(a, head, hl, hl + c.y, c.x, blockIdx.x % parts, parts, row_bytes, es);
 }
 
+// positions, classes and the evicted slots' bits of a head
+static size_t held_bytes(int cap) { return (size_t)cap * 8 + (size_t)(cap + 31) / 32 * 4; }
+
 cudaError_t prepare_shared_evict() {
-    return cudaFuncSetAttribute(select_kernel<1024, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, HELD_CAP * 8);
+    return cudaFuncSetAttribute(select_kernel<1024, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)held_bytes(HELD_CAP));
 }
 
 size_t evict_bytes(int heads, int cap) {
@@ -332,7 +349,7 @@ cudaError_t launch_evict(const View& a, int dtype, int d, const int32_t* budget,
     const int es = dtype == HKV_DTYPE_F32 ? 4 : 2, heads = a.S * a.Hk, row = d * es;
     int2* counts = reinterpret_cast<int2*>(scratch);
     int32_t* lists = reinterpret_cast<int32_t*>(scratch + ((size_t)heads * 8 + 255) / 256 * 256);
-    const size_t held = (size_t)a.cap * 8;
+    const size_t held = held_bytes(a.cap);
     if (a.cap <= SHORT_CAP)
         return launch(select_kernel<128, true>, heads, 128, held, st, a, budget, recent, slack, row, es, 1, lists, counts);
     const cudaError_t e =
