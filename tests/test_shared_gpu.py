@@ -360,15 +360,17 @@ def test_generation_run(dtype, T):
     assert (c.next_pos == 30 + T * steps).all() and (c.pos[0, 0, :budget] >= 0).all()
 
 
-def test_captured_step_replays():
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("S,T,P", [(4, 1, 70), (16, 1, 4200), (4, 20, 70)])
+def test_captured_step_replays(dtype, S, T, P):
     """append + attend + evict captured once and replayed equals eager steps;
     two graphs of one cache hold their own scratch."""
     g = torch.Generator().manual_seed(6)
-    make_one = lambda: make("bf16", S=4, H=8, Hk=2, d=128, cap=48, P=70, lens=32, seed=9)  # noqa: E731
-    c, q = make_one()
-    e, _ = make_one()
-    kt, vt = rows(g, "bf16", 4, 2, 1, 128), rows(g, "bf16", 4, 2, 1, 128)
-    b = torch.full((4, 2), 32, dtype=torch.int32, device=DEV)
+    make_one = lambda: make(dtype, S=S, H=8, Hk=4, d=128, cap=56, P=P, lens=32, seed=9)[0]  # noqa: E731
+    c, e = make_one(), make_one()
+    q = rows(g, dtype, S, 8, T, 128)
+    kt, vt = rows(g, dtype, S, 4, T, 128), rows(g, dtype, S, 4, T, 128)
+    b = torch.full((S, 4), 32, dtype=torch.int32, device=DEV)
 
     def step(x):
         x.append(kt, vt)
@@ -376,17 +378,17 @@ def test_captured_step_replays():
         x.evict(b, 8)
         return r
 
-    state = [t.clone() for t in (c.k, c.v, c.pos, c.weight, c.lens, c.next_pos)]
-    s = torch.cuda.Stream()
-    with torch.cuda.stream(s):
+    parts = lambda x: (x.k, x.v, x.pos, x.weight, x.lens, x.next_pos)  # noqa: E731
+    state = [t.clone() for t in parts(c)]
+    with torch.cuda.stream(torch.cuda.Stream()):
         step(c)
     torch.cuda.synchronize()
-    for t, x in zip((c.k, c.v, c.pos, c.weight, c.lens, c.next_pos), state):
+    for t, x in zip(parts(c), state):
         t.copy_(x)
     graph, other = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         out, lse = step(c)
-    q2 = rows(g, "bf16", 4, 8, 1, 128)
+    q2 = rows(g, dtype, S, 8, T, 128)
     with torch.cuda.graph(other):
         out2, _ = c.attend(q2, accumulate=False)
     for i in range(5):
@@ -396,21 +398,21 @@ def test_captured_step_replays():
         want, wl = step(e)
         want2, _ = e.attend(q2, accumulate=False)
         assert torch.equal(out, want) and torch.equal(lse, wl) and torch.equal(out2, want2), i
-    for a, x in zip((c.k, c.v, c.pos, c.weight, c.lens, c.next_pos), (e.k, e.v, e.pos, e.weight, e.lens, e.next_pos)):
+    for a, x in zip(parts(c), parts(e)):
         assert torch.equal(a.nan_to_num(-1.0), x.nan_to_num(-1.0))
 
 
-def test_two_streams_at_once():
+@pytest.mark.parametrize("S,T,P,cap", [(8, 1, 2000, 3000), (24, 1, 4000, 300), (3, 40, 500, 900)])
+def test_several_streams_at_once(S, T, P, cap):
     """Calls that only read the cache may overlap: each has its own scratch."""
-    c, q = make("bf16", S=8, H=8, Hk=2, d=128, cap=3000, P=2000, lens=3000)
-    want, _ = c.attend(q, accumulate=False)
+    c, q = make("bf16", S=S, H=8, Hk=2, d=128, T=T, cap=cap, P=P, lens=cap)
+    want, wl = c.attend(q, accumulate=False)
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(3)]
-    outs = []
-    for i in range(12):
-        outs.append(c.attend(q, accumulate=False, stream=streams[i % 3] if i % 2 else streams[i % 3].cuda_stream)[0])
+    outs = [c.attend(q, accumulate=False, stream=streams[i % 3] if i % 2 else streams[i % 3].cuda_stream)
+            for i in range(30)]
     torch.cuda.synchronize()
-    assert all(torch.equal(o, want) for o in outs)
+    assert all(torch.equal(o, want) and torch.equal(e, wl) for o, e in outs)
 
 
 def test_default_stream_by_handle_and_from_another_thread():
