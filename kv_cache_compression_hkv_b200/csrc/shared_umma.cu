@@ -430,16 +430,20 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
             }
             const float mb = m == -INFINITY ? 0.f : m;
             uint32_t w[32];
-            float ls[4] = {0.f, 0.f, 0.f, 0.f};
+            float2 ls[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) ls[u] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int u = 0; u < 32; ++u) {
-                const float p0 = tc::ex2(fmaf(__uint_as_float(sr[(2 * u) >> 5][(2 * u) & 31]), c, -mb));
-                const float p1 = tc::ex2(fmaf(__uint_as_float(sr[(2 * u + 1) >> 5][(2 * u + 1) & 31]), c, -mb));
-                ls[u & 3] += p0 + p1;
-                __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+                const float2 y = tc::fma2(make_float2(__uint_as_float(sr[u >> 4][2 * u & 31]), __uint_as_float(sr[u >> 4][(2 * u & 31) + 1])),
+                                          make_float2(c, c), make_float2(-mb, -mb));
+                const float2 p = make_float2(tc::ex2(y.x), tc::ex2(y.y));
+                ls[u & 3] = tc::add2(ls[u & 3], p);
+                __nv_bfloat162 h2 = __floats2bfloat162_rn(p.x, p.y);
                 w[u] = *reinterpret_cast<uint32_t*>(&h2);
             }
-            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+            ls[0] = tc::add2(tc::add2(ls[0], ls[1]), tc::add2(ls[2], ls[3]));
+            l += ls[0].x + ls[0].y;
             // (P's slot is free: the commit behind S of tile j covers the product
             // of tile j - 2)
             tc::st32(t_s + UK + (j & 1) * 32, w);
