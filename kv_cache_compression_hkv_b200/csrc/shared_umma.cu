@@ -58,6 +58,38 @@ template <int D, int NT> struct Shape {
 
 }  // namespace
 
+// sum over 128 columns from taddr (a thread's lane) of 2^(c S + nl), for the
+// columns from `from` on (all of them: ALL).
+template <bool ALL>
+__device__ __forceinline__ float column_weights(uint32_t taddr, const float* nl, float c, int from) {
+    float total = 0.f;
+#pragma unroll
+    for (int c0 = 0; c0 < QT; c0 += 32) {
+        uint32_t o[32];
+        tc::ld32(taddr + c0, o);
+        tc::ld_wait();
+        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int u = 0; u < 32; u += 4) {
+            const float4 e = *reinterpret_cast<const float4*>(nl + c0 + u);
+#pragma unroll
+            for (int v = 0; v < 4; v += 2) {
+                const float2 y = tc::fma2(make_float2(__uint_as_float(o[u + v]), __uint_as_float(o[u + v + 1])), make_float2(c, c),
+                                          v == 0 ? make_float2(e.x, e.y) : make_float2(e.z, e.w));
+                float2 p = make_float2(tc::ex2(y.x), tc::ex2(y.y));
+                if (!ALL) {
+                    p.x = c0 + u + v >= from ? p.x : 0.f;
+                    p.y = c0 + u + v + 1 >= from ? p.y : 0.f;
+                }
+                acc[v >> 1] = tc::add2(acc[v >> 1], p);
+            }
+        }
+        acc[0] = tc::add2(acc[0], acc[1]);
+        total += acc[0].x + acc[0].y;
+    }
+    return total;
+}
+
 // MODE 0: every key of a row tile of one (sequence, KV head), prefix, then own;
 //         final results.  With a.sum_tiles (and one row tile a block) the block
 //         also sums the weights its own keys get from its rows: S once more,
@@ -735,29 +767,9 @@ __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
             if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_S + slot, (j / C::NS) & 1, WAIT_NS))) { fail = true; break; }
             tc::fence_after();
             const float* nl = nl_s + j % C::NL * C::QN;
-            const int from = key - shift - t0;  // columns before it do not see the key
-            auto sum = [&](auto all) {
-#pragma unroll
-                for (int c0 = 0; c0 < C::QN; c0 += 32) {
-                    uint32_t o[32];
-                    tc::ld32(t_lane + slot * C::QN + c0, o);
-                    tc::ld_wait();
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int u = 0; u < 32; u += 4) {
-                        const float4 e = *reinterpret_cast<const float4*>(nl + c0 + u);
-                        const float ee[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const float p = tc::ex2(fmaf(__uint_as_float(o[u + v]), c, ee[v]));
-                            acc[v] += decltype(all)::value || c0 + u + v >= from ? p : 0.f;
-                        }
-                    }
-                    total += (acc[0] + acc[1]) + (acc[2] + acc[3]);
-                }
-            };
-            if (t0 >= last) sum(std::true_type());
-            else sum(std::false_type());
+            const uint32_t at = t_lane + slot * C::QN;
+            // (columns before key - shift - t0 do not see the key)
+            total += t0 >= last ? column_weights<true>(at, nl, c, 0) : column_weights<false>(at, nl, c, key - shift - t0);
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::arrive(bars + C::B_SF + slot);
