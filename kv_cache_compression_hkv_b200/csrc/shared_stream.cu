@@ -5,11 +5,11 @@
 // kernel is bound by HBM: a warp keeps three stages of 16 rows of K and V in
 // flight (cp.async, 16-byte pieces at a swizzled place; TMA boxes of 16 rows
 // took 16.1 us where these take 11.0, on 1024 heads of 28 to 138 tokens of
-// d = 128) and works on the oldest with mma.sync m16n8k16: S = Q K^T with the rows on the M side, the
-// weights straight from S's registers as the A operand of O += P V.  (A
-// tcgen05 tile would compute 128 rows for these 16 and pass the weights
-// through TMEM; at 8 KB of keys and values a step the legacy instruction's
-// rate is a third of what HBM leaves time for.)
+// d = 128) and works on the oldest with mma.sync m16n8k16: S = Q K^T with the
+// rows on the M side, the weights straight from S's registers as the A operand
+// of O += P V.  (A tcgen05 tile would compute 128 rows for these 16 and pass
+// the weights through TMEM; at 8 KB of keys and values a step the legacy
+// instruction takes a third of the time that HBM leaves for it.)
 #include <math.h>
 
 #include <type_traits>
@@ -59,7 +59,7 @@ __device__ __forceinline__ uint32_t pack(float x, float y) {
 template <int D> constexpr int stream_smem() { return SW * SN * 2 * SK * D * 2; }
 
 // WPH warps of a block work on one (sequence, KV head, key range): 1 (four
-// heads a block, nothing to join), 2 or 4 (steps dealt out in turn, joined in
+// heads a block, nothing to join) or 4 (steps dealt out in turn, joined in
 // shared memory).  LOW: at most 8 rows, the upper half of the M side is empty.
 // Where the item has all of the rows' keys (no splits, the prefix listed with
 // the own keys) the results are final, the accumulated weights too.
@@ -410,7 +410,6 @@ cudaError_t launch_stream(const View& a, int d, int warps_per_head, bool beside,
     auto by_warps = [&](auto dim) {
         constexpr int D = decltype(dim)::value;
         if (warps_per_head == 1) return low ? run(stream_attend_kernel<D, 1, true>) : run(stream_attend_kernel<D, 1, false>);
-        if (warps_per_head == 2) return low ? run(stream_attend_kernel<D, 2, true>) : run(stream_attend_kernel<D, 2, false>);
         return low ? run(stream_attend_kernel<D, 4, true>) : run(stream_attend_kernel<D, 4, false>);
     };
     return d == 128 ? by_warps(std::integral_constant<int, 128>()) : by_warps(std::integral_constant<int, 64>());
@@ -425,8 +424,6 @@ cudaError_t prepare_shared_stream() {
         constexpr int D = decltype(dim)::value;
         set(stream_attend_kernel<D, 1, true>, stream_smem<D>());
         set(stream_attend_kernel<D, 1, false>, stream_smem<D>());
-        set(stream_attend_kernel<D, 2, true>, stream_smem<D>());
-        set(stream_attend_kernel<D, 2, false>, stream_smem<D>());
         set(stream_attend_kernel<D, 4, true>, stream_smem<D>());
         set(stream_attend_kernel<D, 4, false>, stream_smem<D>());
     };

@@ -15,9 +15,8 @@
 // V1 K2, ... as they are used together); an MMA warp a row tile, one lane of
 // which waits and issues.
 // S of tile j + 1 is issued as soon as the rows hold S of tile j in registers,
-// so a softmax warp finds its next logits ready.  (With P over S's own place
-// and two such places, S of tile j + 2 had to wait for the product of tile j
-// behind the other row tile's: 2150 cycles a tile.)
+// so a softmax warp finds its next logits ready.  (With P over S's own place S of
+// tile j + 2 had to wait for the product of tile j behind the other row tile's.)
 #include <math.h>
 
 #include <type_traits>
@@ -40,6 +39,7 @@ using ptx::smem_u32;
 constexpr int QT = 128;
 constexpr int UK = 64;  // keys of a tile
 constexpr float RAISE = 16.f;
+constexpr float BIG = 16777216.f;  // 2^24: logits from here on are off by one and more
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
 template <int D, int NT> struct Shape {
@@ -58,13 +58,24 @@ template <int D, int NT> struct Shape {
 
 }  // namespace
 
+// What the sums add to a row's logits: minus the log2 of its sum (l2 = -inf: the
+// row has no weights).  Where that is beyond BIG it is off by more than one and
+// would let weights be infinite, so there it is lowered by more than its and the
+// logits' rounding.
+__device__ __forceinline__ float less_sum(float l2) {
+    return l2 == -INFINITY ? l2 : fabsf(l2) > BIG ? -l2 - fabsf(l2) * 0x1p-21f : -l2;
+}
+
 // sum over 128 columns from taddr (a thread's lane) of 2^(c S + nl), for the
-// columns from `from` on (all of them: ALL).
+// columns [from, to) (all of them: ALL).  Columns past the last query hold no
+// zeros where a key is infinite.
 template <bool ALL>
-__device__ __forceinline__ float column_weights(uint32_t taddr, const float* nl, float c, int from) {
+__device__ __forceinline__ float column_weights(uint32_t taddr, const float* nl, float c, int from, int to) {
     float total = 0.f;
+    const unsigned span = max(0, to - from);
 #pragma unroll
     for (int c0 = 0; c0 < QT; c0 += 32) {
+        if (!ALL && c0 >= to) break;
         uint32_t o[32];
         tc::ld32(taddr + c0, o);
         tc::ld_wait();
@@ -78,8 +89,8 @@ __device__ __forceinline__ float column_weights(uint32_t taddr, const float* nl,
                                           v == 0 ? make_float2(e.x, e.y) : make_float2(e.z, e.w));
                 float2 p = make_float2(tc::ex2(y.x), tc::ex2(y.y));
                 if (!ALL) {
-                    p.x = c0 + u + v >= from ? p.x : 0.f;
-                    p.y = c0 + u + v + 1 >= from ? p.y : 0.f;
+                    p.x = (unsigned)(c0 + u + v - from) < span ? p.x : 0.f;
+                    p.y = (unsigned)(c0 + u + v + 1 - from) < span ? p.y : 0.f;
                 }
                 acc[v >> 1] = tc::add2(acc[v >> 1], p);
             }
@@ -285,9 +296,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
     } else if (warp >= C::MMA_WARP) {
         // All that an MMA's operands come from is made uniform first (with
         // addresses in per-thread registers an issue took 84 cycles, up to
-        // three times the product), and one lane does the waiting too (votes
-        // of the warp around each wait idled the tensor cores: a tile of two
-        // row tiles took 2150 cycles, of which the products are 1260).
+        // three times the product), and one lane does the waiting too (with
+        // votes of the warp around each wait the products were 1260 cycles of
+        // the 2150 that a key tile of two row tiles took).
         constexpr uint32_t IS = tc::idesc_bf16(UK, false), IO = tc::idesc_bf16(D, true);
         const uint32_t tm = tc::uniform(tmem);
         const int nn = tc::uniform(n);
@@ -386,7 +397,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
         const int lim = MODE != 1 ? (live ? own_limit(a, n_own, ri) : 0x7fffffff) : 0;
         const int lim_warp = __shfl_sync(FULL_MASK, lim, 0);  // the least of the warp's
         const int nt = NT == 2 ? (x == 0 ? nx[0] : nx[NT - 1]) : nx[0];
-        float m = -INFINITY, l = 0.f;  // reference maximum (times c) and sum
+        // reference maximum (before c), the logit above which it is raised, what a
+        // tile's logits are lowered by, and the sum
+        float ref = -INFINITY, above = -INFINITY, mb = 0.f, l = 0.f;
+        // Some row's c ref is so large that c S - c ref would be off by its
+        // rounding: the warp comes to the raise with every tile, and S - ref is formed.
+        bool far = false;
         const bool idle = !__any_sync(FULL_MASK, live);  // no row of the warp is one: it only keeps the barriers' counts
         // every branch around the warp-wide TMEM accesses is taken by the whole warp
         for (int j = 0; j < nt; ++j) {
@@ -435,10 +451,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int u = 0; u < UK; ++u) mx[u & 3] = fmaxf(mx[u & 3], __uint_as_float(sr[u >> 5][u & 31]));
-            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-            if (__any_sync(FULL_MASK, mt > m + RAISE)) {
-                const float mn = fmaxf(m, mt);
-                const float alpha = mn == -INFINITY ? 1.f : exp2f(m - mn);
+            const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            if (__any_sync(FULL_MASK, most * c > above)) {
+                const float rn = fmaxf(ref, most), m = rn * c;
+                const float alpha = rn == -INFINITY ? 1.f : exp2f((ref - rn) * c);
                 if (j > 0) {
                     const int jp = j - 1;
                     if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_PV + 2 * x + (jp & 1), (jp >> 1) & 1, WAIT_NS))) {
@@ -458,9 +474,16 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                     tc::st_wait();
                 }
                 l *= alpha;
-                m = mn;
+                ref = rn;
+                far = __any_sync(FULL_MASK, far || (fabsf(m) > BIG && m != -INFINITY));
+                mb = m == -INFINITY || far ? 0.f : m;
+                above = far ? -INFINITY : m + RAISE;
+                if (far) {
+                    const float r = rn == -INFINITY ? 0.f : rn;
+#pragma unroll
+                    for (int u = 0; u < UK; ++u) sr[u >> 5][u & 31] = __float_as_uint(__uint_as_float(sr[u >> 5][u & 31]) - r);
+                }
             }
-            const float mb = m == -INFINITY ? 0.f : m;
             uint32_t w[32];
             float2 ls[4];
 #pragma unroll
@@ -488,9 +511,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
             const int jl = nt - 1;
             if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_PV + 2 * x + (jl & 1), (jl >> 1) & 1, WAIT_NS))) fail = true;
         }
+        const float m = ref == -INFINITY ? ref : ref * c;
         if (MODE == 0 && NT == 1 && n2 > 0) {
             // every row thread comes here, failed or not
-            nl_s[tid] = live && !(m == -INFINITY && l == 0.f) ? -(m + log2f(l)) : -INFINITY;
+            nl_s[tid] = live && !(m == -INFINITY && l == 0.f) ? less_sum(m + log2f(l)) : -INFINITY;
             asm volatile("bar.sync 1, %0;" ::"n"(C::ROWS) : "memory");
             const int shift = n_own - a.T;  // key j is seen by the queries t >= j - shift
             const int sh = s * a.Hk + hk;
@@ -502,10 +526,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                 if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_T, kb & 1, WAIT_NS))) { fail = true; break; }
                 tc::fence_after();
                 const int from = (key - shift) * a.rep - first;  // rows of the block before it do not see the key
-                const bool whole = __shfl_sync(FULL_MASK, from, 31) <= 0;
+                const bool whole = rows == QT && __shfl_sync(FULL_MASK, from, 31) <= 0;
+                const unsigned span = max(0, rows - from);
                 float total = 0.f;
 #pragma unroll
                 for (int c0 = 0; c0 < QT; c0 += 32) {
+                    if (c0 >= rows) break;  // (past the last row no zeros where a key is infinite)
                     uint32_t o[32];
                     tc::ld32(t_s + c0, o);
                     tc::ld_wait();
@@ -517,7 +543,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
 #pragma unroll
                         for (int v = 0; v < 4; ++v) {
                             const float p = tc::ex2(fmaf(__uint_as_float(o[u + v]), c, ee[v]));
-                            acc[v] += whole || c0 + u + v >= from ? p : 0.f;
+                            acc[v] += whole || (unsigned)(c0 + u + v - from) < span ? p : 0.f;
                         }
                     }
                     total += (acc[0] + acc[1]) + (acc[2] + acc[3]);
@@ -700,8 +726,7 @@ __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
 #pragma unroll
             for (int u = 0; u < C::QN / 32; ++u) {
                 const int t = (tile0 + j % per_head) * C::QN + u * 32 + lane;
-                const float e = j < tiles && t < a.T ? src[t] : -INFINITY;
-                nl[u] = e == -INFINITY ? -INFINITY : -e;
+                nl[u] = less_sum(j < tiles && t < a.T ? src[t] : -INFINITY);
             }
         };
         if (tiles > 0) fetch(0);
@@ -769,7 +794,8 @@ __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
             const float* nl = nl_s + j % C::NL * C::QN;
             const uint32_t at = t_lane + slot * C::QN;
             // (columns before key - shift - t0 do not see the key)
-            total += t0 >= last ? column_weights<true>(at, nl, c, 0) : column_weights<false>(at, nl, c, key - shift - t0);
+            total += t0 >= last && t0 + C::QN <= a.T ? column_weights<true>(at, nl, c, 0, C::QN)
+                                                     : column_weights<false>(at, nl, c, key - shift - t0, min(C::QN, a.T - t0));
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::arrive(bars + C::B_SF + slot);

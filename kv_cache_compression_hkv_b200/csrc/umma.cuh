@@ -110,7 +110,6 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-
 // Two fp32 operations in one instruction: x y + z, and x + y.
 __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
     float2 r;

@@ -224,6 +224,62 @@ def test_masked_places_may_hold_the_lowest_value(dtype):
     assert torch.isnan(out).all() and torch.isnan(lse).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 5, 20, 40, 130, 600])
+def test_infinite_keys_take_no_weight(dtype, T):
+    """A key whose logits are all -inf: no weight, and none becomes NaN, whatever
+    the row tiles' ends hold (the sums of many rows are formed in whole tiles)."""
+    c, q = make(dtype, S=2, H=2, Hk=1, T=T, cap=T + 70, G=1, P=40, lens=T + 70)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    x, y = c.k.clone(), c.weight.clone()
+    c.k[:, :, 5, 0] = -float("inf")
+    out, lse = c.attend(q)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    assert torch.isfinite(c.weight).all() and torch.equal(c.weight[:, :, 5], y[:, :, 5])
+    # the same as without it: a logit far below the others
+    c.k.copy_(x)
+    c.k[:, :, 5] = 0
+    c.k[:, :, 5, 0] = -1e6
+    w = c.weight.clone()
+    c.weight.copy_(y)
+    out2, lse2 = c.attend(q)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2) and torch.equal(w, c.weight)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 5, 20, 130, 600])
+@pytest.mark.parametrize("big", [2.0 ** 30, 2.0 ** 100])
+def test_logits_far_from_zero(dtype, T, big):
+    """Every visible logit near +-big or exactly there: the largest take all the
+    weight, shared alike, however large the numbers (2^24 on, fp32 no longer
+    holds the logits' fractions).  Powers of two, so that nothing rounds."""
+    S, d, n = 1, 64, T + 40
+    c, _ = make(dtype, S=S, H=2, Hk=1, T=T, cap=n, G=0, d=d, lens=n)
+    g = torch.Generator().manual_seed(T)
+    c.v.copy_(torch.randn(c.v.shape, generator=g))
+    q = torch.zeros(S, 2, T, d, dtype=DT[dtype], device=DEV)
+    q[..., 0] = 1
+    for sign in (1.0, -1.0):
+        # all alike: the mean of what a query sees
+        c.k.zero_()
+        c.k[..., 0] = sign * big
+        c.weight.zero_()
+        out, lse = c.attend(q)
+        v = c.v[0, 0].double()
+        see = n - T + 1 + torch.arange(T, device=DEV)
+        want = v.cumsum(0)[see - 1] / see[:, None]
+        bound = 2.0 ** -7 * v.abs().cumsum(0)[see - 1] / see[:, None] + 1e-6
+        assert ((out[0].double() - want).abs() <= bound).all()
+        assert torch.allclose(lse.double(), torch.full_like(lse, sign * big / 8).double(), rtol=1e-6)
+        assert torch.isfinite(c.weight).all() and (c.weight >= 0).all() and (c.weight <= 2 * T).all()
+        # the third key twice as large: all of the weight
+        c.k[0, 0, 2, 0] = sign * big * (2 if sign > 0 else 0.5)
+        c.weight.zero_()
+        out, lse = c.attend(q)
+        assert ((out[0].double() - v[2]).abs() <= 2.0 ** -8 * v[2].abs()).all()
+        assert (c.weight[0, 0, [0, 1, 3]] == 0).all() and 0 <= float(c.weight[0, 0, 2]) <= 2 * T
+
+
 def test_same_bits_twice():
     for T in (1, 6, 60):
         c, q = make("bf16", S=4, H=8, Hk=2, T=T, cap=500, P=300, d=128)
