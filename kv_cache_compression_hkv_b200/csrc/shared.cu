@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(C::THREADS, 4) attend_f32_kernel(const __grid_
                 if (final) {
                     const float l2 = some ? m[u] + log2f(ls) : -INFINITY;
                     if (a.lse) a.lse[row] = l2 * 0.6931471805599453f;
-                    if (a.row_lse) a.row_lse[row] = l2;
+                    if (a.row_nl) a.row_nl[row] = less_sum(l2);
                     sm.ml[r] = make_float2(m[u], f);
                 } else {
                     a.part_ml[ml_index(a, row, slot)] = make_float2(m[u], ls);
@@ -487,7 +487,7 @@ __device__ __forceinline__ void write_row(const View& a, const RowJoin& j, int64
     if (lane == 0) {
         const float l2 = some ? j.M + log2f(j.L) : -INFINITY;
         if (a.lse) a.lse[row] = l2 * 0.6931471805599453f;
-        if (a.row_lse) a.row_lse[row] = l2;
+        if (a.row_nl) a.row_nl[row] = less_sum(l2);
     }
 }
 
@@ -615,11 +615,11 @@ __global__ void __launch_bounds__(C::THREADS, 4) column_sums_f32_kernel(const __
         }
         __syncthreads();
         if (f + RT < rps) fetch(f + RT);
-        float lse[RW];
+        float nl[RW];
 #pragma unroll
         for (int u = 0; u < RW; ++u) {
             const int i = f + warp * RW + u;
-            lse[u] = i < rps ? a.row_lse[row_of(a, s, hk, i)] : -INFINITY;
+            nl[u] = i < rps ? a.row_nl[row_of(a, s, hk, i)] : -INFINITY;
         }
         if (f + warp * RW >= rps) continue;
         float x[RW][KPL], tile[KPL];
@@ -630,8 +630,8 @@ __global__ void __launch_bounds__(C::THREADS, 4) column_sums_f32_kernel(const __
         for (int u = 0; u < RW; ++u)
 #pragma unroll
             for (int p = 0; p < KPL; ++p)
-                if (lse[u] != -INFINITY && k0 + lane + 32 * p < own_limit(a, n, f + warp * RW + u))
-                    tile[p] += exp2f(x[u][p] - lse[u]);
+                if (nl[u] != -INFINITY && k0 + lane + 32 * p < own_limit(a, n, f + warp * RW + u))
+                    tile[p] += exp2f(x[u][p] + nl[u]);
 #pragma unroll
         for (int p = 0; p < KPL; ++p) total[p] += tile[p];
     }

@@ -18,8 +18,10 @@ constexpr int KEY_STEP = 64;     // key ranges start at multiples of this
 constexpr int MAX_SPLITS = 64;   // splits of the own keys, and of the prefix keys
 constexpr int MAX_PREFIXES = 1024;
 // Own tokens of at most this many query rows (query heads of a KV head x
-// queries) are streamed once with every row's logits kept for the
-// accumulated weights; more rows recompute the logits for them.
+// queries) are streamed once with every row's logits kept for the accumulated
+// weights, bf16 as one M side of mma.sync; more rows go to the tcgen05 tiles and
+// recompute the logits.  (16 rows, d = 128, streamed / tiles: 12 heads of 9000 to
+// 32001 slots 39.6 / 112 us, 512 heads of 56 to 477 34.5 / 38.5 us.)
 constexpr int STREAM_ROWS = 16;
 
 // The cache and one call's tensors, by value.
@@ -53,8 +55,19 @@ struct View {
     int32_t lcap;     // capacity rounded up to 4
     int32_t sum_tiles;  // row tiles of a (sequence, KV head) whose blocks sum the weights themselves (0: they do not)
     float* part_sum;    // [sum_tiles][S][Hk][cap] their sums, where there are several
-    float* row_lse;   // [R] log2 of the row sums (tile path, accumulate)
+    float* row_nl;    // [R] less_sum of the rows (weights summed in a pass of their own)
 };
+
+// 2^24: logits from here on are off by one and more.
+constexpr float BIG = 16777216.f;
+
+// What the sums of the weights add to a row's logits: minus the log2 of its sum
+// (l2 = -inf: the row has no weights).  Beyond BIG that is off by more than one
+// and would let weights be infinite: there it is lowered by more than its own
+// and the logits' rounding.
+__device__ __forceinline__ float less_sum(float l2) {
+    return l2 == -INFINITY ? l2 : fabsf(l2) > BIG ? -l2 - fabsf(l2) * 0x1p-21f : -l2;
+}
 
 __device__ __forceinline__ int clamp_len(int n, int cap) { return n < 0 ? 0 : (n > cap ? cap : n); }
 __device__ __forceinline__ int own_len(const View& a, int s, int hk) {
@@ -194,9 +207,9 @@ inline int64_t max_prefix_tiles(int S, int G, int rows_per_seq, int rt) {
 
 // Row tiles of 128 that a tensor-core block takes.  With one, two blocks share
 // an SM and hide each other's beginnings and ends, and the block can sum its
-// keys' weights; with two, the row tiles share the copies of K and V.  (256 rows
-// over 384 keys, 512 heads: 58 us with one, 65 with two; 16004 rows over
-// 5001 keys: 398 with two.)
+// keys' weights; with two, the row tiles share the copies of K and V.  (d = 128,
+// with the weights, one / two: 512 heads of 256 rows 59.9 / 80.3 us, 256 heads of
+// 512 rows 77 / 90; 128 heads of 1024 110 / 110; 16 heads of 16004 580 / 567.)
 constexpr int ONE_TILE_ROWS = 512;
 inline int umma_row_tiles(int64_t rows_per_seq) { return rows_per_seq > ONE_TILE_ROWS ? 2 : 1; }
 

@@ -88,8 +88,11 @@ struct Plan {
     size_t bytes;
 };
 
-// Prefix rows read by all sequences together up to which they are folded.
-constexpr int64_t FOLD_BYTES = 48 << 20;
+// Bytes of prefix rows that all sequences together read up to which they are
+// folded.  (us, d = 128, folded / once: 1024 heads over 64, 192, 384 shared keys
+// 12.9 / 18.5, 17.9 / 19.4, 25.5 / 20.9, which is 34, 101, 201 MB; 128 heads of
+// four query heads over 1024, 2048: 16.0 / 19.3, 20.9 / 21.0, or 67, 134 MB.)
+constexpr int64_t FOLD_BYTES = 128 << 20;
 
 Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char* base) {
     a.T = T;
@@ -116,7 +119,9 @@ Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char
         const int64_t items = heads * ((rps + 128 * nt - 1) / (128 * nt));
         a.no = items >= 148 ? 1 : splits(nt == 2 ? 148 : 296, items, keys, 256);
     } else if (p.stream) {
-        // eight warps fit an SM: a head goes to as many as fill the GPU, one or several blocks of four
+        // eight warps fit an SM: a head goes to as many as fill the GPU, one or
+        // several blocks of four (one warp / a block a head: 1024 heads of 28 to
+        // 138 tokens 12.8 / 18.5 us, 512 of 56 to 477 22.6 / 17.0)
         const int64_t warps = (148 * 8 + heads / 2) / heads, most = (keys + 31) / 32;
         const int64_t n = warps < most ? warps : most;
         p.warps_per_head = n > 1 ? 4 : 1;
@@ -149,7 +154,7 @@ Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char
     a.sum_tiles = accumulate && p.umma_rows && a.no == 1 && rps <= hkv::shared::ONE_TILE_ROWS ? (int)((rps + 127) / 128) : 0;
     if (accumulate && few) a.logit = (float*)take((size_t)heads * rps * a.lcap * 4);
     if (a.sum_tiles > 1) a.part_sum = (float*)take((size_t)a.sum_tiles * heads * a.cap * 4);
-    if (accumulate && !few && !a.sum_tiles) a.row_lse = (float*)take((size_t)R * 4);
+    if (accumulate && !few && !a.sum_tiles) a.row_nl = (float*)take((size_t)R * 4);
     p.bytes = o;
     return p;
 }
@@ -236,7 +241,7 @@ hkv_status hkv_shared_attend(const hkv_shared_cache* c, const void* q, const int
     if (e == cudaSuccess && c->dtype == HKV_DTYPE_F32) e = hkv::shared::launch_attend_f32(a, d, st);
     if (e == cudaSuccess && a.part_ml) e = hkv::shared::launch_combine(a, c->dtype, d, st);
     if (e == cudaSuccess && a.part_sum) e = hkv::shared::launch_add_sums(a, st);
-    if (e == cudaSuccess && a.row_lse)
+    if (e == cudaSuccess && a.row_nl)
         e = p.umma_rows ? hkv::shared::launch_column_sums_umma(a, d, st)
                         : hkv::shared::launch_column_sums_f32(a, d, st);
     return cuda_status(e);

@@ -26,10 +26,17 @@ namespace shared {
 namespace {
 
 constexpr int BINS = 2048;
-constexpr int CAND = 64;        // candidates ranked against each other (256 cost short heads four times the rest)
+constexpr int CAND = 64;        // candidates ranked against each other (with 256, 512 heads of 477 slots took 40 us instead of 23)
 constexpr int LIST = 512;       // moves whose slots stay in shared memory
-constexpr int SHORT_CAP = 2048; // capacities up to this: blocks of 128 threads that also move the rows
-constexpr int HELD_CAP = 24576; // capacities up to this: weights and positions in shared memory (195 KB)
+// Blocks of 128 threads that also move the rows, up to SHORT_CAP slots where
+// there are more heads than SMs, else up to half as many; more: blocks of 1024,
+// and a launch for the rows.  (us, 128 / 1024 threads: 1024 heads of 2000 slots
+// 58.8 / 106.5, 256 of 2000 29.2 / 31.8, 148 of 1400 22.4 / 20.5; 32 heads of 477
+// 13.0 / 15.6, of 1000 18.6 / 17.8, of 2000 26.6 / 20.0.)
+constexpr int SHORT_CAP = 2048;
+// Capacities up to this: weights and positions in shared memory (200 KB; 64 heads
+// of up to 24576 slots: 157 us held, 178 read again for every step).
+constexpr int HELD_CAP = 24576;
 
 // Bits that order as (recent, weight): recent tokens highest, then NaN, then
 // the numbers (-0 as +0).
@@ -350,7 +357,7 @@ cudaError_t launch_evict(const View& a, int dtype, int d, const int32_t* budget,
     int2* counts = reinterpret_cast<int2*>(scratch);
     int32_t* lists = reinterpret_cast<int32_t*>(scratch + ((size_t)heads * 8 + 255) / 256 * 256);
     const size_t held = held_bytes(a.cap);
-    if (a.cap <= SHORT_CAP)
+    if (a.cap <= (heads > 148 ? SHORT_CAP : SHORT_CAP / 2))
         return launch(select_kernel<128, true>, heads, 128, held, st, a, budget, recent, slack, row, es, 1, lists, counts);
     const cudaError_t e =
         a.cap <= HELD_CAP

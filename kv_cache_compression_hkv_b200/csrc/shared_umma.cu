@@ -39,7 +39,6 @@ using ptx::smem_u32;
 constexpr int QT = 128;
 constexpr int UK = 64;  // keys of a tile
 constexpr float RAISE = 16.f;
-constexpr float BIG = 16777216.f;  // 2^24: logits from here on are off by one and more
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
 template <int D, int NT> struct Shape {
@@ -57,14 +56,6 @@ template <int D, int NT> struct Shape {
 };
 
 }  // namespace
-
-// What the sums add to a row's logits: minus the log2 of its sum (l2 = -inf: the
-// row has no weights).  Where that is beyond BIG it is off by more than one and
-// would let weights be infinite, so there it is lowered by more than its and the
-// logits' rounding.
-__device__ __forceinline__ float less_sum(float l2) {
-    return l2 == -INFINITY ? l2 : fabsf(l2) > BIG ? -l2 - fabsf(l2) * 0x1p-21f : -l2;
-}
 
 // sum over 128 columns from taddr (a thread's lane) of 2^(c S + nl), for the
 // columns [from, to) (all of them: ALL).  Columns past the last query hold no
@@ -145,31 +136,30 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
     // Where piece c of row r of a row tile lies in the swizzled K-major tile.
     auto q_off = [](int r, int c) { return (c / 8) * (QT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
     // Starts the copies of the warp's rows of Q into the swizzled tile, whole
-    // rows at a time, so that they run while the lengths are looked up.
+    // rows at a time, so that they run while the lengths are looked up.  Threads
+    // past the last row take that row (zeros would give NaN with a key that is
+    // infinite, in the sums over all of a tile's columns).
     auto load_q = [&]() {
         if (warp >= 4 * NT) return;
         live = tid < rows;
-        if (live) {
-            if constexpr (MODE != 1) {
-                sq = s;
-                ri = first + tid;
-            } else {
-                const int f = first + tid;
-                sq = list[f / rps - first / rps];
-                ri = f % rps;
-            }
+        const int f = first + min(tid, rows - 1);
+        if constexpr (MODE != 1) {
+            sq = s;
+            ri = f;
+        } else {
+            sq = list[f / rps - first / rps];
+            ri = f % rps;
         }
         t = query_of(a, ri);
         h = hk * a.rep + ri - t * a.rep;
         const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-        const int64_t at = live ? sq * a.qs[0] + h * a.qs[1] + t * a.qs[2] : -1;
+        const int64_t at = sq * a.qs[0] + h * a.qs[1] + t * a.qs[2];
         const uint32_t tile = smem_u32(q_s + (warp >> 2) * C::Q_BYTES);
 #pragma unroll
         for (int e = 0; e < CH; ++e) {
             const int r = e * RPI + lane / CH, c = lane % CH;
             const int64_t o = __shfl_sync(FULL_MASK, at, r);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile + q_off((warp & 3) * 32 + r, c)),
-                         "l"(q + (o < 0 ? 0 : o) + c * 8), "r"(o < 0 ? 0 : 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tile + q_off((warp & 3) * 32 + r, c)), "l"(q + o + c * 8)
                          : "memory");
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -393,7 +383,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
         const float c = fabsf(a.qscale);
         const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t t_s = t_lane + x * 128, t_o = t_lane + C::O_COL + x * D;
-        // own keys this row sees; rows past the last one compute on zeros
+        // own keys this row sees; what threads past the last row make is not used
         const int lim = MODE != 1 ? (live ? own_limit(a, n_own, ri) : 0x7fffffff) : 0;
         const int lim_warp = __shfl_sync(FULL_MASK, lim, 0);  // the least of the warp's
         const int nt = NT == 2 ? (x == 0 ? nx[0] : nx[NT - 1]) : nx[0];
@@ -526,12 +516,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                 if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_T, kb & 1, WAIT_NS))) { fail = true; break; }
                 tc::fence_after();
                 const int from = (key - shift) * a.rep - first;  // rows of the block before it do not see the key
-                const bool whole = rows == QT && __shfl_sync(FULL_MASK, from, 31) <= 0;
-                const unsigned span = max(0, rows - from);
+                const bool whole = __shfl_sync(FULL_MASK, from, 31) <= 0;
                 float total = 0.f;
 #pragma unroll
                 for (int c0 = 0; c0 < QT; c0 += 32) {
-                    if (c0 >= rows) break;  // (past the last row no zeros where a key is infinite)
+                    if (c0 >= rows) break;
                     uint32_t o[32];
                     tc::ld32(t_s + c0, o);
                     tc::ld_wait();
@@ -543,7 +532,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
 #pragma unroll
                         for (int v = 0; v < 4; ++v) {
                             const float p = tc::ex2(fmaf(__uint_as_float(o[u + v]), c, ee[v]));
-                            acc[v] += whole || (unsigned)(c0 + u + v - from) < span ? p : 0.f;
+                            acc[v] += whole || c0 + u + v >= from ? p : 0.f;
                         }
                     }
                     total += (acc[0] + acc[1]) + (acc[2] + acc[3]);
@@ -617,7 +606,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                 if (final) {
                     const float l2 = some ? m + log2f(l) : -INFINITY;
                     if (a.lse) a.lse[row] = l2 * 0.6931471805599453f;
-                    if (a.row_lse) a.row_lse[row] = l2;
+                    if (a.row_nl) a.row_nl[row] = less_sum(l2);
                 } else {
                     a.part_ml[ml_index(a, row, piece)] = make_float2(l != l && m == -INFINITY ? 0.f : m, l);
                 }
@@ -667,7 +656,7 @@ template <int D> struct SumShape {
 }  // namespace
 
 // weight[key] += sum over rows of 2^(c q.k - lse2[row]), the log2 of the row
-// sums being known: the logits once more, keys on the M side, so that a
+// sums (row_nl: its negative) being known: the logits once more, keys on the M side, so that a
 // thread owns a key (TMEM lane) and sums along its own columns.  One block
 // per (sequence, KV head, 128 keys) walks 128-query tiles of each query head
 // in turn, from the first query that sees its first key on; two groups of
@@ -722,11 +711,11 @@ __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
         // S was issued after the rows had finished with tile j - 4.
         float nl[C::QN / 32];
         auto fetch = [&](int j) {
-            const float* src = a.row_lse + row_index(a, s, hk * a.rep + j / per_head, 0);
+            const float* src = a.row_nl + row_index(a, s, hk * a.rep + j / per_head, 0);
 #pragma unroll
             for (int u = 0; u < C::QN / 32; ++u) {
                 const int t = (tile0 + j % per_head) * C::QN + u * 32 + lane;
-                nl[u] = less_sum(j < tiles && t < a.T ? src[t] : -INFINITY);
+                nl[u] = j < tiles && t < a.T ? src[t] : -INFINITY;
             }
         };
         if (tiles > 0) fetch(0);
