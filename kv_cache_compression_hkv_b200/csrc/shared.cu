@@ -104,7 +104,8 @@ cudaError_t launch_append(const View& a, int dtype, int d, const void* k_t, cons
 // ---------------------------------------------------------------------------
 
 // A block's shape: four warps of RW rows each, steps of 32 KPL keys in ST
-// stages.  Few rows (up to 16 of a head): 4 x 4 rows, two stages.  More: 4 x 8
+// stages.  Few rows (9 to 16 of a head, and the prefixes' rows beside the
+// streaming kernel): 4 x 4 rows, two stages.  More: 4 x 8
 // rows, and two keys a lane where d = 64 leaves the shared memory for it: a
 // warp then reads 10 times from shared memory for 64 fused multiply-adds
 // instead of 5 for 16; one stage, so that four blocks share an SM and hide each
@@ -663,8 +664,8 @@ template <typename F> cudaError_t by_type(int dtype, int d, F&& f) {
 
 namespace {
 
-template <int D, typename C> cudaError_t attend_f32(const View& a, cudaStream_t st) {
-    const int rps = a.rep * a.T, otiles = (rps + C::RT - 1) / C::RT;
+template <int D, typename C> cudaError_t attend_f32(const View& a, bool rows_too, cudaStream_t st) {
+    const int rps = a.rep * a.T, otiles = rows_too ? (rps + C::RT - 1) / C::RT : 0;
     const int64_t ptiles = a.np ? max_prefix_tiles(a.S, a.G, rps, C::RT) : 0;
     const int64_t blocks = ptiles * a.Hk * a.np + (int64_t)a.S * a.Hk * otiles * a.no;
     return launch(attend_f32_kernel<D, C>, blocks, C::THREADS, sizeof(typename C::Smem) + (size_t)a.G * 4, st, a,
@@ -686,10 +687,10 @@ template <int D> cudaError_t sums_f32(const View& a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_attend_f32(const View& a, int d, cudaStream_t st) {
+cudaError_t launch_attend_f32(const View& a, int d, bool rows_too, cudaStream_t st) {
     if (a.rep * a.T <= STREAM_ROWS)
-        return d == 64 ? attend_f32<64, FewF32<64>>(a, st) : attend_f32<128, FewF32<128>>(a, st);
-    return d == 64 ? attend_f32<64, ManyF32<64>>(a, st) : attend_f32<128, ManyF32<128>>(a, st);
+        return d == 64 ? attend_f32<64, FewF32<64>>(a, rows_too, st) : attend_f32<128, FewF32<128>>(a, rows_too, st);
+    return d == 64 ? attend_f32<64, ManyF32<64>>(a, rows_too, st) : attend_f32<128, ManyF32<128>>(a, rows_too, st);
 }
 
 cudaError_t launch_column_sums_f32(const View& a, int d, cudaStream_t st) {

@@ -23,6 +23,7 @@ constexpr int MAX_PREFIXES = 1024;
 // recompute the logits.  (16 rows, d = 128, streamed / tiles: 12 heads of 9000 to
 // 32001 slots 39.6 / 112 us, 512 heads of 56 to 477 34.5 / 38.5 us.)
 constexpr int STREAM_ROWS = 16;
+constexpr int STREAM_ROWS_F32 = 8;  // see shared_stream_f32.cu
 
 // The cache and one call's tensors, by value.
 struct View {
@@ -137,6 +138,33 @@ __device__ __forceinline__ int own_limit(const View& a, int n, int i) {
     return lim < 0 ? 0 : lim;
 }
 
+// Adds the weights 2^(x - M) / l of a head's kept logits to its accumulated
+// ones, rows in order: slots k0, k0 + step, ..., four at once.  ml: the rows' (M, 1 / l).
+__device__ __forceinline__ void add_kept(const View& a, int sh, int n, const float2* ml, int k0, int step) {
+    const int rps = a.rep * a.T;
+    const float* lg = a.logit + (int64_t)sh * rps * a.lcap;
+    float* w = a.weight + (int64_t)sh * a.cap;
+    for (; k0 < n; k0 += 4 * step) {
+        float sum[4], old[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            sum[v] = 0.f;
+            old[v] = k0 + step * v < n ? w[k0 + step * v] : 0.f;
+        }
+        for (int i = 0; i < rps; ++i) {
+            const float2 y = ml[i];
+            if (y.x == -INFINITY) continue;
+            const float* x = lg + (int64_t)i * a.lcap + k0;
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                if (k0 + step * v < n) sum[v] += exp2f(x[step * v] - y.x) * y.y;
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            if (k0 + step * v < n) w[k0 + step * v] = old[v] + sum[v];
+    }
+}
+
 // Finds the `tile`-th tile of `rt` rows among the prefixes' row lists: the
 // rows of prefix g are those of the sequences that continue it (ascending),
 // rep * T each, and every prefix starts a new tile.  Gives the prefix, the
@@ -247,7 +275,10 @@ cudaError_t launch_add_sums(const View& a, cudaStream_t st);
 cudaError_t launch_prefix_umma(const View& a, int d, cudaStream_t st);
 cudaError_t launch_append(const View& a, int dtype, int d, const void* k_t, const int64_t* kts, const void* v_t,
                           const int64_t* vts, const float* w_t, cudaStream_t st);
-cudaError_t launch_attend_f32(const View& a, int d, cudaStream_t st);
+// rows_too: the own keys of every row, else the prefixes' tiles alone
+cudaError_t launch_attend_f32(const View& a, int d, bool rows_too, cudaStream_t st);
+cudaError_t prepare_shared_stream_f32();
+cudaError_t launch_stream_f32(const View& a, int d, int warps_per_head, bool beside, cudaStream_t st);
 cudaError_t prepare_shared_stream();
 // beside: launched right behind the prefixes' kernel, whose end this launch's end includes
 cudaError_t launch_stream(const View& a, int d, int warps_per_head, bool beside, cudaStream_t st);

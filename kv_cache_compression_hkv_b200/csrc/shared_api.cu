@@ -92,6 +92,8 @@ struct Plan {
 // folded.  (us, d = 128, folded / once: 1024 heads over 64, 192, 384 shared keys
 // 12.9 / 18.5, 17.9 / 19.4, 25.5 / 20.9, which is 34, 101, 201 MB; 128 heads of
 // four query heads over 1024, 2048: 16.0 / 19.3, 20.9 / 21.0, or 67, 134 MB.)
+// fp32 up to half of that, as its rows cost arithmetic (1024 heads over 64: 23.9 /
+// 30.8, 67 MB; 640 heads, d = 64, over 300: 32.0 / 24.2, 98 MB).
 constexpr int64_t FOLD_BYTES = 128 << 20;
 
 Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char* base) {
@@ -99,10 +101,10 @@ Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char
     a.accumulate = accumulate;
     const int64_t rps = (int64_t)a.rep * T, R = (int64_t)a.S * a.H * T, heads = (int64_t)a.S * a.Hk;
     const bool few = rps <= hkv::shared::STREAM_ROWS, bf16 = dtype == HKV_DTYPE_BF16;
-    const bool fold = a.G == 0 || !few || heads * a.pcap * d * (bf16 ? 4 : 8) <= FOLD_BYTES;
+    const bool fold = a.G == 0 || !few || heads * a.pcap * d * (bf16 ? 4 : 8) <= (bf16 ? FOLD_BYTES : FOLD_BYTES / 2);
     const int64_t keys = (int64_t)a.cap + (fold && a.G ? a.pcap : 0);  // of a list of keys, at most
     Plan p;
-    p.stream = bf16 && few;
+    p.stream = few && (bf16 || rps <= hkv::shared::STREAM_ROWS_F32);
     p.umma_rows = bf16 && !few;
     p.umma_prefix = bf16 && !fold;
     p.warps_per_head = 1;
@@ -169,6 +171,7 @@ cudaError_t prepare() {
     if (ready.load() & bit) return cudaSuccess;
     e = hkv::shared::prepare_shared_umma();
     if (e == cudaSuccess) e = hkv::shared::prepare_shared_stream();
+    if (e == cudaSuccess) e = hkv::shared::prepare_shared_stream_f32();
     if (e == cudaSuccess) e = hkv::shared::prepare_shared_evict();
     if (e == cudaSuccess) e = hkv::shared::prepare_shared_f32();
     if (e == cudaSuccess && dev < 64) ready.fetch_or(bit);
@@ -237,8 +240,11 @@ hkv_status hkv_shared_attend(const hkv_shared_cache* c, const void* q, const int
     const int d = c->head_dim;
     if (e == cudaSuccess && p.umma_rows) e = hkv::shared::launch_attend_umma(a, d, st);
     if (e == cudaSuccess && p.umma_prefix) e = hkv::shared::launch_prefix_umma(a, d, st);
-    if (e == cudaSuccess && p.stream) e = hkv::shared::launch_stream(a, d, p.warps_per_head, p.umma_prefix, st);
-    if (e == cudaSuccess && c->dtype == HKV_DTYPE_F32) e = hkv::shared::launch_attend_f32(a, d, st);
+    if (e == cudaSuccess && c->dtype == HKV_DTYPE_F32 && (!p.stream || a.np))
+        e = hkv::shared::launch_attend_f32(a, d, !p.stream, st);
+    if (e == cudaSuccess && p.stream)
+        e = c->dtype == HKV_DTYPE_F32 ? hkv::shared::launch_stream_f32(a, d, p.warps_per_head, a.np > 0, st)
+                                      : hkv::shared::launch_stream(a, d, p.warps_per_head, a.np > 0, st);
     if (e == cudaSuccess && a.part_ml) e = hkv::shared::launch_combine(a, c->dtype, d, st);
     if (e == cudaSuccess && a.part_sum) e = hkv::shared::launch_add_sums(a, st);
     if (e == cudaSuccess && a.row_nl)

@@ -372,27 +372,7 @@ __global__ void __launch_bounds__(32 * SW, 2) stream_attend_kernel(const __grid_
         }
         if (final && a.logit) {  // (the same for the whole block)
             __syncthreads();
-            if (on)
-                for (int k0 = wi * 32 + lane; k0 < n; k0 += 4 * 32 * WPH) {
-                    float sum[4], old[4];
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        const int key = k0 + 32 * WPH * v;
-                        sum[v] = 0.f;
-                        old[v] = key < n ? w[key] : 0.f;
-                    }
-                    for (int i = 0; i < rps; ++i) {
-                        const float2 y = joined[warp / WPH][i];
-                        if (y.x == -INFINITY) continue;
-                        const float* x = lg + (int64_t)i * a.lcap + k0;
-#pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            if (k0 + 32 * WPH * v < n) sum[v] += exp2f(x[32 * WPH * v] - y.x) * y.y;
-                    }
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        if (k0 + 32 * WPH * v < n) w[k0 + 32 * WPH * v] = old[v] + sum[v];
-                }
+            if (on) add_kept(a, sh, n, joined[warp / WPH], wi * 32 + lane, 32 * WPH);
         }
     }
     // this grid ends after the one it was launched beside (the prefixes')

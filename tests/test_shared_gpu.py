@@ -112,6 +112,33 @@ def test_long_prefixes_read_once(dtype, T, H, Hk, d, P):
     check(c, q, accumulate=False)
 
 
+@pytest.mark.parametrize("T,H,Hk,d,P", [(1, 2, 2, 128, 4100), (1, 8, 2, 128, 4100), (4, 4, 2, 64, 8300),
+                                        (2, 14, 2, 128, 4099), (16, 2, 2, 128, 4100)])
+def test_more_sequences_over_long_prefixes(T, H, Hk, d, P):
+    """The same with more sequences: beyond 128 MiB of prefix rows a pass, which
+    bf16 caches read again up to."""
+    S = 37
+    assert S * Hk * P * d * 4 > 128 << 20
+    of = [(i * i + i // 7) % 4 - 1 for i in range(S)]
+    lens = torch.arange(S * Hk).view(S, Hk) * 7 % 60
+    c, q = make("bf16", S=S, H=H, Hk=Hk, d=d, T=T, cap=61, G=3, P=P, plens=[P, P - 77, 0], of=of, lens=lens, seed=T)
+    check(c, q)
+    check(c, q, accumulate=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hk,T", [(1, 1, 1), (2, 1, 1), (3, 1, 1), (4, 1, 1), (5, 1, 1), (8, 1, 1), (9, 1, 1), (3, 1, 3),
+                                    (2, 1, 4), (10, 10, 2)])
+@pytest.mark.parametrize("S", [2, 90])
+def test_few_rows(dtype, d, H, Hk, T, S):
+    """Every row count of the streaming kernels, with several blocks a head, one,
+    and several heads a block."""
+    c, q = make(dtype, S=S, H=H, Hk=Hk, d=d, T=T, cap=T + 300 if S == 2 else T + 30, G=3, P=70 if S == 2 else 9,
+                plens=[70, 33, 0] if S == 2 else [9, 4, 0], seed=H + T, slot_major=T == 3)
+    check(c, q)
+
+
 @pytest.mark.parametrize("dtype,S,H,Hk,T", [("bf16", 10, 16, 16, 20), ("bf16", 37, 4, 2, 130), ("bf16", 1, 2, 1, 300),
                                             ("f32", 10, 16, 16, 20), ("f32", 1, 3, 1, 150)])
 def test_many_rows_one_pass(dtype, S, H, Hk, T):
