@@ -305,6 +305,8 @@ HKV_API hkv_status hkv_ste_select_batch(const float* score, const int32_t* pos, 
  * are contiguous.  k, v and prefix rows start on 16-byte boundaries (bases
  * and strides).  Rows of two slots may not overlap, and strides of held rows
  * are positive (of a dimension of one: anything).
+ * The first attend or evict on a device raises the kernels' shared-memory
+ * limits there: make it before a stream capture.
  * Integers read on the device are taken in range: a len outside
  * [0, capacity] or a prefix_len outside [0, prefix_capacity] as the nearer
  * bound, a prefix_of outside [0, num_prefixes) as no prefix. */
@@ -370,7 +372,11 @@ HKV_API hkv_status hkv_shared_attend_bytes(const hkv_shared_cache* cache, int32_
  *  scratch: >= hkv_shared_attend_bytes bytes, 256-byte aligned, not shared
  *          by calls that may overlap on the GPU.
  * Rows of free slots are never used, whatever they hold; NaN or infinities
- * in k or v rows of tokens that are held reach any query of their sequence.
+ * in k or v rows of tokens that are held reach any query of their sequence
+ * (a logit of -inf is a weight of 0).  Products and sums are held in 32 bits;
+ * with bf16 rows the weights of the values are rounded to bf16.  From logits
+ * of 2^24 (in units of log 2) on, fp32 holds no fractions of them: outputs
+ * are then those of the largest ones, and the weights added lie in 0 .. 1 a row.
  * Errors: INVALID_ARG, CAPACITY (scratch too small), CUDA. */
 HKV_API hkv_status hkv_shared_attend(const hkv_shared_cache* cache, const void* q,
                                      const int64_t* q_stride, void* out,

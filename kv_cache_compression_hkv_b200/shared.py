@@ -200,6 +200,7 @@ class SharedPrefixCache:
         zeros and -inf.  accumulate adds to `weight` the softmax weights each
         own token received.  scale of the logits: 1 / sqrt(d) by default."""
         qs = self._tensor(q, "q", self.cfg.num_heads)
+        accumulate = bool(accumulate)
         plan = self._plans.get((q.shape[2], accumulate))
         if plan is None:
             plan = self._plan(q.shape[2], accumulate)
@@ -244,7 +245,7 @@ class SharedPrefixCache:
         c = self.cfg
         if T < 1 or T > c.capacity:
             raise ValueError("q: between 1 token and the capacity")
-        acc, n = int(bool(accumulate)), C.c_size_t()
+        acc, n = int(accumulate), C.c_size_t()
         _check(lib().hkv_shared_attend_bytes(self._ref, T, acc, C.byref(n)), "hkv_shared_attend_bytes")
         plan = (T, acc, n.value, self.weight.new_empty(1).expand(c.num_seqs, c.num_heads, T),
                 self.lens.new_empty(1).expand(n.value // 4))
@@ -261,8 +262,8 @@ class SharedPrefixCache:
         if not isinstance(budgets, torch.Tensor) or budgets.dtype != torch.int32 or budgets.device != self.device or \
                 budgets.shape != (c.num_seqs, c.num_kv_heads) or not budgets.is_contiguous():
             raise ValueError("budgets: expected a contiguous int32 [S, Hkv] tensor on the device")
-        if recent < 0 or slack < 1:
-            raise ValueError("recent at least 0, slack at least 1")
+        if not (0 <= recent < 1 << 31 and 1 <= slack < 1 << 31):
+            raise ValueError("recent at least 0, slack at least 1, both below 2**31")
 
         def args():
             scratch = torch.empty_like(self._evict_like)

@@ -485,7 +485,7 @@ def test_captured_step_replays(dtype, S, T, P):
         assert torch.equal(a.nan_to_num(-1.0), x.nan_to_num(-1.0))
 
 
-@pytest.mark.parametrize("S,T,P,cap", [(8, 1, 2000, 3000), (24, 1, 4000, 300), (3, 40, 500, 900)])
+@pytest.mark.parametrize("S,T,P,cap", [(8, 1, 2000, 3000), (24, 1, 4000, 300), (36, 1, 4000, 300), (3, 40, 500, 900)])
 def test_several_streams_at_once(S, T, P, cap):
     """Calls that only read the cache may overlap: each has its own scratch."""
     c, q = make("bf16", S=S, H=8, Hk=2, d=128, T=T, cap=cap, P=P, lens=cap)
@@ -549,6 +549,11 @@ def test_python_refusals():
         c.evict(ok, -1)
     with pytest.raises(ValueError):
         c.evict(ok, 0, 0)
+    for far in (1 << 31, 1 << 32):
+        with pytest.raises(ValueError):
+            c.evict(ok, far)
+        with pytest.raises(ValueError):
+            c.evict(ok, 0, far)
     with pytest.raises(ValueError):
         hkv.SharedPrefixCache(c.cfg, DEV, k=c.k[..., :32])
     with pytest.raises(ValueError):
