@@ -8,6 +8,7 @@ and decide what an eviction drops.  This module marshals arguments only.
 from __future__ import annotations
 
 import ctypes as C
+from contextlib import contextmanager
 from dataclasses import dataclass
 
 import torch
@@ -27,6 +28,7 @@ class _Cache(C.Structure):
 
 
 _Strides = C.c_int64 * 3
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 @dataclass
@@ -72,7 +74,7 @@ class SharedPrefixCache:
             raise ValueError(f"device: expected a CUDA device, got {dev}")
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-        self.device = dev
+        self.device, self._index = dev, dev.index
         S, Hk, d, cap, G = cfg.num_seqs, cfg.num_kv_heads, cfg.head_dim, cfg.capacity, cfg.num_prefixes
         if cfg.dtype not in (DTYPE_F32, DTYPE_BF16) or d not in (64, 128) or S < 1 or Hk < 1 or \
                 cfg.num_heads < 1 or cfg.num_heads % Hk or cap < 1 or G < 0 or (G > 0 and cfg.prefix_capacity < 1):
@@ -148,19 +150,13 @@ class SharedPrefixCache:
         raise ValueError(f"{name}: expected a {c.torch_dtype} tensor [{c.num_seqs}, {heads}, T, {c.head_dim}] on "
                          f"{self.device}")
 
-    def _call(self, fn, what, stream, args):
-        """fn(*args, stream) with (args, scratch) = args(): allocations and
-        launches on `stream` (the current one by default) of the cache's
-        device.  The scratch is held until the launches are enqueued."""
-        index = self.device.index
+    @contextmanager
+    def _on(self, stream):
+        """The cache's device and `stream` (its current one by default) as
+        torch's current ones, for allocations and launches; gives the handle."""
         if stream is None:
-            if torch._C._cuda_getDevice() == index:
-                a, _scratch = args()
-                _check(fn(*a, torch._C._cuda_getCurrentRawStream(index)), what)
-            else:
-                with torch.cuda.device(index):
-                    a, _scratch = args()
-                    _check(fn(*a, torch._C._cuda_getCurrentRawStream(index)), what)
+            with torch.cuda.device(self._index):
+                yield _current_stream(self._index)
             return
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=self.device) if int(stream) else \
@@ -168,14 +164,14 @@ class SharedPrefixCache:
         if stream.device != self.device:
             raise ValueError(f"stream: of {stream.device}, the cache is on {self.device}")
         with torch.cuda.stream(stream):
-            a, _scratch = args()
-            _check(fn(*a, stream.cuda_stream), what)
+            yield stream.cuda_stream
 
     # -- calls ---------------------------------------------------------------
     def append(self, k_t, v_t, weight_t=None, stream=None):
         """Adds T tokens to every head: k_t, v_t [S, Hkv, T, d]; weight_t
-        [S, Hkv, T] fp32, their accumulated weights (default 0).  A head
-        without T free slots is left as it was (see check)."""
+        [S, Hkv, T] fp32, their accumulated weights (default 0); none of them
+        views of the cache.  A head without T free slots is left as it was
+        (see check)."""
         c = self.cfg
         ks = self._tensor(k_t, "k_t", c.num_kv_heads)
         vs = self._tensor(v_t, "v_t", c.num_kv_heads)
@@ -188,9 +184,14 @@ class SharedPrefixCache:
             raise ValueError("weight_t: expected a contiguous float32 [S, Hkv, T] tensor on the device")
         if T == 0:
             return
-        self._call(self._append_fn, "hkv_shared_append", stream,
-                   lambda: ((self._ref, k_t.data_ptr(), ks, v_t.data_ptr(), vs,
-                             None if weight_t is None else weight_t.data_ptr(), T), None))
+        w = None if weight_t is None else weight_t.data_ptr()
+        if stream is None and _current_device() == self._index:
+            code = self._append_fn(self._ref, k_t.data_ptr(), ks, v_t.data_ptr(), vs, w, T, _current_stream(self._index))
+        else:
+            with self._on(stream) as handle:
+                code = self._append_fn(self._ref, k_t.data_ptr(), ks, v_t.data_ptr(), vs, w, T, handle)
+        if code:
+            _check(code, "hkv_shared_append")
 
     def attend(self, q, out=None, lse=None, accumulate=True, scale=None, stream=None):
         """Attention of each sequence's newest T tokens (appended before):
@@ -204,7 +205,6 @@ class SharedPrefixCache:
         plan = self._plans.get((q.shape[2], accumulate))
         if plan is None:
             plan = self._plan(q.shape[2], accumulate)
-        T, accumulate, need, lse_like, scratch_like = plan
         if not (qs[0] and qs[1] and qs[2]) and any(n > 1 and st == 0 for n, st in zip(q.shape, q.stride())):
             raise ValueError("q: no repeated rows")
         if scale is None:
@@ -213,30 +213,33 @@ class SharedPrefixCache:
             raise ValueError("scale: a finite number other than 0")
         if out is not None:
             self._tensor(out, "out", self.cfg.num_heads)
-            if out.shape != q.shape or 0 in out.stride():
-                raise ValueError("out: expected q's shape, no repeated rows")
+            if out.shape != q.shape or 0 in out.stride() or out.data_ptr() == q.data_ptr():
+                raise ValueError("out: expected q's shape, no repeated rows, and not q itself")
         if lse is not None and (lse.dtype != torch.float32 or lse.device != self.device or
                                 lse.shape != q.shape[:3] or not lse.is_contiguous()):
             raise ValueError("lse: expected a contiguous float32 [S, H, T] tensor on the device")
 
-        def args():
-            nonlocal out, lse
-            so = qs
-            if out is None:
-                if q.is_contiguous():
-                    out = torch.empty_like(q)
-                else:
-                    out = q.new_empty(q.shape)
-                    so = _Strides(*out.stride()[:3])
-            else:
-                so = _Strides(*out.stride()[:3])
-            if lse is None:
-                lse = torch.empty_like(lse_like)
-            scratch = torch.empty_like(scratch_like)
-            return (self._ref, q.data_ptr(), qs, out.data_ptr(), so, lse.data_ptr(), T, scale, accumulate,
-                    scratch.data_ptr(), need), scratch
+        if stream is None and _current_device() == self._index:
+            return self._attend(q, qs, out, lse, plan, scale, _current_stream(self._index))
+        with self._on(stream) as handle:
+            return self._attend(q, qs, out, lse, plan, scale, handle)
 
-        self._call(self._attend_fn, "hkv_shared_attend", stream, args)
+    def _attend(self, q, qs, out, lse, plan, scale, handle):
+        T, accumulate, need, lse_like, scratch_like = plan
+        so = qs
+        if out is None and q.is_contiguous():
+            out = torch.empty_like(q)
+        else:
+            if out is None:
+                out = q.new_empty(q.shape)
+            so = _Strides(*out.stride()[:3])
+        if lse is None:
+            lse = torch.empty_like(lse_like)
+        scratch = torch.empty_like(scratch_like)  # (held until the launches are enqueued)
+        code = self._attend_fn(self._ref, q.data_ptr(), qs, out.data_ptr(), so, lse.data_ptr(), T, scale, accumulate,
+                               scratch.data_ptr(), need, handle)
+        if code:
+            _check(code, "hkv_shared_attend")
         return out, lse
 
     def _plan(self, T, accumulate):
@@ -265,11 +268,17 @@ class SharedPrefixCache:
         if not (0 <= recent < 1 << 31 and 1 <= slack < 1 << 31):
             raise ValueError("recent at least 0, slack at least 1, both below 2**31")
 
-        def args():
-            scratch = torch.empty_like(self._evict_like)
-            return (self._ref, budgets.data_ptr(), recent, slack, scratch.data_ptr(), self._evict_bytes), scratch
+        if stream is None and _current_device() == self._index:
+            self._evict(budgets, recent, slack, _current_stream(self._index))
+        else:
+            with self._on(stream) as handle:
+                self._evict(budgets, recent, slack, handle)
 
-        self._call(self._evict_fn, "hkv_shared_evict", stream, args)
+    def _evict(self, budgets, recent, slack, handle):
+        scratch = torch.empty_like(self._evict_like)
+        code = self._evict_fn(self._ref, budgets.data_ptr(), recent, slack, scratch.data_ptr(), self._evict_bytes, handle)
+        if code:
+            _check(code, "hkv_shared_evict")
 
     def check(self):
         """(code, detail) of the first error latched on the device (waits)."""

@@ -530,6 +530,8 @@ def test_python_refusals():
         c.attend(q[:, :, :0])
     with pytest.raises(ValueError):
         c.attend(q, out=q[:1].expand(3, 4, 1, 64))
+    with pytest.raises(ValueError, match="not q itself"):
+        c.attend(q, out=q)
     with pytest.raises(ValueError):
         c.attend(q, lse=torch.empty(3, 4, 2, device=DEV))
     for s in (0, float("nan"), float("inf")):
