@@ -60,7 +60,10 @@ template <int D> constexpr int stream_smem() { return SW * SN * 2 * SK * D * 2; 
 
 // WPH warps of a block work on one (sequence, KV head, key range): 1 (four
 // heads a block, nothing to join) or 4 (steps dealt out in turn, joined in
-// shared memory).  LOW: at most 8 rows, the upper half of the M side is empty.
+// shared memory).  LOW: at most 8 rows; the upper half of the M side takes what
+// rounding the weights to bf16 leaves (as weights of their own, added up at the
+// end), which with more rows is a second product.  With the weights rounded alone
+// the outputs were off by as much again as by their own rounding.
 // Where the item has all of the rows' keys (no splits, the prefix listed with
 // the own keys) the results are final, the accumulated weights too.
 template <int D, int WPH, bool LOW>
@@ -220,11 +223,16 @@ __global__ void __launch_bounds__(32 * SW, 2) stream_attend_kernel(const __grid_
                     for (int c = 0; c < D / 8; ++c) {
                         o[c][2 * u] *= alpha;
                         o[c][2 * u + 1] *= alpha;
+                        if (LOW) {
+                            o[c][2] *= alpha;
+                            o[c][3] *= alpha;
+                        }
                     }
                     m[u] = mn;
                 }
             }
-            uint32_t pa[4] = {0u, 0u, 0u, 0u};
+            // a weight as the sum of two bf16: its rounding to one, and of what that leaves
+            uint32_t pa[4], pl[4];
 #pragma unroll
             for (int u = 0; u < NT; ++u) {
                 const float mb = m[u] == -INFINITY ? 0.f : m[u];
@@ -232,7 +240,9 @@ __global__ void __launch_bounds__(32 * SW, 2) stream_attend_kernel(const __grid_
                 for (int h = 0; h < 2; ++h) {
                     const float p0 = tc::ex2(x[h][2 * u] - mb), p1 = tc::ex2(x[h][2 * u + 1] - mb);
                     l[u] += p0 + p1;
-                    pa[2 * h + u] = pack(p0, p1);
+                    const uint32_t w = pack(p0, p1);
+                    pa[2 * h + u] = w;
+                    (LOW ? pa : pl)[2 * h + (LOW ? 1 : u)] = pack(p0 - __uint_as_float(w << 16), p1 - __uint_as_float(w & 0xffff0000u));
                 }
             }
             {
@@ -243,9 +253,19 @@ __global__ void __launch_bounds__(32 * SW, 2) stream_attend_kernel(const __grid_
                     ldsm4t(v_at ^ (c << 5), b);
                     mma16816(o[2 * c], pa, b[0], b[1]);
                     mma16816(o[2 * c + 1], pa, b[2], b[3]);
+                    if (!LOW) {
+                        mma16816(o[2 * c], pl, b[0], b[1]);
+                        mma16816(o[2 * c + 1], pl, b[2], b[3]);
+                    }
                 }
             }
         }
+        if (LOW)
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                o[c][0] += o[c][2];
+                o[c][1] += o[c][3];
+            }
         cp_wait<0>();
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
