@@ -104,12 +104,18 @@ __device__ __forceinline__ float column_weights(uint32_t taddr, const float* nl,
 //         results (slot = piece).
 // MODE 1: rows of all sequences of a prefix over the prefix's keys, cut in
 //         a.np ranges; partial results (slot = range).
+// Modes 1 and 2 (few rows over many keys) use both slots of P for one tile: the
+// weights as bf16, and what that rounding leaves, two products.  Outputs are then
+// off by their own rounding alone.  In mode 0 the second product would take the
+// tensor cores half as long again: there the rounding of the weights stays, about
+// as large as the outputs' own.
 template <int D, int NT, int MODE>
 __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
     attend_umma_kernel(const __grid_constant__ View a, const __grid_constant__ CUtensorMap km,
                        const __grid_constant__ CUtensorMap vm, const __grid_constant__ CUtensorMap pkm,
                        const __grid_constant__ CUtensorMap pvm, int row_tiles, int splits) {
     using C = Shape<D, NT>;
+    constexpr bool TWO = MODE != 0;
     extern __shared__ unsigned char raw[];
     unsigned char* base = reinterpret_cast<unsigned char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     unsigned char* q_s = base;
@@ -330,7 +336,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                     tc::fence_after();
 #pragma unroll
                     for (int kk = 0; kk < UK / 16; ++kk)
-                        tc::mma_ts(t_o, t_s + UK + (j & 1) * 32 + kk * 8, v_desc + pair + kk * 128, IO, (j > 0 || kk > 0));
+                        tc::mma_ts(t_o, t_s + UK + (TWO ? 0 : j & 1) * 32 + kk * 8, v_desc + pair + kk * 128, IO, (j > 0 || kk > 0));
+                    if constexpr (TWO) {
+#pragma unroll
+                        for (int kk = 0; kk < UK / 16; ++kk)
+                            tc::mma_ts(t_o, t_s + UK + 32 + kk * 8, v_desc + pair + kk * 128, IO, 1);
+                    }
                     tc::commit(bars + C::B_PV + 2 * x + (j & 1));
                     pv_done = j;
                 }
@@ -486,12 +497,24 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                 ls[u & 3] = tc::add2(ls[u & 3], p);
                 __nv_bfloat162 h2 = __floats2bfloat162_rn(p.x, p.y);
                 w[u] = *reinterpret_cast<uint32_t*>(&h2);
+                if constexpr (TWO) {  // in S's registers, what the rounding leaves
+                    h2 = __floats2bfloat162_rn(p.x - __uint_as_float(w[u] << 16), p.y - __uint_as_float(w[u] & 0xffff0000u));
+                    sr[0][u] = *reinterpret_cast<uint32_t*>(&h2);
+                }
             }
             ls[0] = tc::add2(tc::add2(ls[0], ls[1]), tc::add2(ls[2], ls[3]));
             l += ls[0].x + ls[0].y;
             // (P's slot is free: the commit behind S of tile j covers the product
-            // of tile j - 2)
-            tc::st32(t_s + UK + (j & 1) * 32, w);
+            // of tile j - 2; with both slots in use the last product has to be done)
+            if constexpr (TWO) {
+                if (j > 0 && __any_sync(FULL_MASK, !mbar_wait(bars + C::B_PV + 2 * x + ((j - 1) & 1), ((j - 1) >> 1) & 1, WAIT_NS))) {
+                    fail = true;
+                    break;
+                }
+                tc::fence_after();
+                tc::st32(t_s + UK + 32, sr[0]);
+            }
+            tc::st32(t_s + UK + (TWO ? 0 : j & 1) * 32, w);
             tc::st_wait();
             tc::fence_before();
             __syncwarp();
