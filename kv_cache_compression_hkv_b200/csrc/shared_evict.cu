@@ -13,7 +13,10 @@
 //
 // What bounds it: a short head (a few hundred tokens) the chain of block-wide
 // steps, so one small block a head and as many heads as fit at once; a long
-// one the rows that move, which a second launch spreads over the GPU.
+// one the rows that move, which a second launch spreads over the GPU.  d = 128,
+// bf16: 64 of 477 tokens of 512 heads 14 us, one of 28 to 107 of 1024 heads 9 us;
+// 8192 of 24576 of 64 heads 42 us for the selection, 64 us for 257 MB of rows
+// (launches alone).
 #include <algorithm>
 
 #include "kernels.h"

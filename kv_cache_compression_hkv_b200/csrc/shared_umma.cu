@@ -5,7 +5,7 @@
 // list of 64-key tiles, prefix first, then own keys up to the rows' causal
 // limit.  Per (row tile X, key tile j):
 //   S = Q_X K_j^T   (M 128, N 64, fp32 in TMEM)
-//   P = 2^(c S - m) as bf16 in TMEM, two slots a row tile
+//   P = 2^(c S - m) as bf16 in TMEM, two slots a row tile (see the modes below)
 //   O_X += P V_j    (A from TMEM, V as the MN-major operand, fp32 in TMEM)
 // Rows: thread = query row = TMEM lane.  m is a reference maximum that is
 // raised (and O rescaled in TMEM) only when a logit passes it by more than
@@ -17,6 +17,12 @@
 // S of tile j + 1 is issued as soon as the rows hold S of tile j in registers,
 // so a softmax warp finds its next logits ready.  (With P over S's own place S of
 // tile j + 2 had to wait for the product of tile j behind the other row tile's.)
+//
+// d = 128: 16004 rows of 16 heads over 2834 keys on average 367 us (1.0 PFLOP/s; the products
+// of a key tile of two row tiles take 1330 of about 2000 cycles, the rest are the
+// softmax's exponentials and the hand-over), 512 heads of 256 rows over 384 keys
+// 58 us with the weights, 512 heads of 49 rows over 49 to 462 and 128 39 us: there
+// each block's beginning and end, two blocks an SM to hide them.
 #include <math.h>
 
 #include <type_traits>
@@ -686,6 +692,8 @@ template <int D> struct SumShape {
 // four warps take every other tile.  (With 64 queries a tile an MMA waits for
 // shared memory, which gives it the 128 keys again for every 64 queries: 408
 // cycles instead of 256.)  A row that is not to be counted has -lse2 = -inf.
+// 16004 rows of 16 heads, 4001 keys, d = 128: 212 us, of exponentials (16 a cycle
+// an SM) as much as of products.
 template <int D>
 __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
     column_sums_umma_kernel(const __grid_constant__ View a, const __grid_constant__ CUtensorMap km,
