@@ -45,7 +45,6 @@ struct View {
     int64_t qs[3], os[3];
     float* lse;
     float qscale;     // scale * log2(e): logits are in the exp2 domain
-    int32_t accumulate;
     // partial results of a row: slots [0, np) the prefix's splits, [np, np + no) its own keys'
     int32_t np, no;
     // 1 (np is 0): the slots are no pieces of one list of 64-key tiles, the prefix's and then the own ones

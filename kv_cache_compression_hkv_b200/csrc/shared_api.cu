@@ -98,7 +98,6 @@ constexpr int64_t FOLD_BYTES = 128 << 20;
 
 Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char* base) {
     a.T = T;
-    a.accumulate = accumulate;
     const int64_t rps = (int64_t)a.rep * T, R = (int64_t)a.S * a.H * T, heads = (int64_t)a.S * a.Hk;
     const bool few = rps <= hkv::shared::STREAM_ROWS, bf16 = dtype == HKV_DTYPE_BF16;
     const bool fold = a.G == 0 || !few || heads * a.pcap * d * (bf16 ? 4 : 8) <= (bf16 ? FOLD_BYTES : FOLD_BYTES / 2);
