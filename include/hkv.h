@@ -373,11 +373,11 @@ HKV_API hkv_status hkv_shared_attend_bytes(const hkv_shared_cache* cache, int32_
  *          by calls that may overlap on the GPU.
  * Rows of free slots are never used, whatever they hold; NaN or infinities
  * in k or v rows of tokens that are held reach any query of their sequence
- * (a logit of -inf is a weight of 0).  Products and sums are held in 32 bits;
- * with bf16 rows and many queries the weights of the values are rounded to
- * bf16, with few they are not.  From logits
- * of 2^24 (in units of log 2) on, fp32 holds no fractions of them: outputs
- * are then those of the largest ones, and the weights added lie in 0 .. 1 a row.
+ * (a logit of -inf is a weight of 0).  Products and sums are held in 32 bits,
+ * and the values of bf16 caches are multiplied by 16 bits of each weight, however
+ * many queries there are.  From logits of 2^24 (in units of log 2) on, fp32 holds
+ * no fractions of them: outputs are then those of the largest ones, and the
+ * weights added lie in 0 .. 1 a row.
  * Errors: INVALID_ARG, CAPACITY (scratch too small), CUDA. */
 HKV_API hkv_status hkv_shared_attend(const hkv_shared_cache* cache, const void* q,
                                      const int64_t* q_stride, void* out,

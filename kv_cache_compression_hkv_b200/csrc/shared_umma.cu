@@ -5,8 +5,12 @@
 // list of 64-key tiles, prefix first, then own keys up to the rows' causal
 // limit.  Per (row tile X, key tile j):
 //   S = Q_X K_j^T   (M 128, N 64, fp32 in TMEM)
-//   P = 2^(c S - m) as bf16 in TMEM, two slots a row tile (see the modes below)
-//   O_X += P V_j    (A from TMEM, V as the MN-major operand, fp32 in TMEM)
+//   P = 2^(c S - m) as the sum of two bf16 in TMEM: its rounding to one, and of
+//       what that leaves
+//   O_X += P V_j    (two products; A from TMEM, V as the MN-major operand, fp32 in TMEM)
+// so that outputs are off by their own rounding alone.  (With P's rounding alone
+// their error was 2.1e-3 to 2.3e-3 relative, instead of 1.7e-3, and not the same in
+// every split of a call; the tensor cores had a third less to do.)
 // Rows: thread = query row = TMEM lane.  m is a reference maximum that is
 // raised (and O rescaled in TMEM) only when a logit passes it by more than
 // 16, so weights stay below 2^16 and bf16's relative rounding is unaffected;
@@ -110,18 +114,12 @@ __device__ __forceinline__ float column_weights(uint32_t taddr, const float* nl,
 //         results (slot = piece).
 // MODE 1: rows of all sequences of a prefix over the prefix's keys, cut in
 //         a.np ranges; partial results (slot = range).
-// Modes 1 and 2 (few rows over many keys) use both slots of P for one tile: the
-// weights as bf16, and what that rounding leaves, two products.  Outputs are then
-// off by their own rounding alone.  In mode 0 the second product would take the
-// tensor cores half as long again: there the rounding of the weights stays, about
-// as large as the outputs' own.
 template <int D, int NT, int MODE>
 __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
     attend_umma_kernel(const __grid_constant__ View a, const __grid_constant__ CUtensorMap km,
                        const __grid_constant__ CUtensorMap vm, const __grid_constant__ CUtensorMap pkm,
                        const __grid_constant__ CUtensorMap pvm, int row_tiles, int splits) {
     using C = Shape<D, NT>;
-    constexpr bool TWO = MODE != 0;
     extern __shared__ unsigned char raw[];
     unsigned char* base = reinterpret_cast<unsigned char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     unsigned char* q_s = base;
@@ -313,8 +311,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
             // Pair i: S of tile i once it has landed and the rows have read S of
             // tile i - 1, then P V of tile i - 1 once its weights are written.
             // (One warp for both row tiles kept S of one waiting for the weights
-            // of the other.)  The commit behind S of tile i also covers P V of
-            // tile i - 2, which tells the rows that P's place is free.
+            // of the other.)
             const uint32_t t_s = tm + x * 128, t_o = tm + C::O_COL + x * D;
             int s_done = -1, pv_done = -1, freed = 0, sums = 0;
             auto full = [&](int i) { return mbar_wait(bars + C::B_FULL + i % C::NS, (i / C::NS) & 1, WAIT_NS); };
@@ -342,12 +339,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                     tc::fence_after();
 #pragma unroll
                     for (int kk = 0; kk < UK / 16; ++kk)
-                        tc::mma_ts(t_o, t_s + UK + (TWO ? 0 : j & 1) * 32 + kk * 8, v_desc + pair + kk * 128, IO, (j > 0 || kk > 0));
-                    if constexpr (TWO) {
+                        tc::mma_ts(t_o, t_s + UK + kk * 8, v_desc + pair + kk * 128, IO, (j > 0 || kk > 0));
 #pragma unroll
-                        for (int kk = 0; kk < UK / 16; ++kk)
-                            tc::mma_ts(t_o, t_s + UK + 32 + kk * 8, v_desc + pair + kk * 128, IO, 1);
-                    }
+                    for (int kk = 0; kk < UK / 16; ++kk)
+                        tc::mma_ts(t_o, t_s + UK + 32 + kk * 8, v_desc + pair + kk * 128, IO, 1);
                     tc::commit(bars + C::B_PV + 2 * x + (j & 1));
                     pv_done = j;
                 }
@@ -503,24 +498,20 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                 ls[u & 3] = tc::add2(ls[u & 3], p);
                 __nv_bfloat162 h2 = __floats2bfloat162_rn(p.x, p.y);
                 w[u] = *reinterpret_cast<uint32_t*>(&h2);
-                if constexpr (TWO) {  // in S's registers, what the rounding leaves
-                    h2 = __floats2bfloat162_rn(p.x - __uint_as_float(w[u] << 16), p.y - __uint_as_float(w[u] & 0xffff0000u));
-                    sr[0][u] = *reinterpret_cast<uint32_t*>(&h2);
-                }
+                // in S's registers, what the rounding leaves
+                h2 = __floats2bfloat162_rn(p.x - __uint_as_float(w[u] << 16), p.y - __uint_as_float(w[u] & 0xffff0000u));
+                sr[0][u] = *reinterpret_cast<uint32_t*>(&h2);
             }
             ls[0] = tc::add2(tc::add2(ls[0], ls[1]), tc::add2(ls[2], ls[3]));
             l += ls[0].x + ls[0].y;
-            // (P's slot is free: the commit behind S of tile j covers the product
-            // of tile j - 2; with both slots in use the last product has to be done)
-            if constexpr (TWO) {
-                if (j > 0 && __any_sync(FULL_MASK, !mbar_wait(bars + C::B_PV + 2 * x + ((j - 1) & 1), ((j - 1) >> 1) & 1, WAIT_NS))) {
-                    fail = true;
-                    break;
-                }
-                tc::fence_after();
-                tc::st32(t_s + UK + 32, sr[0]);
+            // (P's place is free once the last product is done)
+            if (j > 0 && __any_sync(FULL_MASK, !mbar_wait(bars + C::B_PV + 2 * x + ((j - 1) & 1), ((j - 1) >> 1) & 1, WAIT_NS))) {
+                fail = true;
+                break;
             }
-            tc::st32(t_s + UK + (TWO ? 0 : j & 1) * 32, w);
+            tc::fence_after();
+            tc::st32(t_s + UK + 32, sr[0]);
+            tc::st32(t_s + UK, w);
             tc::st_wait();
             tc::fence_before();
             __syncwarp();
