@@ -64,7 +64,7 @@ template <int D> constexpr int stream_smem() { return SW * SN * 2 * SK * D * 2; 
 // WPH warps of a block work on one (sequence, KV head, key range): 1 (four
 // heads a block, nothing to join) or 4 (steps dealt out in turn, joined in
 // shared memory).  LOW: at most 8 rows; the upper half of the M side takes what
-// rounding the weights to bf16 leaves (as weights of their own, added up at the
+// the weights' first 8 bits leave (as weights of their own, added up at the
 // end), which with more rows is a second product.  With the weights rounded alone
 // the outputs were off by as much again as by their own rounding.
 // Where the item has all of the rows' keys (no splits, the prefix listed with
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(32 * SW, 2) stream_attend_kernel(const __grid_
                     m[u] = mn;
                 }
             }
-            // a weight as the sum of two bf16: its rounding to one, and of what that leaves
+            // a weight as the sum of two bf16: its first bits, and of what they leave
             uint32_t pa[4], pl[4];
 #pragma unroll
             for (int u = 0; u < NT; ++u) {
@@ -243,9 +243,7 @@ __global__ void __launch_bounds__(32 * SW, 2) stream_attend_kernel(const __grid_
                 for (int h = 0; h < 2; ++h) {
                     const float p0 = tc::ex2(x[h][2 * u] - mb), p1 = tc::ex2(x[h][2 * u + 1] - mb);
                     l[u] += p0 + p1;
-                    const uint32_t w = pack(p0, p1);
-                    pa[2 * h + u] = w;
-                    (LOW ? pa : pl)[2 * h + (LOW ? 1 : u)] = pack(p0 - __uint_as_float(w << 16), p1 - __uint_as_float(w & 0xffff0000u));
+                    split_weights(p0, p1, pa[2 * h + u], (LOW ? pa : pl)[2 * h + (LOW ? 1 : u)]);
                 }
             }
             {

@@ -5,8 +5,8 @@
 // list of 64-key tiles, prefix first, then own keys up to the rows' causal
 // limit.  Per (row tile X, key tile j):
 //   S = Q_X K_j^T   (M 128, N 64, fp32 in TMEM)
-//   P = 2^(c S - m) as the sum of two bf16 in TMEM: its rounding to one, and of
-//       what that leaves
+//   P = 2^(c S - m) as the sum of two bf16 in TMEM: its first bits, and of what
+//       they leave
 //   O_X += P V_j    (two products; A from TMEM, V as the MN-major operand, fp32 in TMEM)
 // so that outputs are off by their own rounding alone.  (With P's rounding alone
 // their error was 2.1e-3 to 2.3e-3 relative, instead of 1.7e-3, and not the same in
@@ -496,11 +496,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                                           make_float2(c, c), make_float2(-mb, -mb));
                 const float2 p = make_float2(tc::ex2(y.x), tc::ex2(y.y));
                 ls[u & 3] = tc::add2(ls[u & 3], p);
-                __nv_bfloat162 h2 = __floats2bfloat162_rn(p.x, p.y);
-                w[u] = *reinterpret_cast<uint32_t*>(&h2);
-                // in S's registers, what the rounding leaves
-                h2 = __floats2bfloat162_rn(p.x - __uint_as_float(w[u] << 16), p.y - __uint_as_float(w[u] & 0xffff0000u));
-                sr[0][u] = *reinterpret_cast<uint32_t*>(&h2);
+                split_weights(p.x, p.y, w[u], sr[0][u]);  // (over S's registers: logits 0 .. 2 u + 1 have been used)
             }
             ls[0] = tc::add2(tc::add2(ls[0], ls[1]), tc::add2(ls[2], ls[3]));
             l += ls[0].x + ls[0].y;

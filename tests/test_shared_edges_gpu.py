@@ -1,0 +1,43 @@
+"""The shared-prefix cache on the GPU at the ends of its ranges: infinities, the
+largest sizes, shapes of block that only large calls reach."""
+import pytest
+import torch
+
+import kv_cache_compression_hkv_b200 as hkv
+
+from test_shared_gpu import make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from kv_cache_compression_hkv_b200 import build
+    build.build()
+    assert torch.cuda.is_available(), "these tests need a CUDA device"
+
+
+# (S, H, Hk, T, own slots, prefix slots): every kernel, final results and pieces
+SHAPES = [(2, 4, 4, 1, 500, 100), (300, 4, 4, 1, 40, 20), (3, 12, 1, 1, 900, 100), (80, 32, 2, 1, 50, 33),
+          (40, 2, 2, 1, 60, 4100), (2, 4, 2, 10, 900, 100), (3, 2, 1, 400, 700, 100), (20, 8, 8, 49, 90, 30),
+          (2, 8, 1, 100, 140, 100)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("S,H,Hk,T,n,P", SHAPES)
+@pytest.mark.parametrize("where", ["own", "prefix"])
+def test_infinite_values_give_infinities(dtype, S, H, Hk, T, n, P, where):
+    """A value of +-inf that every query sees, with a weight above zero: that
+    infinity, in its column alone; both signs in one column: NaN."""
+    c, q = make(dtype, S=S, H=H, Hk=Hk, T=T, cap=n, G=1, P=P, plens=[P], of=[0] * S, lens=n, seed=n, sharp=0.0)
+    v = c.v if where == "own" else c.prefix_v
+    v[:, :, 0, 3] = float("inf")
+    v[:, :, 5, 3] = float("inf")
+    v[:, :, 7, 4] = -float("inf")
+    v[:, :, 1, 5] = -float("inf")
+    v[:, :, 2, 5] = float("inf")
+    out, lse = c.attend(q)
+    assert c.check() == (0, 0)
+    assert torch.isposinf(out[..., 3]).all() and torch.isneginf(out[..., 4]).all() and torch.isnan(out[..., 5]).all()
+    for x in (out[..., :3], out[..., 6:], lse, c.weight):
+        assert torch.isfinite(x).all()
