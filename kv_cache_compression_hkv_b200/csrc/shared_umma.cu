@@ -531,7 +531,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, NT == 2 ? 1 : 2)
                 const float old = a.sum_tiles == 1 && key < seen ? wrow[key] : 0.f;
                 if (__any_sync(FULL_MASK, !mbar_wait(bars + C::B_T, kb & 1, WAIT_NS))) { fail = true; break; }
                 tc::fence_after();
-                const int from = (key - shift) * a.rep - first;  // rows of the block before it do not see the key
+                // rows of the block before it do not see the key (the first slots of a long head, which
+                // every row sees, lie far below shift: times rep that would pass 32 bits)
+                const int from = max(0, key - shift) * a.rep - first;
                 const bool whole = __shfl_sync(FULL_MASK, from, 31) <= 0;
                 float total = 0.f;
 #pragma unroll

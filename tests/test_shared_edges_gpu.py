@@ -1,11 +1,13 @@
 """The shared-prefix cache on the GPU at the ends of its ranges: infinities, the
 largest sizes, shapes of block that only large calls reach."""
+import math
+
 import pytest
 import torch
 
 import kv_cache_compression_hkv_b200 as hkv
 
-from test_shared_gpu import make
+from test_shared_gpu import DEV, make
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +43,19 @@ def test_infinite_values_give_infinities(dtype, S, H, Hk, T, n, P, where):
     assert torch.isposinf(out[..., 3]).all() and torch.isneginf(out[..., 4]).all() and torch.isnan(out[..., 5]).all()
     for x in (out[..., :3], out[..., 6:], lse, c.weight):
         assert torch.isfinite(x).all()
+
+
+def test_weights_of_heads_past_32_bits_of_slots_times_rows():
+    """512 query rows a head over more than 2^22 slots: slot x row is beyond 2^31,
+    and every row's weight arrives.  All keys alike, so that each slot receives
+    512 / n: to 2^-21 for the exponential, 22 half steps of fp32 for the
+    logarithm of the sum and at most 512 for the sums, 4e-5 in all."""
+    S, rep, n, d = 37, 512, (1 << 22) + 200, 64
+    k = torch.zeros(S, 1, n, d, dtype=torch.bfloat16, device=DEV)
+    c = hkv.SharedPrefixCache(hkv.SharedConfig(S, rep, 1, d, n), DEV, k=k, v=k)
+    c.lens.fill_(n)
+    q = torch.randn(S, rep, 1, d, device=DEV).bfloat16()
+    out, lse = c.attend(q)
+    assert c.check() == (0, 0)
+    assert not out.any() and ((lse - math.log(n)).abs() < 1e-5).all()
+    assert ((c.weight * (n / rep) - 1).abs() < 4e-5).all()
