@@ -30,10 +30,9 @@ namespace shared {
 // them yet); with one, here.  8192 tokens of 64 heads, d = 128, bf16: 98 us, 537
 // MB or 5.5 TB/s.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) append_rows_kernel(View a, const T* __restrict__ kt, int64_t k0, int64_t k1,
-                                                          int64_t k2, const T* __restrict__ vt, int64_t v0,
-                                                          int64_t v1, int64_t v2, const float* __restrict__ wt,
-                                                          int n_new, int slices) {
+__global__ void __launch_bounds__(256) append_rows_kernel(View a, const T* kt, int64_t k0, int64_t k1, int64_t k2,
+                                                          const T* vt, int64_t v0, int64_t v1, int64_t v2,
+                                                          const float* wt, int n_new, int slices) {
     const int head = blockIdx.x / slices, part = blockIdx.x % slices;
     const int s = head / a.Hk, hk = head % a.Hk;
     ptx::grid_dep_wait();

@@ -255,7 +255,10 @@ __device__ __forceinline__ void split_weights(float p0, float p1, uint32_t& hi, 
 // the kernel in front of it in the stream drains, so it executes
 // griddepcontrol.wait before it touches memory, and lets the next launch begin
 // only after that.  (The streaming kernel beside the prefixes' one is the
-// exception: it starts on that kernel's word.)
+// exception: it starts on that kernel's word.)  A kernel's lifetime so begins before
+// what it reads is written: its parameters are not __restrict__ and nothing is read
+// by __ldg, which promise data that do not change during the kernel and may be
+// moved in front of the wait.
 template <typename... P, typename... A>
 cudaError_t launch(void (*kernel)(P...), int64_t blocks, int threads, size_t smem, cudaStream_t st, A... args) {
     if (blocks < 1 || blocks > 0x7fffffff) return cudaErrorInvalidValue;

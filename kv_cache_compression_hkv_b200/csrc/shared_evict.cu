@@ -108,9 +108,9 @@ __device__ __forceinline__ void move_rows(const View& a, int head, const int* ho
 // counts in `counts`) for move_kernel.
 template <int THREADS, bool HELD>
 __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__ View a,
-                                                         const int32_t* __restrict__ budget, int recent, int slack,
-                                                         int row_bytes, int es, int move, int32_t* __restrict__ lists,
-                                                         int2* __restrict__ counts) {
+                                                         const int32_t* budget, int recent, int slack,
+                                                         int row_bytes, int es, int move, int32_t* lists,
+                                                         int2* counts) {
     __shared__ EvictSmem<THREADS> sm;
     extern __shared__ __align__(16) unsigned char held_raw[];
     constexpr int WARPS = THREADS / 32;
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
 
 // Block (head, part): every parts-th group of the head's moves.
 __global__ void __launch_bounds__(256) move_kernel(const __grid_constant__ View a, int parts, int row_bytes, int es,
-                                                   const int32_t* __restrict__ lists, const int2* __restrict__ counts) {
+                                                   const int32_t* lists, const int2* counts) {
     const int head = blockIdx.x / parts;
     ptx::grid_dep_wait();
     const int2 c = counts[head];

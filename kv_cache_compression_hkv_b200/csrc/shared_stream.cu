@@ -94,8 +94,8 @@ __global__ void __launch_bounds__(32 * SW, 2) stream_attend_kernel(const __grid_
                                   t * a.qs[2];
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-            qa[kk][u] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + kk * 16 + q2)) : 0u;
-            qa[kk][2 + u] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + kk * 16 + q2 + 8)) : 0u;
+            qa[kk][u] = live ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + q2) : 0u;
+            qa[kk][2 + u] = live ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + q2 + 8) : 0u;
         }
     }
     const int n = own_len(a, s, hk);
