@@ -7,7 +7,7 @@ import torch
 
 import kv_cache_compression_hkv_b200 as hkv
 
-from test_shared_gpu import DEV, make
+from test_shared_gpu import DEV, evict_both, make
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,27 @@ def test_weights_of_heads_past_32_bits_of_slots_times_rows():
     assert c.check() == (0, 0)
     assert not out.any() and ((lse - math.log(n)).abs() < 1e-5).all()
     assert ((c.weight * (n / rep) - 1).abs() < 4e-5).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cap", [1025, 1400, 2048])
+def test_evict_many_heads_of_many_moves(dtype, cap):
+    """More heads than SMs of up to 2048 slots: small blocks that move their own
+    rows, up to 512 of them from lists in shared memory, more from the scratch."""
+    S, Hk = 19, 8
+    g = torch.Generator().manual_seed(cap)
+    c, _ = make(dtype, S=S, H=Hk, Hk=Hk, d=64, cap=cap, G=0, lens=cap, seed=cap)
+    c.pos.copy_(torch.argsort(torch.rand(S, Hk, cap, generator=g), -1))
+    b = torch.randint(cap // 2 - 100, cap // 2 + 100, (S, Hk), generator=g)
+    c.lens[3:7] = torch.randint(0, cap + 1, (4, Hk), generator=g).to(DEV)
+    # exactly so many moves: light tokens before the budget, and all but as many behind it
+    for h, moves in enumerate((0, 1, 511, 512, 513, cap - (cap + 1) // 2)):
+        moves = min(moves, cap // 2)
+        b[7, h] = (cap + 1) // 2
+        w = torch.full((cap,), 2.0)
+        w[:moves] = 1.0                                        # holes
+        w[(cap + 1) // 2 + moves:] = 1.0                       # gone in place
+        c.weight[7, h] = w
+    evict_both(c, b, 0, 1)
+    assert torch.equal(c.lens[7].cpu(), b[7].int())
+    evict_both(c, b // 2, 5, 3)
