@@ -31,6 +31,40 @@ _Strides = C.c_int64 * 3
 _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
+def _reaches(dims, lo, hi):
+    """Whether some sum of n_i s_i lies in (lo, hi): dims are (s_i, least n_i, most
+    n_i), largest s_i first."""
+    if not dims:
+        return lo < 0 < hi
+    (s, a, b), rest = dims[0], dims[1:]
+    least, most = sum(t * x for t, x, _ in rest), sum(t * y for t, _, y in rest)
+    # n s + [least, most] meets (lo, hi): n from (lo - most) / s to (hi - least) / s
+    return any(_reaches(rest, lo - n * s, hi - n * s)
+               for n in range(max(a, -((most - lo) // s)), min(b, (hi - least) // s) + 1))
+
+
+def _overlap(x, y):
+    """Whether two tensors hold a common byte.  Their last dimensions are
+    contiguous rows of one dtype's elements; views that lie between each other's
+    rows do not overlap."""
+    def extent(t):
+        return t.data_ptr(), t.data_ptr() + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+    if not x.numel() or not y.numel():
+        return False
+    (xa, xb), (ya, yb) = extent(x), extent(y)
+    if xb <= ya or yb <= xa:
+        return False
+    span = {}  # stride in bytes -> the range of index differences
+    for t, sign in ((x, 1), (y, -1)):
+        for n, s in zip(t.shape[:-1], t.stride()):
+            if n > 1 and s:
+                a, b = span.get(s * t.element_size(), (0, 0))
+                span[s * t.element_size()] = (a, b + n - 1) if sign > 0 else (a - n + 1, b)
+    # a row of x starts less than a row of x before, or of y behind, the start of one of y
+    rx, ry = x.shape[-1] * x.element_size(), y.shape[-1] * y.element_size()
+    return _reaches([(s, *r) for s, r in sorted(span.items(), reverse=True)], ya - xa - rx, ya - xa + ry)
+
+
 @dataclass
 class SharedConfig:
     num_seqs: int
@@ -109,6 +143,8 @@ class SharedPrefixCache:
             self.prefix_lens = own(prefix_lens, "prefix_lens", (G,), i32)
             self.prefix_of = own(prefix_of, "prefix_of", (S,), i32)
         self.status = torch.zeros(2, dtype=i32, device=dev)
+        self._buffers = [x for x in (self.k, self.v, self.pos, self.weight, self.lens, self.next_pos, self.prefix_k,
+                                     self.prefix_v, self.prefix_lens, self.prefix_of, self.status) if x is not None]
 
         c = _Cache(cfg.dtype, d, S, cfg.num_heads, Hk, cap, G, cfg.prefix_capacity if G else 0)
         c.k, c.v = self.k.data_ptr(), self.v.data_ptr()
@@ -198,7 +234,8 @@ class SharedPrefixCache:
         q [S, H, T, d] over the sequence's prompt and own tokens, query t
         seeing the own slots before len - T + t + 1.  Returns (out
         [S, H, T, d], lse float32 [S, H, T]); a query that sees nothing gets
-        zeros and -inf.  accumulate adds to `weight` the softmax weights each
+        zeros and -inf.  out and lse, where given, share no memory with q, each
+        other or the cache.  accumulate adds to `weight` the softmax weights each
         own token received.  scale of the logits: 1 / sqrt(d) by default."""
         qs = self._tensor(q, "q", self.cfg.num_heads)
         accumulate = bool(accumulate)
@@ -215,9 +252,16 @@ class SharedPrefixCache:
             self._tensor(out, "out", self.cfg.num_heads)
             if out.shape != q.shape or 0 in out.stride() or out.data_ptr() == q.data_ptr():
                 raise ValueError("out: expected q's shape, no repeated rows, and not q itself")
+            for x in (q, *self._buffers):
+                if _overlap(out, x):
+                    raise ValueError("out: overlaps q or a buffer of the cache")
         if lse is not None and (lse.dtype != torch.float32 or lse.device != self.device or
                                 lse.shape != q.shape[:3] or not lse.is_contiguous()):
             raise ValueError("lse: expected a contiguous float32 [S, H, T] tensor on the device")
+        if lse is not None:
+            for x in (q, *self._buffers) if out is None else (q, out, *self._buffers):
+                if _overlap(lse, x):
+                    raise ValueError("lse: overlaps q, out or a buffer of the cache")
 
         if stream is None and _current_device() == self._index:
             return self._attend(q, qs, out, lse, plan, scale, _current_stream(self._index))

@@ -83,3 +83,28 @@ def test_evict_many_heads_of_many_moves(dtype, cap):
     evict_both(c, b, 0, 1)
     assert torch.equal(c.lens[7].cpu(), b[7].int())
     evict_both(c, b // 2, 5, 3)
+
+
+def test_outputs_in_memory_of_inputs_are_refused():
+    """out or lse sharing bytes with q, each other or the cache; slices beside
+    q's in one tensor are fine."""
+    S, H, Hk, T, d, n = 3, 4, 2, 2, 64, 40
+    c, q0 = make("bf16", S=S, H=H, Hk=Hk, T=T, d=d, cap=n, lens=n)
+    want, wl = c.attend(q0, accumulate=False)
+    wide = torch.zeros(S, T, H, 3 * d, dtype=torch.bfloat16, device=DEV)
+    q, out = wide[..., d:2 * d].transpose(1, 2), wide[..., 2 * d:].transpose(1, 2)
+    q.copy_(q0)
+    got, lse = c.attend(q, out=out, accumulate=False)
+    assert got is out and torch.equal(out, want) and torch.equal(lse, wl)
+    before = [x.clone() for x in c._buffers]
+    k = c.k.view(-1)[:S * H * T * d].view(S, H, T, d)
+    bad = [dict(out=wide[..., d + 8:2 * d + 8].transpose(1, 2)), dict(out=k),
+           dict(out=c.prefix_v.view(-1)[-S * H * T * d:].view(S, H, T, d)),
+           dict(lse=c.weight.view(-1)[:S * H * T].view(S, H, T)),
+           dict(out=out, lse=wide.view(torch.float32).view(-1)[-S * H * T:].view(S, H, T)),
+           dict(lse=wide.view(torch.float32).view(-1)[d // 2:d // 2 + S * H * T].view(S, H, T))]
+    for kw in bad:
+        with pytest.raises(ValueError, match="overlaps"):
+            c.attend(q, accumulate=False, **kw)
+    for x, y in zip(before, c._buffers):
+        assert torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
