@@ -98,6 +98,8 @@ class SharedPrefixCache:
     unless given) and must be ordered when they write the same buffers.
     Scratch is allocated per call from the stream's memory pool, so calls on
     several streams and captured graphs never share it.
+    No call has a gradient: a tensor that asks for one is refused where
+    gradients are recorded (detach it, or call under torch.no_grad()).
     """
 
     def __init__(self, cfg: SharedConfig, device=None, *, k=None, v=None, pos=None, weight=None, lens=None,
@@ -120,6 +122,8 @@ class SharedPrefixCache:
                 return torch.zeros(shape, dtype=dtype, device=dev)
             if not isinstance(x, torch.Tensor) or x.device != dev or x.dtype != dtype or tuple(x.shape) != shape:
                 raise ValueError(f"{name}: expected a {dtype} tensor {list(shape)} on {dev}")
+            if x.requires_grad:
+                self._no_grad(name)
             if rows:
                 self._rows(x, name)
             elif not x.is_contiguous():
@@ -181,10 +185,16 @@ class SharedPrefixCache:
             n0, n1, _, n3 = x.shape
             c = self.cfg
             if n0 == c.num_seqs and n1 == heads and n3 == c.head_dim and x.device == self.device:
+                if x.requires_grad:
+                    self._no_grad(name)
                 return self._rows(x, name)
         c = self.cfg
         raise ValueError(f"{name}: expected a {c.torch_dtype} tensor [{c.num_seqs}, {heads}, T, {c.head_dim}] on "
                          f"{self.device}")
+
+    def _no_grad(self, name):
+        if torch.is_grad_enabled():
+            raise ValueError(f"{name}: asks for a gradient, which the cache's calls do not have")
 
     @contextmanager
     def _on(self, stream):
@@ -218,6 +228,8 @@ class SharedPrefixCache:
                                      weight_t.shape != (c.num_seqs, c.num_kv_heads, T) or
                                      not weight_t.is_contiguous()):
             raise ValueError("weight_t: expected a contiguous float32 [S, Hkv, T] tensor on the device")
+        if weight_t is not None and weight_t.requires_grad:
+            self._no_grad("weight_t")
         if T == 0:
             return
         w = None if weight_t is None else weight_t.data_ptr()

@@ -108,3 +108,29 @@ def test_outputs_in_memory_of_inputs_are_refused():
             c.attend(q, accumulate=False, **kw)
     for x, y in zip(before, c._buffers):
         assert torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_inputs_that_ask_for_a_gradient_are_refused(dtype):
+    c, q = make(dtype, S=2, H=4, Hk=2, T=2, cap=20, lens=10)
+    kt = torch.randn(2, 2, 2, 64, device=DEV).to(q.dtype)
+    wt = torch.rand(2, 2, 2, device=DEV)
+    lens = c.lens.clone()
+    with pytest.raises(ValueError, match="q: .*gradient"):
+        c.attend(q.clone().requires_grad_())
+    with pytest.raises(ValueError, match="k_t: .*gradient"):
+        c.append(kt.clone().requires_grad_(), kt)
+    with pytest.raises(ValueError, match="v_t: .*gradient"):
+        c.append(kt, kt.clone().requires_grad_() * 2)
+    with pytest.raises(ValueError, match="weight_t: .*gradient"):
+        c.append(kt, kt, wt.clone().requires_grad_())
+    with pytest.raises(ValueError, match="out: .*gradient"):
+        c.attend(q, out=torch.empty_like(q).requires_grad_())
+    with pytest.raises(ValueError, match="prefix_v: .*gradient"):
+        hkv.SharedPrefixCache(c.cfg, DEV, prefix_v=c.prefix_v.clone().requires_grad_())
+    assert torch.equal(c.lens, lens)
+    want, _ = c.attend(q, accumulate=False)
+    with torch.no_grad():
+        got, _ = c.attend(q.clone().requires_grad_(), accumulate=False)
+        c.append(kt.clone().requires_grad_(), kt, wt.clone().requires_grad_())
+    assert torch.equal(got, want) and not got.requires_grad
