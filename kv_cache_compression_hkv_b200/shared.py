@@ -27,6 +27,9 @@ class _Cache(C.Structure):
         ("status", C.c_void_p)]
 
 
+#: Attributes that the C descriptor points into.
+_BUFFERS = frozenset(("k", "v", "pos", "weight", "lens", "next_pos", "prefix_k", "prefix_v", "prefix_lens", "prefix_of",
+                      "status"))
 _Strides = C.c_int64 * 3
 _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
@@ -87,7 +90,8 @@ class SharedPrefixCache:
 
     The buffers are ordinary tensors, allocated here or given by the caller
     (any strides with unit stride in d and 16-byte rows for the four row
-    buffers), and may be read and written between calls:
+    buffers), and may be read and written in place between calls; the cache
+    stays bound to them, so that none can be replaced by another:
       k, v                [S, Hkv, capacity, d]       own rows
       pos, weight         [S, Hkv, capacity]          int32, float32
       lens, next_pos      [S, Hkv]                    int32
@@ -139,16 +143,16 @@ class SharedPrefixCache:
         self.weight = own(weight, "weight", (S, Hk, cap), f32)
         self.lens = own(lens, "lens", (S, Hk), i32)
         self.next_pos = own(next_pos, "next_pos", (S, Hk), i32)
-        self.prefix_k = self.prefix_v = self.prefix_lens = self.prefix_of = None
-        if G:
+        if not G:
+            self.prefix_k = self.prefix_v = self.prefix_lens = self.prefix_of = None
+        else:
             P = cfg.prefix_capacity
             self.prefix_k = own(prefix_k, "prefix_k", (G, Hk, P, d), dt, True)
             self.prefix_v = own(prefix_v, "prefix_v", (G, Hk, P, d), dt, True)
             self.prefix_lens = own(prefix_lens, "prefix_lens", (G,), i32)
             self.prefix_of = own(prefix_of, "prefix_of", (S,), i32)
         self.status = torch.zeros(2, dtype=i32, device=dev)
-        self._buffers = [x for x in (self.k, self.v, self.pos, self.weight, self.lens, self.next_pos, self.prefix_k,
-                                     self.prefix_v, self.prefix_lens, self.prefix_of, self.status) if x is not None]
+        self._buffers = [x for x in (getattr(self, n) for n in sorted(_BUFFERS)) if x is not None]
 
         c = _Cache(cfg.dtype, d, S, cfg.num_heads, Hk, cap, G, cfg.prefix_capacity if G else 0)
         c.k, c.v = self.k.data_ptr(), self.v.data_ptr()
@@ -170,6 +174,11 @@ class SharedPrefixCache:
         self._plans = {}  # (T, accumulate) -> see _plan
         L = lib()
         self._append_fn, self._attend_fn, self._evict_fn = L.hkv_shared_append, L.hkv_shared_attend, L.hkv_shared_evict
+
+    def __setattr__(self, name, value):
+        if name in _BUFFERS and self.__dict__.get(name, value) is not value:
+            raise AttributeError(f"{name}: the cache stays bound to this buffer; write into it, or make another cache")
+        super().__setattr__(name, value)
 
     # -- argument checks (each a few hundred nanoseconds: a decode step's calls
     #    take the GPU ten to twenty microseconds) ------------------------------

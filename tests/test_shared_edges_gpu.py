@@ -134,3 +134,20 @@ def test_inputs_that_ask_for_a_gradient_are_refused(dtype):
         got, _ = c.attend(q.clone().requires_grad_(), accumulate=False)
         c.append(kt.clone().requires_grad_(), kt, wt.clone().requires_grad_())
     assert torch.equal(got, want) and not got.requires_grad
+
+
+@pytest.mark.parametrize("G", [0, 2])
+def test_buffers_cannot_be_replaced(G):
+    """The calls go on using the buffers the cache was made over: assigning
+    another tensor to the attribute says so.  In place is fine."""
+    c, q = make("bf16", S=2, H=4, Hk=2, cap=20, G=G, lens=10)
+    for name in ("k", "v", "pos", "weight", "lens", "next_pos", "status") + ("prefix_k", "prefix_v", "prefix_lens",
+                                                                             "prefix_of"):
+        x = getattr(c, name)
+        with pytest.raises(AttributeError, match=name):
+            setattr(c, name, torch.zeros(1, device=DEV) if x is None else x.clone())
+        assert getattr(c, name) is x
+    c.weight *= 2
+    c.lens += 1
+    c.lens = c.lens
+    c.attend(q)
