@@ -176,7 +176,7 @@ class SharedPrefixCache:
         self._append_fn, self._attend_fn, self._evict_fn = L.hkv_shared_append, L.hkv_shared_attend, L.hkv_shared_evict
 
     def __setattr__(self, name, value):
-        if name in _BUFFERS and self.__dict__.get(name, value) is not value:
+        if name in _BUFFERS and getattr(self, name, value) is not value:
             raise AttributeError(f"{name}: the cache stays bound to this buffer; write into it, or make another cache")
         super().__setattr__(name, value)
 
