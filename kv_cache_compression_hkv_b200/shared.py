@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 from contextlib import contextmanager
-from dataclasses import dataclass
+from dataclasses import dataclass, replace
 
 import torch
 
@@ -108,7 +108,7 @@ class SharedPrefixCache:
 
     def __init__(self, cfg: SharedConfig, device=None, *, k=None, v=None, pos=None, weight=None, lens=None,
                  next_pos=None, prefix_k=None, prefix_v=None, prefix_lens=None, prefix_of=None):
-        self.cfg = cfg
+        self.cfg = cfg = replace(cfg)  # (the caller's may change, and serve another cache)
         dev = torch.device(device if device is not None else "cuda")
         if dev.type != "cuda":
             raise ValueError(f"device: expected a CUDA device, got {dev}")
@@ -119,6 +119,8 @@ class SharedPrefixCache:
         if cfg.dtype not in (DTYPE_F32, DTYPE_BF16) or d not in (64, 128) or S < 1 or Hk < 1 or \
                 cfg.num_heads < 1 or cfg.num_heads % Hk or cap < 1 or G < 0 or (G > 0 and cfg.prefix_capacity < 1):
             raise ValueError(f"unusable config {cfg}")
+        # the sizes that the descriptor is made of, and that calls are checked against
+        self._S, self._H, self._Hk, self._d, self._cap = S, cfg.num_heads, Hk, d, cap
         dt = cfg.torch_dtype
 
         def own(x, name, shape, dtype, rows=False):
@@ -192,14 +194,11 @@ class SharedPrefixCache:
         """Checks a [S, heads, T, d] tensor; its strides for the C call."""
         if isinstance(x, torch.Tensor) and x.dtype == self._dtype and x.dim() == 4:
             n0, n1, _, n3 = x.shape
-            c = self.cfg
-            if n0 == c.num_seqs and n1 == heads and n3 == c.head_dim and x.device == self.device:
+            if n0 == self._S and n1 == heads and n3 == self._d and x.device == self.device:
                 if x.requires_grad:
                     self._no_grad(name)
                 return self._rows(x, name)
-        c = self.cfg
-        raise ValueError(f"{name}: expected a {c.torch_dtype} tensor [{c.num_seqs}, {heads}, T, {c.head_dim}] on "
-                         f"{self.device}")
+        raise ValueError(f"{name}: expected a {self._dtype} tensor [{self._S}, {heads}, T, {self._d}] on {self.device}")
 
     def _no_grad(self, name):
         if torch.is_grad_enabled():
@@ -227,14 +226,13 @@ class SharedPrefixCache:
         [S, Hkv, T] fp32, their accumulated weights (default 0); none of them
         views of the cache.  A head without T free slots is left as it was
         (see check)."""
-        c = self.cfg
-        ks = self._tensor(k_t, "k_t", c.num_kv_heads)
-        vs = self._tensor(v_t, "v_t", c.num_kv_heads)
+        ks = self._tensor(k_t, "k_t", self._Hk)
+        vs = self._tensor(v_t, "v_t", self._Hk)
         T = k_t.shape[2]
-        if v_t.shape[2] != T or T > c.capacity:
+        if v_t.shape[2] != T or T > self._cap:
             raise ValueError("k_t, v_t: as many tokens each, at most the capacity")
         if weight_t is not None and (weight_t.dtype != torch.float32 or weight_t.device != self.device or
-                                     weight_t.shape != (c.num_seqs, c.num_kv_heads, T) or
+                                     weight_t.shape != (self._S, self._Hk, T) or
                                      not weight_t.is_contiguous()):
             raise ValueError("weight_t: expected a contiguous float32 [S, Hkv, T] tensor on the device")
         if weight_t is not None and weight_t.requires_grad:
@@ -258,7 +256,7 @@ class SharedPrefixCache:
         zeros and -inf.  out and lse, where given, share no memory with q, each
         other or the cache.  accumulate adds to `weight` the softmax weights each
         own token received.  scale of the logits: 1 / sqrt(d) by default."""
-        qs = self._tensor(q, "q", self.cfg.num_heads)
+        qs = self._tensor(q, "q", self._H)
         accumulate = bool(accumulate)
         plan = self._plans.get((q.shape[2], accumulate))
         if plan is None:
@@ -270,7 +268,7 @@ class SharedPrefixCache:
         elif not (scale != 0 and abs(scale) < float("inf")):
             raise ValueError("scale: a finite number other than 0")
         if out is not None:
-            self._tensor(out, "out", self.cfg.num_heads)
+            self._tensor(out, "out", self._H)
             if out.shape != q.shape or 0 in out.stride() or out.data_ptr() == q.data_ptr():
                 raise ValueError("out: expected q's shape, no repeated rows, and not q itself")
             for x in (q, *self._buffers):
@@ -310,12 +308,11 @@ class SharedPrefixCache:
     def _plan(self, T, accumulate):
         """What a call of these sizes needs: kept, as it depends on nothing
         else.  (empty_like of an expanded element is the cheapest allocation.)"""
-        c = self.cfg
-        if T < 1 or T > c.capacity:
+        if T < 1 or T > self._cap:
             raise ValueError("q: between 1 token and the capacity")
         acc, n = int(accumulate), C.c_size_t()
         _check(lib().hkv_shared_attend_bytes(self._ref, T, acc, C.byref(n)), "hkv_shared_attend_bytes")
-        plan = (T, acc, n.value, self.weight.new_empty(1).expand(c.num_seqs, c.num_heads, T),
+        plan = (T, acc, n.value, self.weight.new_empty(1).expand(self._S, self._H, T),
                 self.lens.new_empty(1).expand(n.value // 4))
         self._plans[(T, accumulate)] = plan
         return plan
@@ -326,9 +323,8 @@ class SharedPrefixCache:
         (recent, weight, position, slot) go, `recent` being those less than
         that many positions behind the newest; survivors behind the budget
         move into the holes before it."""
-        c = self.cfg
         if not isinstance(budgets, torch.Tensor) or budgets.dtype != torch.int32 or budgets.device != self.device or \
-                budgets.shape != (c.num_seqs, c.num_kv_heads) or not budgets.is_contiguous():
+                budgets.shape != (self._S, self._Hk) or not budgets.is_contiguous():
             raise ValueError("budgets: expected a contiguous int32 [S, Hkv] tensor on the device")
         if not (0 <= recent < 1 << 31 and 1 <= slack < 1 << 31):
             raise ValueError("recent at least 0, slack at least 1, both below 2**31")

@@ -151,3 +151,25 @@ def test_buffers_cannot_be_replaced(G):
     c.lens += 1
     c.lens = c.lens
     c.attend(q)
+
+
+def test_a_config_may_change_behind_the_cache():
+    """Sizes are checked against those the cache was made with, whatever becomes
+    of the config it was given and of the one it shows."""
+    cfg = hkv.SharedConfig(3, 4, 2, 64, 20)
+    c = hkv.SharedPrefixCache(cfg, DEV)
+    c.lens.fill_(5)
+    c.k.normal_()
+    c.v.normal_()
+    q = torch.randn(3, 4, 2, 64, device=DEV).bfloat16()
+    want, _ = c.attend(q, accumulate=False)
+    for shown in (cfg, c.cfg):
+        shown.num_seqs, shown.num_heads, shown.num_kv_heads, shown.capacity = 1, 2, 1, 4
+        assert shown is cfg and c.cfg.num_seqs == 3 or shown is c.cfg
+        with pytest.raises(ValueError):
+            c.attend(q[:1, :2].contiguous())
+        with pytest.raises(ValueError):
+            c.append(c.k[:1, :1, :2].clone(), c.v[:1, :1, :2].clone())
+        with pytest.raises(ValueError):
+            c.evict(torch.zeros(1, 1, dtype=torch.int32, device=DEV))
+        assert torch.equal(c.attend(q, accumulate=False)[0], want)
