@@ -357,7 +357,8 @@ HKV_API hkv_status hkv_shared_attend_bytes(const hkv_shared_cache* cache, int32_
                                            int32_t accumulate, size_t* bytes);
 
 /* Attention of each sequence's newest num_queries = T tokens (already
- * appended) over its prefix and its own tokens, in one softmax.  Query t
+ * appended, and not evicted from since: the newest are taken to be the last T
+ * slots) over its prefix and its own tokens, in one softmax.  Query t
  * sees the whole prefix and the own slots before len - T + t + 1 (all the
  * earlier ones whatever an eviction did to their order, and the new ones up
  * to itself).  A query that sees nothing gets zeros and lse = -inf.

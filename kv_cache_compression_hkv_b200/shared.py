@@ -249,7 +249,8 @@ class SharedPrefixCache:
             _check(code, "hkv_shared_append")
 
     def attend(self, q, out=None, lse=None, accumulate=True, scale=None, stream=None):
-        """Attention of each sequence's newest T tokens (appended before):
+        """Attention of each sequence's newest T tokens (appended before, with
+        no eviction in between: it moves tokens to other slots):
         q [S, H, T, d] over the sequence's prompt and own tokens, query t
         seeing the own slots before len - T + t + 1.  Returns (out
         [S, H, T, d], lse float32 [S, H, T]); a query that sees nothing gets

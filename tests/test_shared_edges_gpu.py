@@ -7,7 +7,8 @@ import torch
 
 import kv_cache_compression_hkv_b200 as hkv
 
-from test_shared_gpu import DEV, evict_both, make
+import shared_oracle as O
+from test_shared_gpu import DEV, check, evict_both, make, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -173,3 +174,26 @@ def test_a_config_may_change_behind_the_cache():
         with pytest.raises(ValueError):
             c.evict(torch.zeros(1, 1, dtype=torch.int32, device=DEV))
         assert torch.equal(c.attend(q, accumulate=False)[0], want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [3, 40, 150])
+def test_prompts_are_filled_by_a_cache_over_them(dtype, T):
+    """The prompts' prefill through a cache whose own buffers they are, the
+    shorter one padded, and then sequences that continue them."""
+    S, H, Hk, d, P = 4, 4, 2, 64, 160
+    g = torch.Generator().manual_seed(T)
+    c, q = make(dtype, S=S, H=H, Hk=Hk, d=d, T=2, cap=30, G=2, P=P, plens=[0, 0], lens=20, seed=T)
+    prompts = hkv.SharedPrefixCache(hkv.SharedConfig(2, H, Hk, d, P, dtype=c.cfg.dtype), DEV, k=c.prefix_k, v=c.prefix_v)
+    kt, vt, qt = rows(g, dtype, 2, Hk, T, d), rows(g, dtype, 2, Hk, T, d), rows(g, dtype, 2, H, T, d)
+    prompts.append(kt, vt)
+    out, lse = prompts.attend(qt, accumulate=False)
+    lens = [T, T // 2]
+    c.prefix_lens.copy_(torch.tensor(lens))
+    for i, n in enumerate(lens):
+        o, e, _, bo, be, _ = O.attend(qt[i:i + 1, :, :n].cpu(), kt[i:i + 1].cpu(), vt[i:i + 1].cpu(),
+                                      torch.full((1, Hk), n), None, None, None, None)
+        O.assert_within(out[i:i + 1, :, :n], o, bo, "out")
+        O.assert_within(lse[i:i + 1, :, :n], e, be, "lse")
+    assert torch.equal(c.prefix_k[:, :, :T], kt) and torch.equal(c.prefix_v[:, :, :T], vt)
+    check(c, q)
