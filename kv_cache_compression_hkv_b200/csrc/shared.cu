@@ -83,7 +83,7 @@ cudaError_t launch_append(const View& a, int dtype, int d, const void* k_t, cons
                           const int64_t* vs, const float* w_t, cudaStream_t st) {
     const int heads = a.S * a.Hk, n_new = a.T;
     int slices = 1;
-    while (heads * slices < 592 && n_new / slices > 64) slices *= 2;
+    while (heads * slices < 4 * SMS && n_new / slices > 64) slices *= 2;
     auto go = [&](auto tag, auto dim) {
         using E = decltype(tag);
         constexpr int D = decltype(dim)::value;

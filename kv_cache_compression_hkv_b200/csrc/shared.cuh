@@ -14,6 +14,7 @@
 namespace hkv {
 namespace shared {
 
+constexpr int SMS = 148;         // of the GPU
 constexpr int KEY_STEP = 64;     // key ranges start at multiples of this
 constexpr int MAX_SPLITS = 64;   // splits of the own keys, and of the prefix keys
 constexpr int MAX_PREFIXES = 1024;

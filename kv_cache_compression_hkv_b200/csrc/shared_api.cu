@@ -8,6 +8,7 @@
 #include "kernels.h"
 #include "shared.cuh"
 
+using hkv::shared::SMS;
 using hkv::shared::View;
 
 namespace {
@@ -96,6 +97,16 @@ struct Plan {
 // 30.8, 67 MB; 640 heads, d = 64, over 300: 32.0 / 24.2, 98 MB).
 constexpr int64_t FOLD_BYTES = 128 << 20;
 
+// Row tiles from which on their keys are not cut, so that no joining follows.
+// (us, whole / two pieces.  bf16, one tile of 49 rows a block: 84 blocks over 590 keys
+// 19.8 / 25.7, over 16000 343 / 294; 104 blocks 20.2 / 26.8, 362 / 349; 120 over 16000
+// 370 / 393; two tiles a block over up to 1280 keys: 60 blocks 40.7 / 45.1, 80 41.2 /
+// 50.9, 120 42.4 / 71.0, 160 44.6 / 87.2; over up to 4352: 96 121 / 107, 128 123 / 122.
+// fp32, 32 rows a block: 180 over 233 keys 49.1 / 48.7, over 2033 286 / 217; 240 52.5 /
+// 58.2, 308 / 270; 300 58.5 / 63.2, 369 / 364; of 16 rows: 200 over 2033 185 / 104, 400
+// over 233 34.2 / 41.1.)
+constexpr int64_t UNCUT = 100, UNCUT_F32 = 240;
+
 Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char* base) {
     a.T = T;
     const int64_t rps = (int64_t)a.rep * T, R = (int64_t)a.S * a.H * T, heads = (int64_t)a.S * a.Hk;
@@ -118,18 +129,18 @@ Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char
     if (p.umma_rows) {
         const int nt = hkv::shared::umma_row_tiles(rps);
         const int64_t items = heads * ((rps + 128 * nt - 1) / (128 * nt));
-        a.no = items >= 148 ? 1 : splits(nt == 2 ? 148 : 296, items, keys, 256);
+        a.no = items >= UNCUT ? 1 : splits(SMS * (nt == 2 ? 1 : 2), items, keys, 256);
     } else if (p.stream) {
         // eight warps fit an SM: a head goes to as many as fill the GPU, one or
         // several blocks of four (one warp / a block a head: 1024 heads of 28 to
         // 138 tokens 12.8 / 18.5 us, 512 of 56 to 477 22.6 / 17.0)
-        const int64_t warps = (148 * 8 + heads / 2) / heads, most = (keys + 31) / 32;
+        const int64_t warps = (SMS * 8 + heads / 2) / heads, most = (keys + 31) / 32;
         const int64_t n = warps < most ? warps : most;
         p.warps_per_head = n > 1 ? 4 : 1;
         a.no = splits((n + 2) / 4, 1, keys, 64);
     } else {
         const int64_t items = heads * (few ? 1 : (rps + 31) / 32);
-        a.no = items >= 148 ? 1 : splits(148 * (few ? 4 : 2), items, keys, 128);
+        a.no = items >= UNCUT_F32 ? 1 : splits(SMS * (few ? 4 : 2), items, keys, 128);
     }
     a.np = 0;
     if (!fold) {
@@ -139,7 +150,7 @@ Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char
         // 16384 shared keys: 65.4 us in 192 blocks, 69.2 in 304, 67.9 in 144)
         const int64_t items = a.Hk * (tiles > groups ? tiles : groups);
         a.np = bf16 ? splits(items > 200 ? 1 : 200 / items, 1, a.pcap, 128)
-                    : splits(148 * 6, a.Hk * (a.S * rps / 16 + 1), a.pcap, 128);
+                    : splits(SMS * 6, a.Hk * (a.S * rps / 16 + 1), a.pcap, 128);
     }
     size_t o = 0;
     auto take = [&](size_t bytes) {

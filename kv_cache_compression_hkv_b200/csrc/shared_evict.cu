@@ -360,14 +360,14 @@ cudaError_t launch_evict(const View& a, int dtype, int d, const int32_t* budget,
     int2* counts = reinterpret_cast<int2*>(scratch);
     int32_t* lists = reinterpret_cast<int32_t*>(scratch + ((size_t)heads * 8 + 255) / 256 * 256);
     const size_t held = held_bytes(a.cap);
-    if (a.cap <= (heads > 148 ? SHORT_CAP : SHORT_CAP / 2))
+    if (a.cap <= (heads > SMS ? SHORT_CAP : SHORT_CAP / 2))
         return launch(select_kernel<128, true>, heads, 128, held, st, a, budget, recent, slack, row, es, 1, lists, counts);
     const cudaError_t e =
         a.cap <= HELD_CAP
             ? launch(select_kernel<1024, true>, heads, 1024, held, st, a, budget, recent, slack, row, es, 0, lists, counts)
             : launch(select_kernel<1024, false>, heads, 1024, 0, st, a, budget, recent, slack, row, es, 0, lists, counts);
     if (e != cudaSuccess) return e;
-    const int parts = std::max(1, (148 * 8 + heads - 1) / heads);
+    const int parts = std::max(1, (SMS * 8 + heads - 1) / heads);
     return launch(move_kernel, (int64_t)heads * parts, 256, 0, st, a, parts, row, es, lists, counts);
 }
 
