@@ -154,11 +154,6 @@ __device__ __forceinline__ void dots(float (&x)[RW][KPL], const float (*q)[KP], 
     }
 }
 
-__device__ __forceinline__ void cp16(void* dst, const void* src, bool on) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
-                 : "memory");
-}
-
 // One block per (tile of RT rows, keys): first the prefixes' tiles, whose rows
 // come from all their sequences (np > 0), then tiles of one (sequence, KV
 // head) over a piece of its list of keys.  The next step's keys are on their
@@ -231,8 +226,8 @@ __global__ void __launch_bounds__(C::THREADS, 4) attend_f32_kernel(const __grid_
                 const int idx = e * THREADS + tid, r = idx / (D / 4), c = idx % (D / 4) * 4;
                 const bool on = k0 + r < hi;
                 const int64_t key = on ? k0 + r : k0;
-                cp16(&sm.k[st % ST][r][c], kp + key * kst + c, on);
-                cp16(&sm.v[st % ST][r][c], vp + key * vst + c, on);
+                cp16(ptx::smem_u32(&sm.k[st % ST][r][c]), kp + key * kst + c, on);
+                cp16(ptx::smem_u32(&sm.v[st % ST][r][c]), vp + key * vst + c, on);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -383,16 +378,7 @@ __global__ void __launch_bounds__(C::THREADS, 4) attend_f32_kernel(const __grid_
     }
     if (!final || !keep) return;
     __syncthreads();
-    const float* lg = a.logit + (int64_t)(s * a.Hk + hk) * rps * a.lcap;
-    float* w = a.weight + (int64_t)(s * a.Hk + hk) * a.cap;
-    for (int j = tid; j < n_own; j += THREADS) {
-        float sum = 0.f;
-        for (int i = 0; i < rps; ++i) {
-            const float2 y = sm.ml[i];
-            if (y.x != -INFINITY) sum += exp2f(lg[(int64_t)i * a.lcap + j] - y.x) * y.y;
-        }
-        w[j] += sum;
-    }
+    add_kept(a, s * a.Hk + hk, n_own, sm.ml, tid, THREADS);
 }
 
 // ---------------------------------------------------------------------------
@@ -584,7 +570,7 @@ __global__ void __launch_bounds__(C::THREADS, 4) column_sums_f32_kernel(const __
     const float* kb = static_cast<const float*>(a.k) + s * a.ks[0] + hk * a.ks[1];
     for (int e = tid; e < KT * (D / 4); e += THREADS) {
         const int r = e / (D / 4), c = e % (D / 4) * 4;
-        cp16(&sm.k[r][c], kb + (int64_t)(k0 + r < n ? k0 + r : k0) * a.ks[2] + c, k0 + r < n);
+        cp16(ptx::smem_u32(&sm.k[r][c]), kb + (int64_t)(k0 + r < n ? k0 + r : k0) * a.ks[2] + c, k0 + r < n);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     // the first row that sees key k0: n - T + t + 1 > k0

@@ -138,6 +138,11 @@ __device__ __forceinline__ int own_limit(const View& a, int n, int i) {
     return lim < 0 ? 0 : lim;
 }
 
+// 16 bytes from global to shared memory, asynchronously; zeros where not `on`.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+
 // Adds the weights 2^(x - M) / l of a head's kept logits to its accumulated
 // ones, rows in order: slots k0, k0 + step, ..., four at once.  ml: the rows' (M, 1 / l).
 __device__ __forceinline__ void add_kept(const View& a, int sh, int n, const float2* ml, int k0, int step) {
@@ -275,11 +280,6 @@ cudaError_t launch(void (*kernel)(P...), int64_t blocks, int threads, size_t sme
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
-
-// Tensor map of bf16 rows [n2][n1][n0] of d elements at strides st (elements:
-// outermost, middle, row): boxes of 64 columns x box rows, 128-byte swizzle,
-// zeros past the ends.
-bool make_map(CUtensorMap* m, const void* ptr, int d, int n0, int n1, int n2, const int64_t* st, int box);
 
 // launchers (host)
 cudaError_t prepare_shared_umma();

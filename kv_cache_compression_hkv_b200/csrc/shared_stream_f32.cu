@@ -35,10 +35,6 @@ constexpr int NK = 8;  // rows of K and V of a step that a lane holds parts of
 constexpr int SN = 3;  // stages of a warp
 constexpr int STAGE = 2 * NK * 512;
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-
 // v[i]: this lane's part of key i's product.  Returns the whole product of key
 // (lane % LPK) / (LPK / NK), summed over the LPK lanes that share the keys.
 template <int LPK> __device__ __forceinline__ float butterfly(float (&v)[NK], int lane) {

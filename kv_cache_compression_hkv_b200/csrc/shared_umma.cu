@@ -841,9 +841,10 @@ static EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// bf16 rows [n2][n1][n0] of d elements at strides st (elements: outermost,
-// middle, row); boxes of 64 columns x box rows, 128-byte swizzle.
-bool make_map(CUtensorMap* m, const void* ptr, int d, int n0, int n1, int n2, const int64_t* st, int box) {
+// Tensor map of bf16 rows [n2][n1][n0] of d elements at strides st (elements:
+// outermost, middle, row): boxes of 64 columns x box rows, 128-byte swizzle,
+// zeros past the ends.
+static bool make_map(CUtensorMap* m, const void* ptr, int d, int n0, int n1, int n2, const int64_t* st, int box) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     // a dimension of one element may come with any stride: give it a lawful one
