@@ -22,7 +22,7 @@ constexpr int MAX_PREFIXES = 1024;
 // queries) are streamed once with every row's logits kept for the accumulated
 // weights, bf16 as one M side of mma.sync; more rows go to the tcgen05 tiles and
 // recompute the logits.  (16 rows, d = 128, streamed / tiles: 12 heads of 9000 to
-// 32001 slots 39.6 / 112 us, 512 heads of 56 to 477 34.5 / 38.5 us.)
+// 32001 slots 45.5 / 213 us, 512 heads of 56 to 477 37.6 / 42.8 us.)
 constexpr int STREAM_ROWS = 16;
 constexpr int STREAM_ROWS_F32 = 8;  // see shared_stream_f32.cu
 
@@ -241,8 +241,8 @@ inline int64_t max_prefix_tiles(int S, int G, int rows_per_seq, int rt) {
 // Row tiles of 128 that a tensor-core block takes.  With one, two blocks share
 // an SM and hide each other's beginnings and ends, and the block can sum its
 // keys' weights; with two, the row tiles share the copies of K and V.  (d = 128,
-// with the weights, one / two: 512 heads of 256 rows 59.9 / 80.3 us, 256 heads of
-// 512 rows 77 / 90; 128 heads of 1024 110 / 110; 16 heads of 16004 580 / 567.)
+// with the weights, one / two: 512 heads of 256 rows 64.1 / 81.9 us, 256 heads of
+// 512 rows 80 / 88; 128 heads of 1024 110 / 111; 16 heads of 16004 679 / 649.)
 constexpr int ONE_TILE_ROWS = 512;
 inline int umma_row_tiles(int64_t rows_per_seq) { return rows_per_seq > ONE_TILE_ROWS ? 2 : 1; }
 

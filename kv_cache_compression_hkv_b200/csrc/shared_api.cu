@@ -91,8 +91,8 @@ struct Plan {
 
 // Bytes of prefix rows that all sequences together read up to which they are
 // folded.  (us, d = 128, folded / once: 1024 heads over 64, 192, 384 shared keys
-// 12.9 / 18.5, 17.9 / 19.4, 25.5 / 20.9, which is 34, 101, 201 MB; 128 heads of
-// four query heads over 1024, 2048: 16.0 / 19.3, 20.9 / 21.0, or 67, 134 MB.)
+// 13.9 / 20.4, 19.0 / 21.2, 26.5 / 23.0, which is 34, 101, 201 MB; 128 heads of
+// four query heads over 1024, 2048: 13.9 / 16.8, 19.2 / 18.4, or 67, 134 MB.)
 // fp32 up to half of that, as its rows cost arithmetic (1024 heads over 64: 23.9 /
 // 30.8, 67 MB; 640 heads, d = 64, over 300: 32.0 / 24.2, 98 MB).
 constexpr int64_t FOLD_BYTES = 128 << 20;
@@ -133,7 +133,7 @@ Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char
     } else if (p.stream) {
         // eight warps fit an SM: a head goes to as many as fill the GPU, one or
         // several blocks of four (one warp / a block a head: 1024 heads of 28 to
-        // 138 tokens 12.8 / 18.5 us, 512 of 56 to 477 22.6 / 17.0)
+        // 138 tokens 13.8 / 19.6 us, 512 of 56 to 477 24.5 / 18.4)
         const int64_t warps = (SMS * 8 + heads / 2) / heads, most = (keys + 31) / 32;
         const int64_t n = warps < most ? warps : most;
         p.warps_per_head = n > 1 ? 4 : 1;
@@ -147,7 +147,7 @@ Plan plan_attend(View& a, int dtype, int d, int T, int accumulate, unsigned char
         const int64_t tiles = (a.S * rps + 127) / 128, groups = a.G < a.S ? a.G : a.S;
         // two blocks of tiles fit an SM; a third of the places is left to the
         // streaming kernel's blocks, which need the other resource (48 sequences,
-        // 16384 shared keys: 65.4 us in 192 blocks, 69.2 in 304, 67.9 in 144)
+        // 16384 shared keys: 62.9 us in 192 blocks, 65.1 in 304, 65.4 in 144)
         const int64_t items = a.Hk * (tiles > groups ? tiles : groups);
         a.np = bf16 ? splits(items > 200 ? 1 : 200 / items, 1, a.pcap, 128)
                     : splits(SMS * 6, a.Hk * (a.S * rps / 16 + 1), a.pcap, 128);

@@ -10,9 +10,9 @@
 // of O += P V.  (A tcgen05 tile would compute 128 rows for these 16 and pass
 // the weights through TMEM; at 8 KB of keys and values a step the legacy
 // instruction takes a third of the time that HBM leaves for it.)
-// d = 128: 1024 heads of 28 to 138 own tokens and 64 shared ones 13.1 us, 512 of
-// 56 to 477 and 128 17.4 us; 12 heads of 8 rows over 9000 to 32001 22 us and 6 of
-// joining (126 MB, 5.7 TB/s while it streams).
+// d = 128: 1024 heads of 28 to 138 own tokens and 64 shared ones 12.8 us, 512 of
+// 56 to 477 and 128 17.0 us (15.4 and 20.3 with their rows in HBM); 12 heads of 8
+// rows over 9000 to 32001 30.3 us with the joining, 126 MB.
 #include <math.h>
 
 #include <type_traits>

@@ -22,11 +22,12 @@
 // so a softmax warp finds its next logits ready.  (With P over S's own place S of
 // tile j + 2 had to wait for the product of tile j behind the other row tile's.)
 //
-// d = 128: 16004 rows of 16 heads over 2834 keys on average 367 us (1.0 PFLOP/s; the products
-// of a key tile of two row tiles take 1330 of about 2000 cycles, the rest are the
-// softmax's exponentials and the hand-over), 512 heads of 256 rows over 384 keys
-// 58 us with the weights, 512 heads of 49 rows over 49 to 462 and 128 39 us: there
-// each block's beginning and end, two blocks an SM to hide them.
+// d = 128: 16004 rows of 16 heads over 2834 keys on average 457 us (0.81 PFLOP/s,
+// 1.22 with the second product of the weights: those products are most of it, the
+// rest the softmax's exponentials and the hand-over; 367 us with one product),
+// 512 heads of 256 rows over 384 keys 63 us with the weights, 512 heads of 49 rows
+// over 49 to 462 and 128 42 us: there each block's beginning and end, two blocks an
+// SM to hide them.
 #include <math.h>
 
 #include <type_traits>
@@ -681,7 +682,7 @@ template <int D> struct SumShape {
 // four warps take every other tile.  (With 64 queries a tile an MMA waits for
 // shared memory, which gives it the 128 keys again for every 64 queries: 408
 // cycles instead of 256.)  A row that is not to be counted has -lse2 = -inf.
-// 16004 rows of 16 heads, 4001 keys, d = 128: 212 us, of exponentials (16 a cycle
+// 16004 rows of 16 heads, 4001 keys, d = 128: 209 us, of exponentials (16 a cycle
 // an SM) as much as of products.
 template <int D>
 __global__ void __launch_bounds__(SumShape<D>::THREADS, 2)
