@@ -8,6 +8,7 @@ and decide what an eviction drops.  This module marshals arguments only.
 from __future__ import annotations
 
 import ctypes as C
+from bisect import bisect_right
 from contextlib import contextmanager
 from dataclasses import dataclass, replace
 
@@ -46,15 +47,23 @@ def _reaches(dims, lo, hi):
                for n in range(max(a, -((most - lo) // s)), min(b, (hi - least) // s) + 1))
 
 
+def _extent(x):
+    """The bytes from the first to the last of a tensor's elements."""
+    at, last = x.data_ptr(), 1
+    if x.is_contiguous():
+        return at, at + x.nbytes
+    for n, s in zip(x.shape, x.stride()):
+        if n == 0:
+            return at, at
+        last += (n - 1) * s
+    return at, at + last * x.element_size()
+
+
 def _overlap(x, y):
     """Whether two tensors hold a common byte.  Their last dimensions are
     contiguous rows of one dtype's elements; views that lie between each other's
     rows do not overlap."""
-    def extent(t):
-        return t.data_ptr(), t.data_ptr() + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
-    if not x.numel() or not y.numel():
-        return False
-    (xa, xb), (ya, yb) = extent(x), extent(y)
+    (xa, xb), (ya, yb) = _extent(x), _extent(y)
     if xb <= ya or yb <= xa:
         return False
     span = {}  # stride in bytes -> the range of index differences
@@ -155,6 +164,14 @@ class SharedPrefixCache:
             self.prefix_of = own(prefix_of, "prefix_of", (S,), i32)
         self.status = torch.zeros(2, dtype=i32, device=dev)
         self._buffers = [x for x in (getattr(self, n) for n in sorted(_BUFFERS)) if x is not None]
+        # their extents in ascending order, those that meet as one (see _apart)
+        self._starts, self._ends = [], []
+        for a, b in sorted(_extent(x) for x in self._buffers):
+            if self._ends and a < self._ends[-1]:
+                self._ends[-1] = max(self._ends[-1], b)
+            else:
+                self._starts.append(a)
+                self._ends.append(b)
 
         c = _Cache(cfg.dtype, d, S, cfg.num_heads, Hk, cap, G, cfg.prefix_capacity if G else 0)
         c.k, c.v = self.k.data_ptr(), self.v.data_ptr()
@@ -199,6 +216,22 @@ class SharedPrefixCache:
                     self._no_grad(name)
                 return self._rows(x, name)
         raise ValueError(f"{name}: expected a {self._dtype} tensor [{self._S}, {heads}, T, {self._d}] on {self.device}")
+
+    def _apart(self, q, out, lse):
+        """Refuses an out or lse that shares memory with q, each other or the
+        cache.  Their extents nearly always lie apart, which takes 2 us."""
+        seen = [(*_extent(q), q)]
+        for name, x in (("out", out), ("lse", lse)):
+            if x is None:
+                continue
+            a, b = _extent(x)
+            i = bisect_right(self._ends, a)  # the first extent that ends behind x's start
+            if i < len(self._starts) and self._starts[i] < b and any(_overlap(x, y) for y in self._buffers):
+                raise ValueError(f"{name}: overlaps a buffer of the cache")
+            for lo, hi, y in seen:
+                if a < hi and lo < b and _overlap(x, y):
+                    raise ValueError(f"{name}: overlaps q or out")
+            seen.append((a, b, x))
 
     def _no_grad(self, name):
         if torch.is_grad_enabled():
@@ -272,16 +305,11 @@ class SharedPrefixCache:
             self._tensor(out, "out", self._H)
             if out.shape != q.shape or 0 in out.stride() or out.data_ptr() == q.data_ptr():
                 raise ValueError("out: expected q's shape, no repeated rows, and not q itself")
-            for x in (q, *self._buffers):
-                if _overlap(out, x):
-                    raise ValueError("out: overlaps q or a buffer of the cache")
         if lse is not None and (lse.dtype != torch.float32 or lse.device != self.device or
                                 lse.shape != q.shape[:3] or not lse.is_contiguous()):
             raise ValueError("lse: expected a contiguous float32 [S, H, T] tensor on the device")
-        if lse is not None:
-            for x in (q, *self._buffers) if out is None else (q, out, *self._buffers):
-                if _overlap(lse, x):
-                    raise ValueError("lse: overlaps q, out or a buffer of the cache")
+        if out is not None or lse is not None:
+            self._apart(q, out, lse)
 
         if stream is None and _current_device() == self._index:
             return self._attend(q, qs, out, lse, plan, scale, _current_stream(self._index))
