@@ -108,7 +108,9 @@ class SharedPrefixCache:
       prefix_lens         [G]                         int32
       prefix_of           [S]                         int32; outside 0..G-1: no prompt
     Calls only enqueue on the stream (the current one of the cache's device
-    unless given) and must be ordered when they write the same buffers.
+    unless given) and must be ordered when they write the same buffers.  Tensors
+    given to a call on another stream than their own are to be kept until it has
+    run there; what it returns belongs to its stream.
     Scratch is allocated per call from the stream's memory pool, so calls on
     several streams and captured graphs never share it.
     No call has a gradient: a tensor that asks for one is refused where
@@ -370,10 +372,13 @@ class SharedPrefixCache:
         if code:
             _check(code, "hkv_shared_evict")
 
-    def check(self):
-        """(code, detail) of the first error latched on the device (waits)."""
-        code, detail = self.status.tolist()
+    def check(self, stream=None):
+        """(code, detail) of the first error latched on the device by the calls
+        enqueued on the stream (waits for them)."""
+        with self._on(stream):
+            code, detail = self.status.tolist()
         return code, detail
 
-    def clear_error(self):
-        self.status.zero_()
+    def clear_error(self, stream=None):
+        with self._on(stream):
+            self.status.zero_()

@@ -197,3 +197,22 @@ def test_prompts_are_filled_by_a_cache_over_them(dtype, T):
         O.assert_within(lse[i:i + 1, :, :n], e, be, "lse")
     assert torch.equal(c.prefix_k[:, :, :T], kt) and torch.equal(c.prefix_v[:, :, :T], vt)
     check(c, q)
+
+
+@pytest.mark.parametrize("by_handle", [False, True])
+def test_errors_of_calls_on_another_stream(by_handle):
+    """check waits for the stream it is given, as the calls go to it: an append
+    without room, held up by 50 ms of other work."""
+    c, _ = make("bf16", S=2, H=4, Hk=2, cap=20, lens=20)
+    kt = torch.randn(2, 2, 1, 64, device=DEV).bfloat16()
+    side = torch.cuda.Stream()
+    at = side.cuda_stream if by_handle else side
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    c.append(kt, kt, stream=at)
+    code, detail = c.check(stream=at)
+    assert code == 3 and detail in range(4)
+    c.clear_error(stream=at)
+    assert c.check(stream=at) == (0, 0)
+    assert c.check() == (0, 0) and c.check(stream=0) == (0, 0)
