@@ -247,9 +247,10 @@ constexpr int ONE_TILE_ROWS = 512;
 inline int umma_row_tiles(int64_t rows_per_seq) { return rows_per_seq > ONE_TILE_ROWS ? 2 : 1; }
 
 // Two weights p >= 0 as sums of two bf16 each, hi + lo, packed in pairs: off by at
-// most 2^-15 of p.  hi is cut off from a little less than p, so that lo lies in (2^-9
-// p, 2^-7 p 5/4] and both are above zero wherever p is (down to 2^-124): a product with
-// an infinite value is that infinity, where a lo of zero or below gave NaN.
+// most 2^-15 of p (of weights below 2^-119, 2^-134).  hi is cut off from a little less
+// than p, so that lo lies between 2^-9 p (less its rounding) and 2^-7 p 5/4, and both
+// are above zero wherever p is (down to 2^-124): a product with an infinite value is
+// that infinity, where a lo of zero or below gave NaN.
 __device__ __forceinline__ void split_weights(float p0, float p1, uint32_t& hi, uint32_t& lo) {
     constexpr float LESS = 1.f - 0x1p-9f;
     hi = __byte_perm(__float_as_uint(p0 * LESS), __float_as_uint(p1 * LESS), 0x7632);
